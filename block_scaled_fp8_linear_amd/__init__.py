@@ -15,6 +15,11 @@ hand-written HIP) provides:
 * ``fp8_act_quantize(x)`` -> (xq, x_scale)  per-token 1x128 activation quantizer
 * ``fp8_block_linear_w8a8(xq, x_scale, q, s)`` / ``fp8_block_linear_w8a8_bf16(x, q, s)``
   -> bf16 Y from E4M3 x E4M3 products on the FP8 matrix cores (W8A8 route)
+* ``fp8_block_linear_act(x, q, s, bias, residual, act)`` -> bf16
+  act(X W_hat^T + bias) + residual in one pass
+* ``fp8_block_glu(x, qg, sg, qu, su, act)`` -> bf16 act(X Wg^T) * (X Wu^T)
+* ``fp8_block_linear_act_backward`` / ``fp8_block_glu_backward`` -> their
+  gradients through the frozen weight
 * ``fp8_block_stream_read(buf)`` -> a plain streaming read of device memory
   (measurement aid: the practical HBM ceiling)
 
@@ -23,7 +28,8 @@ serialized block-FP8 checkpoint (quantization on the GPU, safetensors shards,
 index and ``quantization_config``).
 
 The functions here only marshal torch tensors (device memory and the current
-stream) into the C ABI declared in include/fp8bl.h; all arithmetic runs in
+stream) into the C ABI declared in include/fp8bl.h and
+include/fp8bl_layers.h; all arithmetic runs in
 the HIP kernels. There is no CPU fallback: without the built library every
 call raises.
 """
@@ -34,8 +40,9 @@ import torch
 
 from . import _lib
 from ._lib import (  # noqa: F401
+    ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU,
     PATH_AUTO, PATH_LARGE, PATH_SKINNY, PATH_TILED, Fp8blError, abi_version, device_supported,
-    status_string, w8a8_workspace_size, workspace_size,
+    layer_workspace_size, status_string, w8a8_workspace_size, workspace_size,
 )
 
 BLOCK = 128
@@ -44,6 +51,8 @@ __all__ = [
     "fp8_block_quantize", "fp8_block_dequant", "fp8_block_linear", "fp8_block_mlp_gate_up",
     "fp8_act_quantize", "fp8_block_linear_w8a8", "fp8_block_linear_w8a8_bf16",
     "fp8_block_linear_noalloc",
+    "fp8_block_linear_act", "fp8_block_linear_act_backward", "fp8_block_glu", "fp8_block_glu_backward",
+    "layer_workspace_size", "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH",
     "workspace_size", "w8a8_workspace_size",
     "device_supported", "abi_version", "status_string", "Fp8blError",
     "PATH_AUTO", "PATH_TILED", "PATH_SKINNY", "PATH_LARGE", "scale_grid_shape", "fp8_block_stream_read",
@@ -311,3 +320,173 @@ def fp8_block_stream_read(buf: torch.Tensor, blocks: int = 2048,
         _check(_lib.stream_read_raw(buf.data_ptr(), nbytes, sink.data_ptr(), blocks,
                                     _stream(buf.device)), "fp8_block_stream_read")
     return sink
+
+
+def _array(t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: torch.device, name: str) -> int:
+    """The device address of an argument, checked; several of a call must
+    share one device."""
+    _need(t, dtype, name)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    return t.data_ptr()
+
+
+def _optional(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, dev: torch.device,
+              name: str) -> int:
+    return 0 if t is None else _array(t, dtype, shape, dev, name)
+
+
+def _weight(q: torch.Tensor, s: torch.Tensor, shape: tuple, dev: torch.device, name: str) -> tuple:
+    return (_array(q, torch.uint8, shape, dev, f"q{name}"),
+            _array(s, torch.float32, scale_grid_shape(*shape), dev, f"s{name}"))
+
+
+def _matrix(t: torch.Tensor, name: str) -> tuple:
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got {list(t.shape)}")
+    return tuple(t.shape)
+
+
+def _layer_workspace(op: str, m: int, n: int, k: int, workspace: torch.Tensor | None,
+                     dev: torch.device) -> tuple:
+    if workspace is None:
+        need = layer_workspace_size(op, m, n, k)
+        if need == 0:
+            return None, 0, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def fp8_block_linear_act(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor,
+                         bias: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                         act: int = ACT_NONE, out: torch.Tensor | None = None,
+                         z: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """bf16 x [M,K], block-FP8 weight -> bf16 y [M,N] = act(x W_hat^T + bias) + residual.
+
+    ``bias`` bf16 [N], ``residual`` bf16 [M,N] (``out`` may be the residual:
+    added in place), ``act`` an ``ACT_*``. ``z``, when given, receives the
+    bf16 pre-activation the backward pass needs. ``workspace``, when given,
+    holds at least ``layer_workspace_size("linear_act", M, N, K)`` bytes."""
+    bf = torch.bfloat16
+    dev = x.device
+    m, k = _matrix(x, "x")
+    n = _matrix(q, "q")[0]
+    px = _array(x, bf, (m, k), dev, "x")
+    pq, ps = _weight(q, s, (n, k), dev, "")
+    pb = _optional(bias, bf, (n,), dev, "bias")
+    pr = _optional(residual, bf, (m, n), dev, "residual")
+    pz = _optional(z, bf, (m, n), dev, "z")
+    if out is None:
+        out = torch.empty((m, n), dtype=bf, device=dev)
+    py = _array(out, bf, (m, n), dev, "out")
+    workspace, ws, ws_bytes = _layer_workspace("linear_act", m, n, k, workspace, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.linear_act_raw(px, pq, ps, pb, pr, pz, py, m, n, k, int(act), ws, ws_bytes,
+                                   _stream(dev)), "fp8_block_linear_act")
+    return out
+
+
+def fp8_block_linear_act_backward(dy: torch.Tensor, q: torch.Tensor, s: torch.Tensor,
+                                  z: torch.Tensor | None = None, act: int = ACT_NONE,
+                                  dx: torch.Tensor | None = None, dz: torch.Tensor | None = None,
+                                  dbias: torch.Tensor | None = None,
+                                  workspace: torch.Tensor | None = None) -> tuple:
+    """Backward pass of ``fp8_block_linear_act``: bf16 dy [M,N] -> (dx, dz) with
+    dz = dy act'(z) bf16 [M,N] and dx = dz W_hat bf16 [M,K].
+
+    ``z`` is the saved pre-activation (None with ``ACT_NONE``, where dz is dy
+    itself). ``dbias``, when given, is an fp32 [N] tensor that receives the sum
+    of dz over rows. The residual's gradient is dy; the weight is a constant."""
+    bf = torch.bfloat16
+    dev = dy.device
+    m, n = _matrix(dy, "dy")
+    k = _matrix(q, "q")[1]
+    pdy = _array(dy, bf, (m, n), dev, "dy")
+    pq, ps = _weight(q, s, (n, k), dev, "")
+    if act == ACT_NONE:
+        if z is not None or dz is not None:
+            raise ValueError("without an activation there is no z, and dz is dy")
+        dz, pz, pdz = dy, 0, 0
+    else:
+        if z is None:
+            raise ValueError("z is needed for the activation's derivative")
+        pz = _array(z, bf, (m, n), dev, "z")
+        if dz is None:
+            dz = torch.empty((m, n), dtype=bf, device=dev)
+        pdz = _array(dz, bf, (m, n), dev, "dz")
+    pdb = _optional(dbias, torch.float32, (n,), dev, "dbias")
+    if dx is None:
+        dx = torch.empty((m, k), dtype=bf, device=dev)
+    pdx = _array(dx, bf, (m, k), dev, "dx")
+    workspace, ws, ws_bytes = _layer_workspace("linear_act_backward", m, n, k, workspace, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.linear_act_backward_raw(pdy, pz, pq, ps, pdz, pdb, pdx, m, n, k, int(act), ws,
+                                            ws_bytes, _stream(dev)), "fp8_block_linear_act_backward")
+    return dx, dz
+
+
+def fp8_block_glu(x: torch.Tensor, q_gate: torch.Tensor, s_gate: torch.Tensor, q_up: torch.Tensor,
+                  s_up: torch.Tensor, act: int = ACT_SILU, out: torch.Tensor | None = None,
+                  g: torch.Tensor | None = None, u: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """bf16 x [M,K] and two block-FP8 weights [N,K] -> bf16 h [M,N] =
+    act(x Wg^T) * (x Wu^T), rounded once (``fp8_block_mlp_gate_up`` rounds on
+    the way). ``g`` and ``u``, given together, receive the two bf16 products,
+    which the backward pass needs."""
+    bf = torch.bfloat16
+    dev = x.device
+    m, k = _matrix(x, "x")
+    n = _matrix(q_gate, "q_gate")[0]
+    px = _array(x, bf, (m, k), dev, "x")
+    pqg, psg = _weight(q_gate, s_gate, (n, k), dev, "_gate")
+    pqu, psu = _weight(q_up, s_up, (n, k), dev, "_up")
+    if (g is None) != (u is None):
+        raise ValueError("g and u are saved together")
+    pg = _optional(g, bf, (m, n), dev, "g")
+    pu = _optional(u, bf, (m, n), dev, "u")
+    if out is None:
+        out = torch.empty((m, n), dtype=bf, device=dev)
+    ph = _array(out, bf, (m, n), dev, "out")
+    workspace, ws, ws_bytes = _layer_workspace("glu", m, n, k, workspace, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.glu_raw(px, pqg, psg, pqu, psu, pg, pu, ph, m, n, k, int(act), ws, ws_bytes,
+                            _stream(dev)), "fp8_block_glu")
+    return out
+
+
+def fp8_block_glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, q_gate: torch.Tensor,
+                           s_gate: torch.Tensor, q_up: torch.Tensor, s_up: torch.Tensor,
+                           act: int = ACT_SILU, dx: torch.Tensor | None = None,
+                           dg: torch.Tensor | None = None, du: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None) -> tuple:
+    """Backward pass of ``fp8_block_glu``: bf16 dh [M,N] and the saved g, u ->
+    (dx, dg, du) with dg = dh u act'(g), du = dh act(g) and
+    dx = dg Wg_hat + du Wu_hat."""
+    bf = torch.bfloat16
+    dev = dh.device
+    m, n = _matrix(dh, "dh")
+    k = _matrix(q_gate, "q_gate")[1]
+    pdh = _array(dh, bf, (m, n), dev, "dh")
+    pg = _array(g, bf, (m, n), dev, "g")
+    pu = _array(u, bf, (m, n), dev, "u")
+    pqg, psg = _weight(q_gate, s_gate, (n, k), dev, "_gate")
+    pqu, psu = _weight(q_up, s_up, (n, k), dev, "_up")
+    if dg is None:
+        dg = torch.empty((m, n), dtype=bf, device=dev)
+    if du is None:
+        du = torch.empty((m, n), dtype=bf, device=dev)
+    if dx is None:
+        dx = torch.empty((m, k), dtype=bf, device=dev)
+    pdg = _array(dg, bf, (m, n), dev, "dg")
+    pdu = _array(du, bf, (m, n), dev, "du")
+    pdx = _array(dx, bf, (m, k), dev, "dx")
+    workspace, ws, ws_bytes = _layer_workspace("glu_backward", m, n, k, workspace, dev)
+    with torch.cuda.device(dev):
+        _check(_lib.glu_backward_raw(pdh, pg, pu, pqg, psg, pqu, psu, pdg, pdu, pdx, m, n, k, int(act),
+                                     ws, ws_bytes, _stream(dev)), "fp8_block_glu_backward")
+    return dx, dg, du

@@ -14,6 +14,7 @@ import re
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG_DIR, "libfp8bl.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG_DIR), "include", "fp8bl.h")
+LAYERS_HEADER_PATH = os.path.join(os.path.dirname(_PKG_DIR), "include", "fp8bl_layers.h")
 
 FP8BL_OK = 0
 FP8BL_INVALID_ARG = 1
@@ -26,6 +27,12 @@ PATH_AUTO = 0
 PATH_TILED = 1
 PATH_SKINNY = 2
 PATH_LARGE = 3
+
+ACT_NONE = 0
+ACT_RELU = 1
+ACT_SILU = 2
+ACT_GELU = 3
+ACT_GELU_TANH = 4
 
 _lib = None
 
@@ -82,13 +89,22 @@ def load() -> ctypes.CDLL:
     lib.fp8_block_quantize_bf16.argtypes = [vp, vp, vp, i64, i64, vp]
     lib.fp8_block_stream_read.restype = c_int
     lib.fp8_block_stream_read.argtypes = [vp, sz, vp, c_int, vp]
+    for op in ("linear_act", "linear_act_backward", "glu", "glu_backward"):
+        size = getattr(lib, f"fp8_block_{op}_workspace_size")
+        size.restype = sz
+        size.argtypes = [i64, i64, i64]
+    tail = [i64, i64, i64, c_int, vp, sz, vp]   # m, n, k, act, workspace, its bytes, stream
+    for op, pointers in (("linear_act", 7), ("linear_act_backward", 7), ("glu", 8), ("glu_backward", 10)):
+        call = getattr(lib, f"fp8_block_{op}")
+        call.restype = c_int
+        call.argtypes = [vp] * pointers + tail
     _lib = lib
     return lib
 
 
-def header_functions() -> list[str]:
-    """Names of the functions include/fp8bl.h declares."""
-    text = open(HEADER_PATH).read()
+def header_functions(path: str | None = None) -> list[str]:
+    """Names of the functions a header declares (include/fp8bl.h by default)."""
+    text = open(path or HEADER_PATH).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return re.findall(r"^\s*(?:const\s+)?\w+\*?\s+\*?(fp8_\w+)\s*\(", text, flags=re.M)
 
@@ -172,3 +188,35 @@ def quantize_bf16_raw(w: int, q: int, s: int, n: int, k: int, stream: int = 0) -
 
 def stream_read_raw(buf: int, nbytes: int, sink: int, blocks: int, stream: int = 0) -> int:
     return load().fp8_block_stream_read(buf, nbytes, sink, blocks, stream)
+
+
+# Layer operators (include/fp8bl_layers.h).
+
+def layer_workspace_size(op: str, m: int, n: int, k: int) -> int:
+    """Workspace bytes of fp8_block_<op>: linear_act, linear_act_backward, glu
+    or glu_backward."""
+    return int(getattr(load(), f"fp8_block_{op}_workspace_size")(m, n, k))
+
+
+def linear_act_raw(x: int, q: int, s: int, bias: int, residual: int, z: int, y: int, m: int, n: int,
+                   k: int, act: int, ws: int, ws_bytes: int, stream: int = 0) -> int:
+    return load().fp8_block_linear_act(x, q, s, bias, residual, z, y, m, n, k, act, ws, ws_bytes,
+                                       stream)
+
+
+def linear_act_backward_raw(dy: int, z: int, q: int, s: int, dz: int, dbias: int, dx: int, m: int,
+                            n: int, k: int, act: int, ws: int, ws_bytes: int, stream: int = 0) -> int:
+    return load().fp8_block_linear_act_backward(dy, z, q, s, dz, dbias, dx, m, n, k, act, ws,
+                                                ws_bytes, stream)
+
+
+def glu_raw(x: int, qg: int, sg: int, qu: int, su: int, g: int, u: int, h: int, m: int, n: int, k: int,
+            act: int, ws: int, ws_bytes: int, stream: int = 0) -> int:
+    return load().fp8_block_glu(x, qg, sg, qu, su, g, u, h, m, n, k, act, ws, ws_bytes, stream)
+
+
+def glu_backward_raw(dh: int, g: int, u: int, qg: int, sg: int, qu: int, su: int, dg: int, du: int,
+                     dx: int, m: int, n: int, k: int, act: int, ws: int, ws_bytes: int,
+                     stream: int = 0) -> int:
+    return load().fp8_block_glu_backward(dh, g, u, qg, sg, qu, su, dg, du, dx, m, n, k, act, ws,
+                                         ws_bytes, stream)

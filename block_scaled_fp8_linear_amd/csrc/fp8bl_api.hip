@@ -9,15 +9,14 @@
 #include <cstring>
 #include <mutex>
 
+#include "fp8bl_checks.h"
 #include "fp8bl_internal.h"
-
-#define FP8BL_EXPORT extern "C" __attribute__((visibility("default")))
 
 namespace {
 
-constexpr int kMaxDevices = 64;
-constexpr int64_t kMaxDim = (int64_t)1 << 31;     // every dimension fits int32
-constexpr int64_t kMaxElems = (int64_t)1 << 35;   // N*K, M*K and M*N stay below this (8-element chunk index fits uint32)
+using namespace fp8bl::checks;
+using fp8bl::gate_current_device;
+
 constexpr int kSkinnyMaxM = 32;
 // The GEMM kernels address a tile's rows with 32-bit buffer offsets.
 constexpr int64_t kMaxLinearK = (int64_t)1 << 20;
@@ -28,26 +27,10 @@ constexpr int64_t kLargeMaxN = (int64_t)1 << 21;
 // 0 = unknown, 1 = gfx950, 2 = other.
 std::atomic<int> g_arch[kMaxDevices];
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + nb && b0 < a0 + na;
-}
-
-size_t grid_elems(int64_t n, int64_t k) {
-  return (size_t)((n + FP8BL_BLOCK - 1) / FP8BL_BLOCK) * (size_t)((k + FP8BL_BLOCK - 1) / FP8BL_BLOCK);
-}
-
-int check_nk(int64_t n, int64_t k) {
-  if (n < 0 || k <= 0 || (k % 16) != 0) return FP8BL_INVALID_ARG;
-  if (n >= kMaxDim || k >= kMaxDim || (n > 0 && n * k >= kMaxElems)) return FP8BL_INVALID_ARG;
-  if ((n + FP8BL_BLOCK - 1) / FP8BL_BLOCK > 65535) return FP8BL_INVALID_ARG;
-  return FP8BL_OK;
-}
+}  // namespace
 
 // The current device must be a gfx950; the answer is cached per device.
-int gate_current_device() {
+int fp8bl::gate_current_device() {
   int dev = -1;
   if (hipGetDevice(&dev) != hipSuccess) return FP8BL_HIP_ERROR;
   if (dev < 0 || dev >= kMaxDevices) return FP8BL_UNSUPPORTED_DEVICE;
@@ -61,7 +44,7 @@ int gate_current_device() {
   return state == 1 ? FP8BL_OK : FP8BL_UNSUPPORTED_DEVICE;
 }
 
-int hip_status(hipError_t e) { return e == hipSuccess ? FP8BL_OK : FP8BL_HIP_ERROR; }
+namespace {
 
 int validate_linear(const uint16_t* x, const uint8_t* q, const float* s, const uint16_t* y,
                     int64_t m, int64_t n, int64_t k, int path) {

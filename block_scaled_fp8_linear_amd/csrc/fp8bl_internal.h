@@ -87,6 +87,46 @@ hipError_t launch_reduce_partials(const float* part, uint16_t* y, int splits,
 hipError_t launch_stream_read(const void* buf, size_t bytes, uint32_t* sink, int blocks,
                               hipStream_t stream);
 
+// ---- Layer operators (fp8bl_layers.h).
+// What an epilogue reads and writes besides its main output; unused pointers
+// are null. `act` is an enum fp8bl_act value.
+struct LayerEpilogue {
+  const uint16_t* bias;       // [N]
+  const uint16_t* residual;   // [M,N], may be the output itself
+  uint16_t* z;                // [M,N], the pre-activation
+  uint16_t* g;                // [M,N], the gated pair's products
+  uint16_t* u;
+  int act;
+};
+size_t linear_act_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t launch_linear_act(const uint16_t* x, const uint8_t* q, const float* s, uint16_t* y,
+                             const LayerEpilogue& ep, int64_t m, int64_t n, int64_t k, void* ws,
+                             size_t ws_bytes, hipStream_t stream);
+size_t glu_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t launch_glu(const uint16_t* x, const uint8_t* qg, const float* sg, const uint8_t* qu,
+                      const float* su, uint16_t* h, const LayerEpilogue& ep, int64_t m, int64_t n,
+                      int64_t k, void* ws, size_t ws_bytes, hipStream_t stream);
+// dx[M,K] = a W^ (+ a2 W2^), reduction over n. a and a2 have rows of `lda`
+// elements (a multiple of 8), zero from n on.
+size_t input_gradient_bytes(int64_t m, int64_t n, int64_t k, int products);
+hipError_t launch_input_gradient(const uint16_t* a, const uint8_t* q, const float* s, const uint16_t* a2,
+                                 const uint8_t* q2, const float* s2, int64_t lda, uint16_t* dx,
+                                 int64_t m, int64_t n, int64_t k, void* ws, size_t ws_bytes,
+                                 hipStream_t stream);
+// Elementwise gradients. `pad`: a copy with rows of ld elements for the
+// product above (null where n % 8 == 0 and the gradient itself serves).
+size_t column_sum_bytes(int64_t m, int64_t n);
+hipError_t launch_act_backward(const uint16_t* dy, const uint16_t* z, uint16_t* dz, uint16_t* pad,
+                               int64_t ld, float* dbias, float* part, int64_t m, int64_t n, int act,
+                               hipStream_t stream);
+hipError_t launch_glu_backward(const uint16_t* dh, const uint16_t* g, const uint16_t* u, uint16_t* dg,
+                               uint16_t* du, uint16_t* pad_g, uint16_t* pad_u, int64_t ld, int64_t m,
+                               int64_t n, int act, hipStream_t stream);
+hipError_t launch_fill_zero(void* p, size_t bytes, hipStream_t stream);
+
+// Checks shared by the two ABI files.
+int gate_current_device();
+
 constexpr size_t kWorkspaceAlign = 256;
 inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 // Split-K partial slabs ([M,N] fp32 each) start every 64 floats, so every
