@@ -33,6 +33,9 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
   return __builtin_bit_cast(uint32_t, v);
 }
 
+__device__ __forceinline__ float bf16_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+__device__ __forceinline__ uint16_t f32_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+
 // Four E4M3 codes (byte i of `codes` is element i) -> two packed bf16 pairs,
 // each element scaled by `s` in fp32 first.
 __device__ __forceinline__ u32x2 dequant4(uint32_t codes, float s) {

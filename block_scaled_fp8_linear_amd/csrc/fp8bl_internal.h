@@ -53,6 +53,11 @@ struct LargePlan {
   double cost;      // planner's time estimate, the units of tiled_cost
 };
 LargePlan plan_large(int64_t m, int64_t n, int64_t k);
+int device_cus();           // compute units of the current device
+// Its split-K partials alone (the caller joins them).
+hipError_t launch_gemm_large_partials(const LargePlan& p, const uint16_t* x, const uint8_t* q,
+                                      const float* s, float* part, int64_t m, int64_t n, int64_t k,
+                                      hipStream_t stream);
 size_t large_workspace_bytes(int64_t m, int64_t n, int64_t k);
 hipError_t launch_gemm_large(const uint16_t* x, const uint8_t* q, const float* s,
                              uint16_t* y, int64_t m, int64_t n, int64_t k,
