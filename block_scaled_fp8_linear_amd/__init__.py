@@ -322,43 +322,57 @@ def fp8_block_stream_read(buf: torch.Tensor, blocks: int = 2048,
     return sink
 
 
-def _array(t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: torch.device, name: str) -> int:
-    """The device address of an argument, checked; several of a call must
-    share one device."""
+def _device_index(t: torch.Tensor, name: str) -> int:
+    idx = t.get_device()
+    if idx < 0:
+        raise TypeError(f"{name} must be a device tensor")
+    return idx
+
+
+def _array(t: torch.Tensor, dtype: torch.dtype, shape: tuple, idx: int, name: str) -> int:
+    """The address of one array of a call, checked; all of a call's arrays are
+    on one device."""
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == idx and t.is_contiguous()):
+        return t.data_ptr()
     _need(t, dtype, name)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{idx}")
 
 
-def _optional(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, dev: torch.device,
-              name: str) -> int:
-    return 0 if t is None else _array(t, dtype, shape, dev, name)
-
-
-def _weight(q: torch.Tensor, s: torch.Tensor, shape: tuple, dev: torch.device, name: str) -> tuple:
-    return (_array(q, torch.uint8, shape, dev, f"q{name}"),
-            _array(s, torch.float32, scale_grid_shape(*shape), dev, f"s{name}"))
+def _optional(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, idx: int, name: str) -> int:
+    return 0 if t is None else _array(t, dtype, shape, idx, name)
 
 
 def _matrix(t: torch.Tensor, name: str) -> tuple:
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix, got {list(t.shape)}")
-    return tuple(t.shape)
+    return t.shape
 
 
-def _layer_workspace(op: str, m: int, n: int, k: int, workspace: torch.Tensor | None,
-                     dev: torch.device) -> tuple:
+def _layer_call(op: str, pointers: tuple, m: int, n: int, k: int, act: int,
+                workspace: torch.Tensor | None, idx: int) -> None:
+    """Workspace, stream and the call itself, on the arrays' device."""
+    size, call = _lib.layer_calls(op)
+    if torch.cuda.current_device() != idx:
+        with torch.cuda.device(idx):
+            return _layer_call(op, pointers, m, n, k, act, workspace, idx)
+    ws = ws_bytes = 0
     if workspace is None:
-        need = layer_workspace_size(op, m, n, k)
-        if need == 0:
-            return None, 0, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws_bytes = size(m, n, k)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device="cuda")
+            ws = workspace.data_ptr()
+    elif workspace.get_device() != idx or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{idx}")
+    else:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    status = call(*pointers, m, n, k, int(act), ws, ws_bytes, torch.cuda.current_stream().cuda_stream)
+    if status != _lib.FP8BL_OK:
+        raise Fp8blError(status, f"fp8_block_{op}")
+
+
+_BF16 = torch.bfloat16
 
 
 def fp8_block_linear_act(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor,
@@ -372,22 +386,20 @@ def fp8_block_linear_act(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor,
     added in place), ``act`` an ``ACT_*``. ``z``, when given, receives the
     bf16 pre-activation the backward pass needs. ``workspace``, when given,
     holds at least ``layer_workspace_size("linear_act", M, N, K)`` bytes."""
-    bf = torch.bfloat16
-    dev = x.device
+    idx = _device_index(x, "x")
     m, k = _matrix(x, "x")
     n = _matrix(q, "q")[0]
-    px = _array(x, bf, (m, k), dev, "x")
-    pq, ps = _weight(q, s, (n, k), dev, "")
-    pb = _optional(bias, bf, (n,), dev, "bias")
-    pr = _optional(residual, bf, (m, n), dev, "residual")
-    pz = _optional(z, bf, (m, n), dev, "z")
+    mn = (m, n)
     if out is None:
-        out = torch.empty((m, n), dtype=bf, device=dev)
-    py = _array(out, bf, (m, n), dev, "out")
-    workspace, ws, ws_bytes = _layer_workspace("linear_act", m, n, k, workspace, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.linear_act_raw(px, pq, ps, pb, pr, pz, py, m, n, k, int(act), ws, ws_bytes,
-                                   _stream(dev)), "fp8_block_linear_act")
+        out = x.new_empty(mn)
+    pointers = (_array(x, _BF16, (m, k), idx, "x"),
+                _array(q, torch.uint8, (n, k), idx, "q"),
+                _array(s, torch.float32, scale_grid_shape(n, k), idx, "s"),
+                _optional(bias, _BF16, (n,), idx, "bias"),
+                _optional(residual, _BF16, mn, idx, "residual"),
+                _optional(z, _BF16, mn, idx, "z"),
+                _array(out, _BF16, mn, idx, "out"))
+    _layer_call("linear_act", pointers, m, n, k, act, workspace, idx)
     return out
 
 
@@ -402,32 +414,27 @@ def fp8_block_linear_act_backward(dy: torch.Tensor, q: torch.Tensor, s: torch.Te
     ``z`` is the saved pre-activation (None with ``ACT_NONE``, where dz is dy
     itself). ``dbias``, when given, is an fp32 [N] tensor that receives the sum
     of dz over rows. The residual's gradient is dy; the weight is a constant."""
-    bf = torch.bfloat16
-    dev = dy.device
-    m, n = _matrix(dy, "dy")
+    idx = _device_index(dy, "dy")
+    m, n = mn = _matrix(dy, "dy")
     k = _matrix(q, "q")[1]
-    pdy = _array(dy, bf, (m, n), dev, "dy")
-    pq, ps = _weight(q, s, (n, k), dev, "")
     if act == ACT_NONE:
         if z is not None or dz is not None:
             raise ValueError("without an activation there is no z, and dz is dy")
-        dz, pz, pdz = dy, 0, 0
-    else:
-        if z is None:
-            raise ValueError("z is needed for the activation's derivative")
-        pz = _array(z, bf, (m, n), dev, "z")
-        if dz is None:
-            dz = torch.empty((m, n), dtype=bf, device=dev)
-        pdz = _array(dz, bf, (m, n), dev, "dz")
-    pdb = _optional(dbias, torch.float32, (n,), dev, "dbias")
+    elif z is None:
+        raise ValueError("z is needed for the activation's derivative")
+    elif dz is None:
+        dz = dy.new_empty(mn)
     if dx is None:
-        dx = torch.empty((m, k), dtype=bf, device=dev)
-    pdx = _array(dx, bf, (m, k), dev, "dx")
-    workspace, ws, ws_bytes = _layer_workspace("linear_act_backward", m, n, k, workspace, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.linear_act_backward_raw(pdy, pz, pq, ps, pdz, pdb, pdx, m, n, k, int(act), ws,
-                                            ws_bytes, _stream(dev)), "fp8_block_linear_act_backward")
-    return dx, dz
+        dx = dy.new_empty((m, k))
+    pointers = (_array(dy, _BF16, mn, idx, "dy"),
+                _optional(z, _BF16, mn, idx, "z"),
+                _array(q, torch.uint8, (n, k), idx, "q"),
+                _array(s, torch.float32, scale_grid_shape(n, k), idx, "s"),
+                _optional(dz, _BF16, mn, idx, "dz"),
+                _optional(dbias, torch.float32, (n,), idx, "dbias"),
+                _array(dx, _BF16, (m, k), idx, "dx"))
+    _layer_call("linear_act_backward", pointers, m, n, k, act, workspace, idx)
+    return dx, (dy if act == ACT_NONE else dz)
 
 
 def fp8_block_glu(x: torch.Tensor, q_gate: torch.Tensor, s_gate: torch.Tensor, q_up: torch.Tensor,
@@ -438,24 +445,23 @@ def fp8_block_glu(x: torch.Tensor, q_gate: torch.Tensor, s_gate: torch.Tensor, q
     act(x Wg^T) * (x Wu^T), rounded once (``fp8_block_mlp_gate_up`` rounds on
     the way). ``g`` and ``u``, given together, receive the two bf16 products,
     which the backward pass needs."""
-    bf = torch.bfloat16
-    dev = x.device
+    idx = _device_index(x, "x")
     m, k = _matrix(x, "x")
     n = _matrix(q_gate, "q_gate")[0]
-    px = _array(x, bf, (m, k), dev, "x")
-    pqg, psg = _weight(q_gate, s_gate, (n, k), dev, "_gate")
-    pqu, psu = _weight(q_up, s_up, (n, k), dev, "_up")
+    mn, grid = (m, n), scale_grid_shape(n, k)
     if (g is None) != (u is None):
         raise ValueError("g and u are saved together")
-    pg = _optional(g, bf, (m, n), dev, "g")
-    pu = _optional(u, bf, (m, n), dev, "u")
     if out is None:
-        out = torch.empty((m, n), dtype=bf, device=dev)
-    ph = _array(out, bf, (m, n), dev, "out")
-    workspace, ws, ws_bytes = _layer_workspace("glu", m, n, k, workspace, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.glu_raw(px, pqg, psg, pqu, psu, pg, pu, ph, m, n, k, int(act), ws, ws_bytes,
-                            _stream(dev)), "fp8_block_glu")
+        out = x.new_empty(mn)
+    pointers = (_array(x, _BF16, (m, k), idx, "x"),
+                _array(q_gate, torch.uint8, (n, k), idx, "q_gate"),
+                _array(s_gate, torch.float32, grid, idx, "s_gate"),
+                _array(q_up, torch.uint8, (n, k), idx, "q_up"),
+                _array(s_up, torch.float32, grid, idx, "s_up"),
+                _optional(g, _BF16, mn, idx, "g"),
+                _optional(u, _BF16, mn, idx, "u"),
+                _array(out, _BF16, mn, idx, "out"))
+    _layer_call("glu", pointers, m, n, k, act, workspace, idx)
     return out
 
 
@@ -467,26 +473,25 @@ def fp8_block_glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, q
     """Backward pass of ``fp8_block_glu``: bf16 dh [M,N] and the saved g, u ->
     (dx, dg, du) with dg = dh u act'(g), du = dh act(g) and
     dx = dg Wg_hat + du Wu_hat."""
-    bf = torch.bfloat16
-    dev = dh.device
-    m, n = _matrix(dh, "dh")
+    idx = _device_index(dh, "dh")
+    m, n = mn = _matrix(dh, "dh")
     k = _matrix(q_gate, "q_gate")[1]
-    pdh = _array(dh, bf, (m, n), dev, "dh")
-    pg = _array(g, bf, (m, n), dev, "g")
-    pu = _array(u, bf, (m, n), dev, "u")
-    pqg, psg = _weight(q_gate, s_gate, (n, k), dev, "_gate")
-    pqu, psu = _weight(q_up, s_up, (n, k), dev, "_up")
+    grid = scale_grid_shape(n, k)
     if dg is None:
-        dg = torch.empty((m, n), dtype=bf, device=dev)
+        dg = dh.new_empty(mn)
     if du is None:
-        du = torch.empty((m, n), dtype=bf, device=dev)
+        du = dh.new_empty(mn)
     if dx is None:
-        dx = torch.empty((m, k), dtype=bf, device=dev)
-    pdg = _array(dg, bf, (m, n), dev, "dg")
-    pdu = _array(du, bf, (m, n), dev, "du")
-    pdx = _array(dx, bf, (m, k), dev, "dx")
-    workspace, ws, ws_bytes = _layer_workspace("glu_backward", m, n, k, workspace, dev)
-    with torch.cuda.device(dev):
-        _check(_lib.glu_backward_raw(pdh, pg, pu, pqg, psg, pqu, psu, pdg, pdu, pdx, m, n, k, int(act),
-                                     ws, ws_bytes, _stream(dev)), "fp8_block_glu_backward")
+        dx = dh.new_empty((m, k))
+    pointers = (_array(dh, _BF16, mn, idx, "dh"),
+                _array(g, _BF16, mn, idx, "g"),
+                _array(u, _BF16, mn, idx, "u"),
+                _array(q_gate, torch.uint8, (n, k), idx, "q_gate"),
+                _array(s_gate, torch.float32, grid, idx, "s_gate"),
+                _array(q_up, torch.uint8, (n, k), idx, "q_up"),
+                _array(s_up, torch.float32, grid, idx, "s_up"),
+                _array(dg, _BF16, mn, idx, "dg"),
+                _array(du, _BF16, mn, idx, "du"),
+                _array(dx, _BF16, (m, k), idx, "dx"))
+    _layer_call("glu_backward", pointers, m, n, k, act, workspace, idx)
     return dx, dg, du

@@ -192,10 +192,23 @@ def stream_read_raw(buf: int, nbytes: int, sink: int, blocks: int, stream: int =
 
 # Layer operators (include/fp8bl_layers.h).
 
+_layer_calls: dict = {}
+
+
+def layer_calls(op: str) -> tuple:
+    """The workspace query and the call of fp8_block_<op>."""
+    got = _layer_calls.get(op)
+    if got is None:
+        lib = load()
+        got = _layer_calls[op] = (getattr(lib, f"fp8_block_{op}_workspace_size"),
+                                  getattr(lib, f"fp8_block_{op}"))
+    return got
+
+
 def layer_workspace_size(op: str, m: int, n: int, k: int) -> int:
     """Workspace bytes of fp8_block_<op>: linear_act, linear_act_backward, glu
     or glu_backward."""
-    return int(getattr(load(), f"fp8_block_{op}_workspace_size")(m, n, k))
+    return int(layer_calls(op)[0](int(m), int(n), int(k)))
 
 
 def linear_act_raw(x: int, q: int, s: int, bias: int, residual: int, z: int, y: int, m: int, n: int,

@@ -52,6 +52,18 @@ __device__ __forceinline__ float act_grad_f32(float t) {
   return 1.0f;
 }
 
+// The activation chosen at run time (a wave-uniform value), for epilogues
+// that finish a few outputs a lane.
+__device__ __forceinline__ float act_any(int act, float t) {
+  switch (act) {
+    case kActRelu: return act_f32<kActRelu>(t);
+    case kActSilu: return act_f32<kActSilu>(t);
+    case kActGelu: return act_f32<kActGelu>(t);
+    case kActGeluTanh: return act_f32<kActGeluTanh>(t);
+    default: return t;
+  }
+}
+
 // One call site per activation: `f` is a generic lambda called with the
 // activation as a compile-time constant.
 template <int A>

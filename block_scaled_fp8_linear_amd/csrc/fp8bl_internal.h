@@ -77,6 +77,10 @@ hipError_t launch_mlp_gate_up(const uint16_t* x, const uint8_t* qg, const float*
                               int64_t m, int64_t n, int64_t k, hipStream_t stream);
 
 // Skinny-M (M <= 32 rows per pass) weight-streaming GEMM.
+struct SkinnyPlan {
+  int mt, nt, splits, ss_per_split;
+};
+SkinnyPlan plan_skinny(int64_t m, int64_t n, int64_t k);
 size_t skinny_workspace_bytes(int64_t m, int64_t n, int64_t k);
 hipError_t launch_gemm_skinny(const uint16_t* x, const uint8_t* q, const float* s,
                               uint16_t* y, int64_t m, int64_t n, int64_t k,
@@ -118,6 +122,26 @@ hipError_t launch_input_gradient(const uint16_t* a, const uint8_t* q, const floa
                                  const uint8_t* q2, const float* s2, int64_t lda, uint16_t* dx,
                                  int64_t m, int64_t n, int64_t k, void* ws, size_t ws_bytes,
                                  hipStream_t stream);
+// The three at few rows (m <= 32), and joins of split partials (slab stride
+// partial_slab(m, n)) with an epilogue; the pair's partials alternate gate and
+// up slabs.
+size_t linear_act_skinny_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t launch_linear_act_skinny(const uint16_t* x, const uint8_t* q, const float* s, uint16_t* y,
+                                    const LayerEpilogue& ep, int64_t m, int64_t n, int64_t k, void* ws,
+                                    size_t ws_bytes, hipStream_t stream);
+size_t glu_skinny_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t launch_glu_skinny(const uint16_t* x, const uint8_t* qg, const float* sg, const uint8_t* qu,
+                             const float* su, uint16_t* h, const LayerEpilogue& ep, int64_t m, int64_t n,
+                             int64_t k, void* ws, size_t ws_bytes, hipStream_t stream);
+size_t input_gradient_skinny_bytes(int64_t m, int64_t n, int64_t k, int products);
+hipError_t launch_input_gradient_skinny(const uint16_t* a, const uint8_t* q, const float* s,
+                                        const uint16_t* a2, const uint8_t* q2, const float* s2, int64_t lda,
+                                        uint16_t* dx, int64_t m, int64_t n, int64_t k, void* ws,
+                                        size_t ws_bytes, hipStream_t stream);
+hipError_t launch_join_layer(const float* part, uint16_t* y, int splits, int64_t m, int64_t n,
+                             const LayerEpilogue& ep, hipStream_t stream);
+hipError_t launch_join_glu(const float* part, uint16_t* h, int splits, int64_t m, int64_t n,
+                           const LayerEpilogue& ep, hipStream_t stream);
 // Elementwise gradients. `pad`: a copy with rows of ld elements for the
 // product above (null where n % 8 == 0 and the gradient itself serves).
 size_t column_sum_bytes(int64_t m, int64_t n);
