@@ -200,19 +200,47 @@ GradientPlan plan_gradient_skinny(int64_t n, int64_t k, int products) {
   return p;
 }
 
+// K splits of the two forward forms, by the workgroups (32 weight rows each)
+// and a wave's super-steps. A split costs its join, about 3 us, so it has to
+// save iterations: 16 x 5120 x 5120 (160 workgroups, 5 super-steps a wave)
+// runs 12.2 us unsplit and 14.2 in two, 1 x 2048 x 2048 5.0 and 5.9; but
+// 1 x 1024 x 8192 (32 workgroups, 8 super-steps) 10.8 unsplit and 7.1 in four,
+// and 16 x 5120 x 25600 (25 super-steps, 160 workgroups on 256 CUs) 42.7
+// unsplit and 37.9 in four.
+struct LayerPlan {
+  int splits, ss_per_split;
+};
+LayerPlan plan_layer(int64_t groups, int64_t k) {
+  const int nss = (int)((k + kSuper - 1) / kSuper);
+  const int iters = (nss + kWaves - 1) / kWaves;
+  int splits = 1;
+  if (groups < 128 && iters >= 4) {
+    while (groups * splits < 128 && splits * 2 <= iters) splits *= 2;
+  } else if (groups < 256 && iters >= 16) {
+    splits = 4;
+  }
+  LayerPlan p;
+  p.ss_per_split = (nss + splits - 1) / splits;
+  p.splits = (nss + p.ss_per_split - 1) / p.ss_per_split;
+  return p;
+}
+
 }  // namespace
 
-size_t linear_act_skinny_bytes(int64_t m, int64_t n, int64_t k) { return skinny_workspace_bytes(m, n, k); }
+size_t linear_act_skinny_bytes(int64_t m, int64_t n, int64_t k) {
+  const int splits = plan_layer((n + 31) / 32, k).splits;
+  return splits <= 1 ? 0 : round_up((size_t)splits * partial_slab(m, n) * sizeof(float), kWorkspaceAlign);
+}
 
 hipError_t launch_linear_act_skinny(const uint16_t* x, const uint8_t* q, const float* s, uint16_t* y,
                                     const LayerEpilogue& ep, int64_t m, int64_t n, int64_t k, void* ws,
                                     size_t ws_bytes, hipStream_t stream) {
-  const SkinnyPlan p = plan_skinny(m, n, k);
+  const LayerPlan p = plan_layer((n + 31) / 32, k);
   if (p.splits > 1 && (ws == nullptr || ws_bytes < linear_act_skinny_bytes(m, n, k))) return hipErrorInvalidValue;
   float* const part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
   const dim3 grid((uint32_t)((n + 31) / 32), (uint32_t)p.splits), block(kWaves * 64);
   const int gk = (int)((k + kBlock - 1) / kBlock);
-  if (p.mt == 1)
+  if (m <= 16)
     hipLaunchKernelGGL((linear_act_skinny_kernel<1>), grid, block, 0, stream, x, q, s, y, part, (int)m, (int)n,
                        (int)k, gk, p.ss_per_split, ep);
   else
@@ -223,23 +251,20 @@ hipError_t launch_linear_act_skinny(const uint16_t* x, const uint8_t* q, const f
   return launch_join_layer(part, y, p.splits, m, n, ep, stream);
 }
 
-// The pair's plan: two weights of n rows stream through 16-column workgroups,
-// as many as the linear's over 2 n rows.
 size_t glu_skinny_bytes(int64_t m, int64_t n, int64_t k) {
-  const SkinnyPlan p = plan_skinny(m, 2 * n, k);
-  if (p.splits <= 1) return 0;
-  return round_up((size_t)(2 * p.splits) * partial_slab(m, n) * sizeof(float), kWorkspaceAlign);
+  const int splits = plan_layer((n + 15) / 16, k).splits;
+  return splits <= 1 ? 0 : round_up((size_t)(2 * splits) * partial_slab(m, n) * sizeof(float), kWorkspaceAlign);
 }
 
 hipError_t launch_glu_skinny(const uint16_t* x, const uint8_t* qg, const float* sg, const uint8_t* qu,
                              const float* su, uint16_t* h, const LayerEpilogue& ep, int64_t m, int64_t n,
                              int64_t k, void* ws, size_t ws_bytes, hipStream_t stream) {
-  const SkinnyPlan p = plan_skinny(m, 2 * n, k);
+  const LayerPlan p = plan_layer((n + 15) / 16, k);
   if (p.splits > 1 && (ws == nullptr || ws_bytes < glu_skinny_bytes(m, n, k))) return hipErrorInvalidValue;
   float* const part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
   const dim3 grid((uint32_t)((n + 15) / 16), (uint32_t)p.splits), block(kWaves * 64);
   const int gk = (int)((k + kBlock - 1) / kBlock);
-  if (p.mt == 1)
+  if (m <= 16)
     hipLaunchKernelGGL((glu_skinny_kernel<1>), grid, block, 0, stream, x, qg, sg, qu, su, h, part, (int)m,
                        (int)n, (int)k, gk, p.ss_per_split, ep);
   else
