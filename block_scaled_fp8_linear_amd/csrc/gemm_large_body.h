@@ -12,18 +12,14 @@ namespace fp8bl {
 namespace {
 
 constexpr int kBK = 64;                     // K per step
-constexpr int kBM = 256;                    // X rows per tile
+constexpr int kBM = 256;                    // X rows per tile (the plain kernels' and the tallest)
 constexpr int kBN = 256;                    // weight rows per tile
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * 64;
-constexpr int kStages = 3;
-constexpr int kXElems = kBM * kBK;          // bf16 elements of one stage's X tile (32 KB)
 constexpr int kWBytes = kBN * kBK;          // bytes of one stage's codes (16 KB)
-constexpr int kXLoads = kXElems * 2 / 16 / kThreads;   // 16-byte X loads per lane per step
 constexpr int kWLoads = kWBytes / 16 / kThreads;       // 16-byte code loads per lane per step
 constexpr uint32_t kOob = 0x80000000u;      // buffer offset past every valid range
 
-static_assert(kXLoads == 8, "one wave's X loads cover 64 rows of a stage");
 static_assert(kWLoads == 4, "one wave's code loads cover its 64 rows of a stage");
 static_assert(kBK == 64, "the X chunk permutation assumes 128-byte LDS rows");
 
@@ -73,7 +69,11 @@ struct LargeArgs {
 // (q, s) is the weight; for GATED and kGlu it is the gate weight and (q2, s2)
 // the up weight, and y receives the product of the pair. For kGradient N is
 // the weight's row length and K the number of its rows.
-template <bool SPLIT, bool GATED, Form FORM, int ACT>
+// MB: 32-row blocks of X per tile (8, 4 or 2), STAGES: ring length. Fewer rows
+// make a step shorter, so that the codes of a weight stream through at the
+// rate of HBM when there are not 256 rows to multiply: with MB = 2 two
+// workgroups share a CU.
+template <bool SPLIT, bool GATED, Form FORM, int ACT, int MB = 8, int STAGES = 3>
 __device__ __forceinline__
 void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__ q,
                      const float* __restrict__ s, const uint8_t* __restrict__ q2,
@@ -81,11 +81,17 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
                      float* __restrict__ part, int M, int N, int K, int gk,
                      int tiles_m, int tiles_n, int kt_per_split, int splits, int steps_per_unit,
                      const LargeArgs& la) {
-  static_assert(!(SPLIT && (GATED || FORM == kGlu)), "the gate needs whole sums: no K split");
-  static_assert(!GATED || FORM == kPlain, "GATED is a form of its own");
+  static_assert(!(SPLIT && GATED), "the SwiGLU needs whole sums: no K split");
+  static_assert(!GATED || (FORM == kPlain && MB == 8), "GATED is a form of its own");
+  static_assert(MB == 8 || MB == 4 || MB == 2, "row blocks go in pairs, a ring of eight fragments");
+  constexpr int kStages = STAGES;
+  constexpr int kTileM = 32 * MB;
+  constexpr int kXElems = kTileM * kBK;                         // bf16 elements of one stage's X tile
+  constexpr int kXLoads = kXElems * 2 / 16 / kThreads;          // 16-byte X loads per lane per step
+  static_assert(kXLoads == MB, "one wave's X loads cover a quarter of a stage's rows");
   constexpr int kScales = FORM == kGlu ? 2 : 1;                 // scale words per wave and step
   constexpr int kSElems = kScales * kWaves * 64 * 4 / 2;        // their slots (256 B each)
-  constexpr int kStageElems = kXElems + kWBytes / 2 + kSElems;  // stage size in bf16 elements (49 or 50 KB)
+  constexpr int kStageElems = kXElems + kWBytes / 2 + kSElems;  // stage size in bf16 elements (MB = 8: 49 KB)
   constexpr int kLoadsPerStep = kXLoads + kWLoads + kScales;
   static_assert((kStageElems * 2) % 256 == 0, "stages keep the LDS bank phase of their rows");
   static_assert(kStages * kStageElems * 2 <= 160 * 1024, "the ring fits the CU's LDS");
@@ -126,7 +132,7 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
     const int first_m = group * GM;
     const int gsize = min(tiles_m - first_m, GM);
     const int in_group = id - group * GM * tiles_n;
-    U.m0 = (first_m + in_group % gsize) * kBM;
+    U.m0 = (first_m + in_group % gsize) * kTileM;
     U.n0 = (in_group / gsize) * kTileN;
     U.kt0 = U.split * kt_per_split;
     U.nreal = min(kt_per_split, nkt - U.kt0);
@@ -147,7 +153,7 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   uint32_t xvo[kXLoads];
 #pragma unroll
   for (int i = 0; i < kXLoads; ++i)
-    xvo[i] = (uint32_t)((64 * wave + 8 * i + (lane >> 3)) * ldx * 2 + ((i & 1) ? xc_odd : xc_even) * 16);
+    xvo[i] = (uint32_t)((8 * MB * wave + 8 * i + (lane >> 3)) * ldx * 2 + ((i & 1) ? xc_odd : xc_even) * 16);
   // codes: load i of wave w fills the stage's code rows 64w + 16i .. +16
   // (64 bytes each, the step's K range) from its weight rows wrow + 16i ..;
   // lane l lands on row (l / 4), physical 16-byte chunk l % 4, holding the
@@ -182,7 +188,7 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   int lsrow;
   auto set_load_unit = [&](const Unit& U) {
     LU = U;
-    const uint32_t xrange = (uint32_t)(U.nreal > 0 ? min(M - U.m0, kBM) * ldx * 2 : 0);
+    const uint32_t xrange = (uint32_t)(U.nreal > 0 ? min(M - U.m0, kTileM) * ldx * 2 : 0);
     xrs = make_rsrc(x + (size_t)U.m0 * ldx, xrange);
     lwave_live = U.n0 + wrow < N;
     lsrow = lwave_live ? (U.n0 + wrow) / kBlock : 0;
@@ -212,7 +218,7 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
     // starts below it
     const int klim = kt < LU.nreal ? K - kbase : 0;
     const bool in = ((i & 1) ? xc_odd : xc_even) * 8 < klim;
-    lds_ptr_t to = (lds_ptr_t)&xs[sb + (64 * wave + 8 * i) * kBK];
+    lds_ptr_t to = (lds_ptr_t)&xs[sb + (8 * MB * wave + 8 * i) * kBK];
     if (FORM == kGradient && second(kt))
       __builtin_amdgcn_raw_ptr_buffer_load_lds(xrs2, to, 16, in ? xvo[i] : kOob, (uint32_t)(kbase * 2), 0, 0);
     else
@@ -317,16 +323,16 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   const int ahalf = lane >> 5;
   const int aswz = (arow >> 1) & 7;
   auto read_xf = [&](int sb, int f) -> bf16x8 {
-    const int t = f >> 3, mb = f & 7;
+    const int t = f / MB, mb = f % MB;
     const int c = 2 * ahalf + 4 * (t >> 1) + (t & 1);
     return *reinterpret_cast<const bf16x8*>(&xs[sb + arow * kBK + ((c ^ aswz) << 3) + mb * 32 * kBK]);
   };
 
-  f32x16 acc[2][8];
+  f32x16 acc[2][MB];
 #pragma unroll
   for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
-    for (int mb = 0; mb < 8; ++mb)
+    for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[nb][mb][r] = 0.0f;
 
@@ -354,16 +360,27 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   // slot of a fragment the same in every step (32 fragments a step)
   constexpr int kRing = 8;
   constexpr int kAhead = 4;
+  constexpr int kFrags = 4 * MB;
+  static_assert(kFrags % kRing == 0, "a fragment's slot is the same in every step");
+  // Fragment at which the next step's loads are waited for and its codes
+  // read, and the one with the barrier, before the first read of the next
+  // stage. Loads of the step STAGES - 1 ahead that are out by then.
+  constexpr int kFragBar = kFrags - kAhead;
+  constexpr int kFragWait = MB == 8 ? 24 : MB == 4 ? 8 : 4;
+  constexpr int kIssued = MB == 8 ? kXLoads + kWLoads : MB == 4 ? kXLoads + 2 : kXLoads + 2;
+  constexpr int kInFlight = (kStages - 3) * kLoadsPerStep + kIssued;
+  static_assert(kInFlight <= 63 && (kStages - 2) * kLoadsPerStep <= 63, "vmcnt holds the loads in flight");
   bf16x8 xr[kRing];
   u32x4 wdh[2][2];          // decoded weight operands (bf16 pairs), by sub-step parity
   u32x4 cA[2], cB[2];       // codes of K halves 0 and 1
-  float sc[2];              // this step's scales of the two weight blocks (one scale unless kGlu)
+  float sc[2], scn[2];      // this and the next step's scales of the two weight blocks (one unless kGlu)
 
-  // Prologue: steps 0 and 1 of the first unit in flight (every unit has at
-  // least three steps); wait for step 0, then prepare its first operands.
-  issue_all(0, 0);
-  issue_all(kStageElems, 1);
-  __builtin_amdgcn_s_waitcnt(vm_wait(kLoadsPerStep));
+  // Prologue: the first unit's first STAGES - 1 steps in flight (every unit has
+  // at least that many, dead ones included); wait for step 0, then prepare its
+  // first operands.
+#pragma unroll
+  for (int p = 0; p < kStages - 1; ++p) issue_all(p * kStageElems, p);
+  __builtin_amdgcn_s_waitcnt(vm_wait((kStages - 2) * kLoadsPerStep));
   wg_barrier();
   read_w(cA, 0, 0);
   sc[0] = read_s(0, 0);
@@ -375,36 +392,36 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
 
   const int col_lane = 64 * wave + 4 * ahalf;
   int S = 0;                 // stage of the step being computed
-  int lkt = 1;               // step (of LU) most recently loaded
+  int lkt = kStages - 2;     // step (of LU) most recently loaded
   for (int ci = 0; ci < my_units; ++ci) {
   for (int kt = 0; kt < steps_per_unit; ++kt) {
-    // the step two ahead: next step of LU, or step 0 of the next unit
+    // the step STAGES - 1 ahead: next step of LU, or step 0 of the next unit
     if (++lkt == steps_per_unit) {
       set_load_unit(unit_of(ci + 1));
       lkt = 0;
     }
     const int Sn = S == kStages - 1 ? 0 : S + 1;
-    const int L = Sn == kStages - 1 ? 0 : Sn + 1;
+    const int L = S == 0 ? kStages - 1 : S - 1;
     const int sb = S * kStageElems, sbn = Sn * kStageElems, sbl = L * kStageElems;
 
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       if (t == 0) read_w(cB, sb, 1);
 #pragma unroll
-      for (int mb = 0; mb < 8; mb += 2) {
+      for (int mb = 0; mb < MB; mb += 2) {
         // one region: the MFMAs of fragments f, f+1 with their share of the
         // other work, in a fixed order relative to the other regions
-        const int f = 8 * t + mb;
-        if (f == 24) {
-          // this wave's loads of the next step (issued during the previous
-          // step) have landed, with 12 of this step's still in flight: read
-          // its codes of K half 0 and its scale
-          __builtin_amdgcn_s_waitcnt(vm_wait(kXLoads + kWLoads));
+        const int f = MB * t + mb;
+        if (f == kFragWait) {
+          // this wave's loads of the next step (issued STAGES - 2 steps ago)
+          // have landed, with the later ones still in flight: read its codes
+          // of K half 0 and its scale
+          __builtin_amdgcn_s_waitcnt(vm_wait(kInFlight));
           read_w(cA, sbn, 0);
-          sc[0] = read_s(sbn, 0);
-          sc[1] = kScales == 2 ? read_s(sbn, 1) : sc[0];
+          scn[0] = read_s(sbn, 0);
+          scn[1] = kScales == 2 ? read_s(sbn, 1) : scn[0];
         }
-        if (f == 28) {
+        if (f == kFragBar) {
           // every wave is done with this stage (its last reads returned)
           // and has put its part of the next stage in place
           __builtin_amdgcn_s_waitcnt(kLgkmWait0);
@@ -415,12 +432,23 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int fa = f + j + kAhead;
-          xr[fa % kRing] = fa < 32 ? read_xf(sb, fa) : read_xf(sbn, fa - 32);
+          xr[fa % kRing] = fa < kFrags ? read_xf(sb, fa) : read_xf(sbn, fa - kFrags);
         }
-        // the loads of the step two ahead, into the stage freed by the last barrier
-        if (f <= 14) issue_x(sbl, lkt, (f >> 1) + 0);
-        if (f >= 16 && f <= 22) issue_w(sbl, lkt, (f - 16) >> 1);
-        if (f == 24) issue_s(sbl, lkt);
+        // the loads of the step STAGES - 1 ahead, into the stage freed by the last barrier
+        if constexpr (MB == 8) {
+          if (f <= 14) issue_x(sbl, lkt, (f >> 1) + 0);
+          if (f >= 16 && f <= 22) issue_w(sbl, lkt, (f - 16) >> 1);
+          if (f == 24) issue_s(sbl, lkt);
+        } else if constexpr (MB == 4) {
+          if (f <= 2) { issue_x(sbl, lkt, f); issue_x(sbl, lkt, f + 1); }
+          if (f >= 4 && f <= 10) issue_w(sbl, lkt, (f - 4) >> 1);
+          if (f == 12) issue_s(sbl, lkt);
+        } else {
+          if (f == 0) { issue_x(sbl, lkt, 0); issue_x(sbl, lkt, 1); }
+          if (f == 2) { issue_w(sbl, lkt, 0); issue_w(sbl, lkt, 1); }
+          if (f == 4) { issue_w(sbl, lkt, 2); issue_w(sbl, lkt, 3); }
+          if (f == 6) issue_s(sbl, lkt);
+        }
         // the next sub-step's weight operands, a quarter (one block's half
         // K of the sub-step: four codes to bf16) per region: sub-steps 1..3
         // from this step's codes, the next step's sub-step 0 from its codes
@@ -429,15 +457,18 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
           const int nb = q4 >> 1, half = q4 & 1;
           const int tn = (t + 1) & 3;          // sub-step being prepared
           const u32x4 (&c)[2] = tn <= 1 ? cA : cB;
-          const u32x2 v = dequant4(c[nb][2 * (tn & 1) + half], sc[nb]);
+          const u32x2 v = dequant4(c[nb][2 * (tn & 1) + half], tn == 0 ? scn[nb] : sc[nb]);
           wdh[tn & 1][nb][2 * half] = v[0];
           wdh[tn & 1][nb][2 * half + 1] = v[1];
         };
         if (t < 3) {
-          piece(mb >> 1);
-        } else if (f >= 28) {
-          piece(f - 28);
-          piece(f - 28 + 1);
+          constexpr int kPieces = 8 / MB;
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) piece((mb >> 1) * kPieces + i);
+        } else if (f >= kFragBar) {
+          constexpr int kPieces = MB == 2 ? 4 : 2;
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) piece((f - (MB == 2 ? 6 : kFragBar)) + i);
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -445,21 +476,25 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
           for (int nb = 0; nb < 2; ++nb)
             acc[nb][mb + j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
                 __builtin_bit_cast(bf16x8, wdh[t & 1][nb]), xr[(f + j) % kRing], acc[nb][mb + j], 0, 0, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
-        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+        if constexpr (MB == 8) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+          __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
     }
 
+    sc[0] = scn[0];
+    sc[1] = scn[1];
     S = Sn;
   }
 
@@ -470,7 +505,7 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
     // the hardware; columns past N get an out-of-range offset. (The host
     // keeps 256 rows of the output within 2^31 bytes.)
     const Unit CU = unit_of(ci);
-    const int rows = min(M - CU.m0, kBM);
+    const int rows = min(M - CU.m0, kTileM);
     const int col_base = CU.n0 + col_lane;
     if constexpr (GATED) {
       // Gate wave w < 2 finishes row blocks 0..3 of the slice and up wave
@@ -548,152 +583,176 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
           }
         }
       }
-    } else if constexpr ((FORM == kLayer || FORM == kGradient) && !SPLIT) {
-      // Each 32-row block of the wave's slice through LDS in fp32 (the layout
-      // of the split partials below), back as four consecutive columns of a
-      // row per lane: a lane keeps its columns' bias, and residual, z and y
-      // move as whole 128-byte pieces of rows. One rounding per output.
+    } else if constexpr (FORM != kPlain && (!SPLIT || FORM == kGlu) || MB < 8) {
+      // The forms' outputs go through LDS in fp32, kEpiRows rows of the wave's
+      // 64 weight rows at a time: 256-byte rows, 16-byte chunk c of row r at
+      // c ^ (r % 16), read back as four consecutive columns of a row per lane.
+      // A lane keeps its columns' bias, and residual, z and y move as whole
+      // 128-byte pieces of rows (kGlu: chunks 0..7 of a row are its 32 gate
+      // columns, 8..15 the up columns, and a lane reads four of each). One
+      // rounding per output. The LDS is the wave's own part of the stage the
+      // last step used, X rows (8 KB) for MB = 8, else codes (4 KB): every
+      // wave finished reading that stage before the last barrier, and only
+      // this wave refills its part, with loads it issues after these reads
+      // have returned.
+      constexpr int kHalves = MB == 8 ? 1 : 2;
+      constexpr int kEpiRows = 32 / kHalves;
+      constexpr int kLanesRow = FORM == kGlu ? 8 : 16;        // lanes side by side on a row
+      constexpr int kRowsRead = 64 / kLanesRow;
+      const LayerEpilogue ep = FORM == kLayer || FORM == kGlu ? la.ep : LayerEpilogue{};
       int le;
       asm volatile("" : "=v"(le) : "0"(lane));
       const int er = le & 31, eh = le >> 5;
-      const int cc = le & 15, rq = le >> 4;
-      const int col4 = CU.n0 + 64 * wave + 4 * cc;
-      uint8_t* const buf =
-          reinterpret_cast<uint8_t*>(&xs[(S == 0 ? 2 : S - 1) * kStageElems + wave * 64 * kBK]);
-      // (kGradient has no such parts: none of this is compiled for it)
-      const LayerEpilogue ep = FORM == kLayer ? la.ep : LayerEpilogue{};
-      const size_t tile = (size_t)CU.m0 * N;
-      const uint32_t range = (uint32_t)(rows * N * 2);
-      const __amdgpu_buffer_rsrc_t yrs = make_rsrc(y + tile, range);
-      const __amdgpu_buffer_rsrc_t rrs =
-          make_rsrc(ep.residual ? ep.residual + tile : y + tile, ep.residual ? range : 0);
-      const __amdgpu_buffer_rsrc_t zrs = make_rsrc(ep.z ? ep.z + tile : y + tile, ep.z ? range : 0);
-      const __amdgpu_buffer_rsrc_t brs =
-          make_rsrc(ep.bias ? ep.bias : y, ep.bias ? (uint32_t)(N * 2) : 0);
-      const bool quad = FORM == kGradient || (N & 3) == 0;
-      float bias[4];
+      const int cc = le % kLanesRow, rq = le / kLanesRow;
+      const int col4 = CU.n0 + (FORM == kGlu ? 32 : 64) * wave + 4 * cc;
+      const int last = (S == 0 ? kStages - 1 : S - 1) * kStageElems;
+      uint8_t* const buf = reinterpret_cast<uint8_t*>(
+          &xs[last + (MB == 8 ? wave * 64 * kBK : kXElems + wave * 64 * kBK / 2)]);
+      // The lanes of one half write while the others wait: without the wave
+      // barriers the compiler may run the two halves' lanes through the whole
+      // epilogue one after the other, and reads would miss their writes.
+      auto put = [&](int mb, int hf) {
+        if constexpr (kHalves == 2) __builtin_amdgcn_wave_barrier();
+        if (kHalves == 1 || (er >> 4) == hf) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        bias[e] = bf16_f32(__builtin_amdgcn_raw_buffer_load_b16(brs, (uint32_t)((col4 + e) * 2), 0, 0));
+          for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
-      for (int mb = 0; mb < 8; ++mb) {
-#pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const f32x16& a = acc[nb][mb];
-            const u32x4 v = {__float_as_uint(a[4 * g]), __float_as_uint(a[4 * g + 1]),
-                             __float_as_uint(a[4 * g + 2]), __float_as_uint(a[4 * g + 3])};
-            const int c = 8 * nb + 2 * g + eh;
-            *reinterpret_cast<u32x4*>(buf + er * 256 + ((c ^ (er & 15)) << 4)) = v;
-          }
-        if (quad) {
-          const uint32_t at0 = (uint32_t)(((32 * mb + rq) * N + col4) * 2);
-          const bool in = col4 < N;
-          u32x2 res[8] = {};
-          if (ep.residual)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              res[j] = __builtin_bit_cast(
-                u32x2, __builtin_amdgcn_raw_buffer_load_b64(rrs, in ? at0 + (uint32_t)(8 * j * N) : kOob, 0, 0));
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int r = 4 * j + rq;
-            const u32x4 v = *reinterpret_cast<const u32x4*>(buf + r * 256 + ((cc ^ (r & 15)) << 4));
-            float t[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) t[e] = __uint_as_float(v[e]) + bias[e];
-            const uint32_t off = in ? at0 + (uint32_t)(8 * j * N) : kOob;
-            const u32x2 zo = {pack_bf16x2(t[0], t[1]), pack_bf16x2(t[2], t[3])};
-            if (ep.z) __builtin_amdgcn_raw_buffer_store_b64(zo, zrs, off, 0, kNonTemporal);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) t[e] = act_f32<ACT>(t[e]);
-            if (ep.residual) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                t[e] += __uint_as_float((e & 1) ? res[j][e >> 1] & 0xFFFF0000u : res[j][e >> 1] << 16);
+            for (int g = 0; g < 4; ++g) {
+              const f32x16& a = acc[nb][mb];
+              const u32x4 v = {__float_as_uint(a[4 * g]), __float_as_uint(a[4 * g + 1]),
+                               __float_as_uint(a[4 * g + 2]), __float_as_uint(a[4 * g + 3])};
+              const int c = 8 * nb + 2 * g + eh;
+              *reinterpret_cast<u32x4*>(buf + (er & (kEpiRows - 1)) * 256 + ((c ^ (er & 15)) << 4)) = v;
             }
-            const u32x2 yo = {pack_bf16x2(t[0], t[1]), pack_bf16x2(t[2], t[3])};
-            __builtin_amdgcn_raw_buffer_store_b64(yo, yrs, off, 0, kNonTemporal);
+        }
+        if constexpr (kHalves == 2) __builtin_amdgcn_wave_barrier();
+      };
+      auto get = [&](int r, int c) -> u32x4 {
+        return *reinterpret_cast<const u32x4*>(buf + r * 256 + ((c ^ (r & 15)) << 4));
+      };
+      const size_t tile = (size_t)CU.m0 * N;
+      const bool quad = FORM == kGradient || (N & 3) == 0;    // (kGradient: a multiple of 16 always)
+      if constexpr (SPLIT) {
+        // fp32 partials: slab `split`, for kGlu slabs 2 split (gate) and 2 split + 1 (up)
+        const size_t slab = partial_slab(M, N);
+        float* const p0 = part + (size_t)(FORM == kGlu ? 2 * CU.split : CU.split) * slab + tile;
+        const uint32_t range = (uint32_t)(rows * N * 4);
+        const __amdgpu_buffer_rsrc_t prs = make_rsrc(p0, range);
+        const __amdgpu_buffer_rsrc_t prs2 = make_rsrc(p0 + slab, FORM == kGlu ? range : 0);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int hf = 0; hf < kHalves; ++hf) {
+            put(mb, hf);
+#pragma unroll
+            for (int j = 0; j < kEpiRows / kRowsRead; ++j) {
+              const int r = kRowsRead * j + rq;
+              const u32x4 v = get(r, cc);
+              u32x4 v2 = {};
+              if (FORM == kGlu) v2 = get(r, cc + 8);
+              const uint32_t at = (uint32_t)(((32 * mb + kEpiRows * hf + r) * N + col4) * 4);
+              if (quad) {
+                const uint32_t off = col4 < N ? at : kOob;
+                __builtin_amdgcn_raw_buffer_store_b128(v, prs, off, 0, 0);
+                if (FORM == kGlu) __builtin_amdgcn_raw_buffer_store_b128(v2, prs2, off, 0, 0);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t off = col4 + e < N ? at + 4 * e : kOob;
+                  const uint32_t w = v[e], w2 = v2[e];
+                  __builtin_amdgcn_raw_buffer_store_b32(w, prs, off, 0, 0);
+                  if (FORM == kGlu) __builtin_amdgcn_raw_buffer_store_b32(w2, prs2, off, 0, 0);
+                }
+              }
+            }
           }
-        } else {
-          // rows are only 2-byte aligned: one element at a time
+      } else {
+        const uint32_t range = (uint32_t)(rows * N * 2);
+        const __amdgpu_buffer_rsrc_t yrs = make_rsrc(y + tile, range);
+        // (an absent array: no range, so nothing is read or written)
+        const __amdgpu_buffer_rsrc_t rrs =
+            make_rsrc(ep.residual ? ep.residual + tile : y + tile, ep.residual ? range : 0);
+        const __amdgpu_buffer_rsrc_t brs = make_rsrc(ep.bias ? ep.bias : y, ep.bias ? (uint32_t)(N * 2) : 0);
+        uint16_t* const save = FORM == kGlu ? ep.g : ep.z;
+        const __amdgpu_buffer_rsrc_t zrs = make_rsrc(save ? save + tile : y + tile, save ? range : 0);
+        const __amdgpu_buffer_rsrc_t urs = make_rsrc(ep.u ? ep.u + tile : y + tile, ep.u ? range : 0);
+        float bias[4] = {};
+        if (FORM == kLayer && ep.bias)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            bias[e] = bf16_f32(__builtin_amdgcn_raw_buffer_load_b16(brs, (uint32_t)((col4 + e) * 2), 0, 0));
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int hf = 0; hf < kHalves; ++hf) {
+            put(mb, hf);
+            const uint32_t at0 = (uint32_t)(((32 * mb + kEpiRows * hf + rq) * N + col4) * 2);
+            const uint32_t step = (uint32_t)(2 * kRowsRead * N);
+            if (quad) {
+              const bool in = col4 < N;
+              u32x2 res[kEpiRows / kRowsRead] = {};
+              if (FORM == kLayer && ep.residual)
+#pragma unroll
+                for (int j = 0; j < kEpiRows / kRowsRead; ++j)
+                  res[j] = __builtin_bit_cast(
+                      u32x2, __builtin_amdgcn_raw_buffer_load_b64(rrs, in ? at0 + (uint32_t)j * step : kOob, 0, 0));
+#pragma unroll
+              for (int j = 0; j < kEpiRows / kRowsRead; ++j) {
+                const int r = kRowsRead * j + rq;
+                const uint32_t off = in ? at0 + (uint32_t)j * step : kOob;
+                const u32x4 v = get(r, cc);
+                float t[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) t[e] = __uint_as_float(v[e]) + bias[e];
+                const u32x2 zo = {pack_bf16x2(t[0], t[1]), pack_bf16x2(t[2], t[3])};
+                if (FORM != kGradient && save) __builtin_amdgcn_raw_buffer_store_b64(zo, zrs, off, 0, kNonTemporal);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) t[e] = act_f32<ACT>(t[e]);
+                if constexpr (FORM == kGlu) {
+                  const u32x4 v2 = get(r, cc + 8);
+                  float u[4];
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    u[e] = __uint_as_float(v2[e]);
+                    t[e] *= u[e];
+                  }
+                  const u32x2 uo = {pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3])};
+                  if (save) __builtin_amdgcn_raw_buffer_store_b64(uo, urs, off, 0, kNonTemporal);
+                }
+                if (FORM == kLayer && ep.residual) {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    t[e] += __uint_as_float((e & 1) ? res[j][e >> 1] & 0xFFFF0000u : res[j][e >> 1] << 16);
+                }
+                const u32x2 yo = {pack_bf16x2(t[0], t[1]), pack_bf16x2(t[2], t[3])};
+                __builtin_amdgcn_raw_buffer_store_b64(yo, yrs, off, 0, kNonTemporal);
+              }
+            } else {
+              // rows are only 2-byte aligned: one element at a time
 #pragma unroll 1
-          for (int j = 0; j < 8; ++j) {
-            const int r = 4 * j + rq;
-            const u32x4 v = *reinterpret_cast<const u32x4*>(buf + r * 256 + ((cc ^ (r & 15)) << 4));
+              for (int j = 0; j < kEpiRows / kRowsRead; ++j) {
+                const int r = kRowsRead * j + rq;
+                const u32x4 v = get(r, cc);
+                u32x4 v2 = {};
+                if (FORM == kGlu) v2 = get(r, cc + 8);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t off = col4 + e < N ? (uint32_t)(((32 * mb + r) * N + col4 + e) * 2) : kOob;
-              float t = __uint_as_float(v[e]) + bias[e];
-              __builtin_amdgcn_raw_buffer_store_b16(f32_bf16(t), zrs, off, 0, 0);
-              t = act_f32<ACT>(t);
-              if (ep.residual) t += bf16_f32(__builtin_amdgcn_raw_buffer_load_b16(rrs, off, 0, 0));
-              __builtin_amdgcn_raw_buffer_store_b16(f32_bf16(t), yrs, off, 0, 0);
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t off = col4 + e < N ? at0 + (uint32_t)j * step + 2 * e : kOob;
+                  const uint32_t w = v[e], w2 = v2[e];
+                  const float z = __uint_as_float(w) + bias[e], u = __uint_as_float(w2);
+                  float t = act_f32<ACT>(z);
+                  if (FORM == kGlu) t *= u;
+                  if (FORM == kLayer && ep.residual)
+                    t += bf16_f32(__builtin_amdgcn_raw_buffer_load_b16(rrs, off, 0, 0));
+                  if (save) {
+                    __builtin_amdgcn_raw_buffer_store_b16(f32_bf16(z), zrs, off, 0, 0);
+                    if (FORM == kGlu) __builtin_amdgcn_raw_buffer_store_b16(f32_bf16(u), urs, off, 0, 0);
+                  }
+                  __builtin_amdgcn_raw_buffer_store_b16(f32_bf16(t), yrs, off, 0, 0);
+                }
+              }
             }
           }
-        }
-      }
-    } else if constexpr (FORM == kGlu) {
-      // The same trip through LDS: chunks 0..7 of a row are its 32 gate
-      // columns, 8..15 the up columns; a lane reads four of each.
-      int le;
-      asm volatile("" : "=v"(le) : "0"(lane));
-      const int er = le & 31, eh = le >> 5;
-      const int cc = le & 7, rq = le >> 3;
-      const int col4 = CU.n0 + 32 * wave + 4 * cc;
-      uint8_t* const buf =
-          reinterpret_cast<uint8_t*>(&xs[(S == 0 ? 2 : S - 1) * kStageElems + wave * 64 * kBK]);
-      const size_t tile = (size_t)CU.m0 * N;
-      const uint32_t range = (uint32_t)(rows * N * 2);
-      const __amdgpu_buffer_rsrc_t yrs = make_rsrc(y + tile, range);
-      const __amdgpu_buffer_rsrc_t grs = make_rsrc(la.ep.g ? la.ep.g + tile : y + tile, la.ep.g ? range : 0);
-      const __amdgpu_buffer_rsrc_t urs = make_rsrc(la.ep.u ? la.ep.u + tile : y + tile, la.ep.u ? range : 0);
-      const bool quad = (N & 3) == 0;
-#pragma unroll
-      for (int mb = 0; mb < 8; ++mb) {
-#pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const f32x16& a = acc[nb][mb];
-            const u32x4 v = {__float_as_uint(a[4 * g]), __float_as_uint(a[4 * g + 1]),
-                             __float_as_uint(a[4 * g + 2]), __float_as_uint(a[4 * g + 3])};
-            const int c = 8 * nb + 2 * g + eh;
-            *reinterpret_cast<u32x4*>(buf + er * 256 + ((c ^ (er & 15)) << 4)) = v;
-          }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = 8 * j + rq;
-          const u32x4 gv = *reinterpret_cast<const u32x4*>(buf + r * 256 + ((cc ^ (r & 15)) << 4));
-          const u32x4 uv = *reinterpret_cast<const u32x4*>(buf + r * 256 + (((cc + 8) ^ (r & 15)) << 4));
-          float g4[4], u4[4], h4[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            g4[e] = __uint_as_float(gv[e]);
-            u4[e] = __uint_as_float(uv[e]);
-            h4[e] = act_f32<ACT>(g4[e]) * u4[e];
-          }
-          if (quad) {
-            const uint32_t off = col4 < N ? (uint32_t)(((32 * mb + r) * N + col4) * 2) : kOob;
-            const u32x2 go = {pack_bf16x2(g4[0], g4[1]), pack_bf16x2(g4[2], g4[3])};
-            const u32x2 uo = {pack_bf16x2(u4[0], u4[1]), pack_bf16x2(u4[2], u4[3])};
-            const u32x2 ho = {pack_bf16x2(h4[0], h4[1]), pack_bf16x2(h4[2], h4[3])};
-            if (la.ep.g) {
-              __builtin_amdgcn_raw_buffer_store_b64(go, grs, off, 0, kNonTemporal);
-              __builtin_amdgcn_raw_buffer_store_b64(uo, urs, off, 0, kNonTemporal);
-            }
-            __builtin_amdgcn_raw_buffer_store_b64(ho, yrs, off, 0, kNonTemporal);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t off = col4 + e < N ? (uint32_t)(((32 * mb + r) * N + col4 + e) * 2) : kOob;
-              __builtin_amdgcn_raw_buffer_store_b16(f32_bf16(g4[e]), grs, off, 0, 0);
-              __builtin_amdgcn_raw_buffer_store_b16(f32_bf16(u4[e]), urs, off, 0, 0);
-              __builtin_amdgcn_raw_buffer_store_b16(f32_bf16(h4[e]), yrs, off, 0, 0);
-            }
-          }
-        }
       }
     } else if constexpr (!SPLIT) {
       const __amdgpu_buffer_rsrc_t yrs = make_rsrc(y + (size_t)CU.m0 * N, (uint32_t)(rows * N * 2));
@@ -825,7 +884,7 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
 #pragma unroll
     for (int nb = 0; nb < 2; ++nb)
 #pragma unroll
-      for (int mb = 0; mb < 8; ++mb)
+      for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[nb][mb][r] = 0.0f;
   }

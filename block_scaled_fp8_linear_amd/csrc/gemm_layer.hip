@@ -7,137 +7,265 @@ namespace fp8bl {
 
 namespace {
 
-template <int ACT>
-__global__ __launch_bounds__(kThreads, 1)
-void linear_act_large_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ q,
-                             const float* __restrict__ s, uint16_t* __restrict__ y, int M, int N, int K,
-                             int gk, int tiles_m, int tiles_n, int steps, LargeArgs la) {
-  gemm_large_body<false, false, kLayer, ACT>(x, q, s, nullptr, nullptr, y, nullptr, M, N, K, gk, tiles_m,
-                                             tiles_n, steps, 1, max(steps, 2), la);
+// Tile heights (32-row blocks of X, ring stages, workgroups a CU).
+template <int MB>
+struct Tile;
+template <>
+struct Tile<8> {
+  static constexpr int kStages = 3, kPerCu = 1;
+};
+template <>
+struct Tile<4> {
+  static constexpr int kStages = 4, kPerCu = 1;
+};
+template <>
+struct Tile<2> {
+  static constexpr int kStages = 3, kPerCu = 2;
+};
+
+struct Grid {
+  int gk, tiles_m, tiles_n, steps, splits, steps_per_unit;
+};
+
+template <bool SPLIT, int ACT, int MB>
+__global__ __launch_bounds__(kThreads, Tile<MB>::kPerCu)
+void linear_act_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ q,
+                       const float* __restrict__ s, uint16_t* y, float* __restrict__ part, int M, int N,
+                       int K, Grid g, LargeArgs la) {
+  gemm_large_body<SPLIT, false, kLayer, ACT, MB, Tile<MB>::kStages>(
+      x, q, s, nullptr, nullptr, y, part, M, N, K, g.gk, g.tiles_m, g.tiles_n, g.steps, g.splits,
+      g.steps_per_unit, la);
 }
 
-template <int ACT>
-__global__ __launch_bounds__(kThreads, 1)
-void glu_large_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ qg,
-                      const float* __restrict__ sg, const uint8_t* __restrict__ qu,
-                      const float* __restrict__ su, uint16_t* __restrict__ h, int M, int N, int K, int gk,
-                      int tiles_m, int tiles_n, int steps, LargeArgs la) {
-  gemm_large_body<false, false, kGlu, ACT>(x, qg, sg, qu, su, h, nullptr, M, N, K, gk, tiles_m, tiles_n,
-                                           steps, 1, max(steps, 2), la);
+template <bool SPLIT, int ACT, int MB>
+__global__ __launch_bounds__(kThreads, Tile<MB>::kPerCu)
+void glu_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ qg, const float* __restrict__ sg,
+                const uint8_t* __restrict__ qu, const float* __restrict__ su, uint16_t* __restrict__ h,
+                float* __restrict__ part, int M, int N, int K, Grid g, LargeArgs la) {
+  gemm_large_body<SPLIT, false, kGlu, ACT, MB, Tile<MB>::kStages>(
+      x, qg, sg, qu, su, h, part, M, N, K, g.gk, g.tiles_m, g.tiles_n, g.steps, g.splits, g.steps_per_unit, la);
 }
 
 // dx = x W (+ x2 W2): C output columns, R weight rows. The weight's rows are
 // the reduction: codes come in as [row][column] and transposing LDS reads
 // (ds_read_b64_tr_b8) hand each lane eight rows of its column, so neither a
 // transposed copy of the weight nor a shuffle is needed, and one decode per
-// code feeds 256 rows as in the forward.
-template <bool SPLIT>
-__global__ __launch_bounds__(kThreads, 1)
+// code feeds the tile's rows as in the forward.
+template <bool SPLIT, int MB>
+__global__ __launch_bounds__(kThreads, Tile<MB>::kPerCu)
 void input_gradient_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ q,
                            const float* __restrict__ s, const uint8_t* __restrict__ q2,
                            const float* __restrict__ s2, uint16_t* __restrict__ dx,
-                           float* __restrict__ part, int M, int C, int R, int gk, int tiles_m, int tiles_c,
-                           int steps_per_split, int splits, LargeArgs la) {
-  gemm_large_body<SPLIT, false, kGradient, kActNone>(x, q, s, q2, s2, dx, part, M, C, R, gk, tiles_m,
-                                                     tiles_c, steps_per_split, splits,
-                                                     max(steps_per_split, 2), la);
+                           float* __restrict__ part, int M, int C, int R, Grid g, LargeArgs la) {
+  gemm_large_body<SPLIT, false, kGradient, kActNone, MB, Tile<MB>::kStages>(
+      x, q, s, q2, s2, dx, part, M, C, R, g.gk, g.tiles_m, g.tiles_n, g.steps, g.splits, g.steps_per_unit, la);
 }
 
 int blocks_of(int64_t v) { return (int)((v + kBlock - 1) / kBlock); }
 
-// The input gradient's plan: the large kernel's over the summed reduction.
-LargePlan plan_gradient(int64_t m, int64_t n, int64_t k, int products) {
-  const int64_t steps = (n + kBK - 1) / kBK * products;
-  return plan_large(m, k, steps * kBK);
+// Tile height and K splits of one of the three products: tiles of `cols`
+// output columns, `steps` 64-wide steps of the reduction, `words` fp32 partials
+// an output (two for the gated pair). The model, in microseconds, was fitted
+// to 900 measurements of the three products on MI355X (48 to 512 rows, six
+// weights from 1024 x 1024 to 25600 x 5120, every tile height, 1 to 12
+// splits; rms 7%, and the plan it picks is 2% slower than the best measured
+// one on average, 19% at worst): a fixed part, then rounds of units over the
+// chip, a step taking longer the more of the chip runs, then the join.
+//   64 x 5120 x 5120    64-row tiles, 12 splits 20.2   256-row tiles 25.2
+//   128 x 25600 x 5120  64 rows 71, 128 rows, 2 splits 58.5, 256 rows 72
+//   512 x 25600 x 5120  64 rows 194, 128 rows 156, 256 rows, unsplit 122
+struct LayerPlan {
+  int mb, splits, steps_per_split;
+  double cost;
+};
+struct TileCost {
+  int mb, slots;                             // slots: units at once on 256 CUs
+  double fixed, step_few, step_full, unit;   // step_few: when few CUs run
+};
+constexpr TileCost kTileCosts[] = {{8, 256, 8.8, 1.07, 1.20, 1.2},
+                                   {4, 256, 8.7, 0.77, 0.84, 0.4},
+                                   {2, 512, 7.3, 0.71, 1.15, 0.0}};
+constexpr int kMaxSplits = 32;
+
+LayerPlan plan_tiles(int64_t m, int64_t n, int cols, int64_t steps, int words) {
+  LayerPlan best{8, 1, (int)steps, 1e300};
+  for (const TileCost& t : kTileCosts) {
+    const int64_t tiles = ((m + 32 * t.mb - 1) / (32 * t.mb)) * ((n + cols - 1) / cols);
+    for (int sp = 1; sp <= kMaxSplits; ++sp) {
+      const int64_t per = (steps + sp - 1) / sp;
+      if (sp > 1 && per < 4) break;
+      const int64_t units = tiles * sp;
+      const int64_t rest = units % t.slots;
+      double cost = t.fixed + (double)(units / t.slots) * (per * t.step_full + t.unit);
+      if (rest > 0) {
+        // where two workgroups share a CU, one CU with two sets the time
+        const double fill = t.slots == 256 ? (double)rest / 256 : rest <= 256 ? 0.0 : 0.7 + 0.3 * (rest - 256) / 256;
+        cost += per * (t.step_few + (t.step_full - t.step_few) * fill) + t.unit;
+      }
+      if (sp > 1) cost += 1.0 + 1.2e-6 * (double)(m * n) * (sp * words + 1);
+      if (cost < best.cost) best = LayerPlan{t.mb, sp, (int)per, cost};
+    }
+  }
+  best.splits = (int)((steps + best.steps_per_split - 1) / best.steps_per_split);
+  return best;
 }
+
+Grid grid_of(const LayerPlan& p, int64_t m, int64_t n, int cols, int64_t k) {
+  const int stages = p.mb == 4 ? Tile<4>::kStages : Tile<8>::kStages;
+  static_assert(Tile<8>::kStages == Tile<2>::kStages, "two ring lengths");
+  return Grid{blocks_of(k), (int)((m + 32 * p.mb - 1) / (32 * p.mb)), (int)((n + cols - 1) / cols),
+              p.steps_per_split, p.splits, p.steps_per_split > stages - 1 ? p.steps_per_split : stages - 1};
+}
+
+// One persistent workgroup per slot walks its (tile, split) units.
+dim3 blocks_for(const LayerPlan& p, const Grid& g) {
+  const int64_t units = (int64_t)g.tiles_m * g.tiles_n * g.splits;
+  const int64_t slots = (int64_t)device_cus() * (p.mb == 2 ? Tile<2>::kPerCu : 1);
+  return dim3((uint32_t)(units < slots ? units : slots));
+}
+
+// Calls f with the tile height as a compile-time constant.
+template <int V>
+struct Const {
+  static constexpr int value = V;
+};
+template <typename F>
+void with_rows(int mb, F&& f) {
+  if (mb == 8) f(Const<8>{});
+  else if (mb == 4) f(Const<4>{});
+  else f(Const<2>{});
+}
+
+size_t partial_bytes(const LayerPlan& p, int64_t m, int64_t n, int words) {
+  return p.splits <= 1 ? 0 : round_up((size_t)p.splits * words * partial_slab(m, n) * sizeof(float), kWorkspaceAlign);
+}
+
+int64_t steps_of(int64_t r) { return (r + kBK - 1) / kBK; }
 
 }  // namespace
 
-// Rows up to which the weight-streaming kernels of gemm_layer_skinny.hip run
-// (one pass over the weight; they hold two 16-row operands).
-constexpr int64_t kSkinnyRows = 32;
+// Which of a product's two kernels runs: the streams of gemm_layer_skinny.hip
+// (up to 32 rows) or the tiles. The streams start and end faster and keep more
+// codes in flight; the tiles read X once a workgroup instead of once a wave.
+// Measured on MI355X, stream against tiles, microseconds:
+//   linear  16 x 25600 x 5120  38.0  39.4    32 x 5120 x 5120  16.6  17.5
+//           32 x 12288 x 4096  24.8  21.3    32 x 25600 x 5120  53.1  40.5
+//   gated    4 x 25600 x 5120  39.3  49.9    16 x 12288 x 4096  22.8  26.9
+//           16 x 5120 x 25600  71.8  50.8    32 x 5120 x 2560  16.2  17.2
+//           32 x 5120 x 5120   27.6  21.1
+//   input gradient (rows x weight rows x columns)
+//           16 x 12288 x 4096  17.9  22.0    16 x 25600 x 5120  40.5  37.4
+//           32 x 2048 x 4096   10.4  12.2    32 x 5120 x 5120   18.9  16.6
+enum Product { kLinear, kPair, kInputGradient };
+bool streams(Product p, int64_t m, int64_t codes) {
+  if (m > 32) return false;
+  switch (p) {
+    case kLinear: return m <= 16 || codes <= (1 << 25);
+    case kPair: return m <= 4 || codes <= (m <= 16 ? 1 << 27 : 1 << 25);
+    default: return codes <= (m <= 16 ? 1 << 26 : 1 << 23);
+  }
+}
 
 size_t linear_act_bytes(int64_t m, int64_t n, int64_t k) {
-  return m <= kSkinnyRows ? linear_act_skinny_bytes(m, n, k) : large_workspace_bytes(m, n, k);
+  if (streams(kLinear, m, n * k)) return linear_act_skinny_bytes(m, n, k);
+  return partial_bytes(plan_tiles(m, n, kBN, steps_of(k), 1), m, n, 1);
 }
 
 hipError_t launch_linear_act(const uint16_t* x, const uint8_t* q, const float* s, uint16_t* y,
                              const LayerEpilogue& ep, int64_t m, int64_t n, int64_t k, void* ws,
                              size_t ws_bytes, hipStream_t stream) {
-  if (m <= kSkinnyRows) return launch_linear_act_skinny(x, q, s, y, ep, m, n, k, ws, ws_bytes, stream);
-  const LargePlan p = plan_large(m, n, k);
-  if (p.splits > 1) {
-    if (ws == nullptr || ws_bytes < large_workspace_bytes(m, n, k)) return hipErrorInvalidValue;
-    float* const part = static_cast<float*>(ws);
-    const hipError_t e = launch_gemm_large_partials(p, x, q, s, part, m, n, k, stream);
-    if (e != hipSuccess) return e;
-    return launch_join_layer(part, y, p.splits, m, n, ep, stream);
-  }
-  const int tiles_m = (int)((m + kBM - 1) / kBM), tiles_n = (int)((n + kBN - 1) / kBN);
-  const int units = tiles_m * tiles_n, grid = units < device_cus() ? units : device_cus();
+  if (streams(kLinear, m, n * k)) return launch_linear_act_skinny(x, q, s, y, ep, m, n, k, ws, ws_bytes, stream);
+  const LayerPlan p = plan_tiles(m, n, kBN, steps_of(k), 1);
+  const Grid g = grid_of(p, m, n, kBN, k);
   const LargeArgs la{ep, nullptr, 0, 0};
-  with_act(ep.act, [&](auto a) {
-    hipLaunchKernelGGL((linear_act_large_kernel<decltype(a)::value>), dim3((uint32_t)grid), dim3(kThreads), 0,
-                       stream, x, q, s, y, (int)m, (int)n, (int)k, blocks_of(k), tiles_m, tiles_n,
-                       p.kt_per_split, la);
+  const dim3 grid = blocks_for(p, g);
+  if (p.splits == 1) {
+    with_act(ep.act, [&](auto a) {
+      constexpr int A = decltype(a)::value;
+      with_rows(p.mb, [&](auto mb) {
+        hipLaunchKernelGGL((linear_act_kernel<false, A, decltype(mb)::value>), grid, dim3(kThreads), 0, stream,
+                           x, q, s, y, nullptr, (int)m, (int)n, (int)k, g, la);
+      });
+    });
+    return hipGetLastError();
+  }
+  if (ws == nullptr || ws_bytes < partial_bytes(p, m, n, 1)) return hipErrorInvalidValue;
+  float* const part = static_cast<float*>(ws);
+  with_rows(p.mb, [&](auto mb) {
+    hipLaunchKernelGGL((linear_act_kernel<true, kActNone, decltype(mb)::value>), grid, dim3(kThreads), 0, stream,
+                       x, q, s, y, part, (int)m, (int)n, (int)k, g, la);
   });
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch_join_layer(part, y, p.splits, m, n, ep, stream);
 }
 
 size_t glu_bytes(int64_t m, int64_t n, int64_t k) {
-  return m <= kSkinnyRows ? glu_skinny_bytes(m, n, k) : 0;
+  if (streams(kPair, m, 2 * n * k)) return glu_skinny_bytes(m, n, k);
+  return partial_bytes(plan_tiles(m, n, kBN / 2, steps_of(k), 2), m, n, 2);
 }
 
 hipError_t launch_glu(const uint16_t* x, const uint8_t* qg, const float* sg, const uint8_t* qu,
                       const float* su, uint16_t* h, const LayerEpilogue& ep, int64_t m, int64_t n,
                       int64_t k, void* ws, size_t ws_bytes, hipStream_t stream) {
-  if (m <= kSkinnyRows) return launch_glu_skinny(x, qg, sg, qu, su, h, ep, m, n, k, ws, ws_bytes, stream);
-  const int tiles_m = (int)((m + kBM - 1) / kBM), tiles_n = (int)((n + kBN / 2 - 1) / (kBN / 2));
-  const int units = tiles_m * tiles_n, grid = units < device_cus() ? units : device_cus();
+  if (streams(kPair, m, 2 * n * k)) return launch_glu_skinny(x, qg, sg, qu, su, h, ep, m, n, k, ws, ws_bytes, stream);
+  const LayerPlan p = plan_tiles(m, n, kBN / 2, steps_of(k), 2);
+  const Grid g = grid_of(p, m, n, kBN / 2, k);
   const LargeArgs la{ep, nullptr, 0, 0};
-  with_act(ep.act, [&](auto a) {
-    hipLaunchKernelGGL((glu_large_kernel<decltype(a)::value>), dim3((uint32_t)grid), dim3(kThreads), 0, stream,
-                       x, qg, sg, qu, su, h, (int)m, (int)n, (int)k, blocks_of(k), tiles_m, tiles_n,
-                       (int)((k + kBK - 1) / kBK), la);
+  const dim3 grid = blocks_for(p, g);
+  if (p.splits == 1) {
+    with_act(ep.act, [&](auto a) {
+      constexpr int A = decltype(a)::value;
+      with_rows(p.mb, [&](auto mb) {
+        hipLaunchKernelGGL((glu_kernel<false, A, decltype(mb)::value>), grid, dim3(kThreads), 0, stream, x, qg,
+                           sg, qu, su, h, nullptr, (int)m, (int)n, (int)k, g, la);
+      });
+    });
+    return hipGetLastError();
+  }
+  if (ws == nullptr || ws_bytes < partial_bytes(p, m, n, 2)) return hipErrorInvalidValue;
+  float* const part = static_cast<float*>(ws);
+  with_rows(p.mb, [&](auto mb) {
+    hipLaunchKernelGGL((glu_kernel<true, kActNone, decltype(mb)::value>), grid, dim3(kThreads), 0, stream, x, qg,
+                       sg, qu, su, h, part, (int)m, (int)n, (int)k, g, la);
   });
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch_join_glu(part, h, p.splits, m, n, ep, stream);
 }
 
 size_t input_gradient_bytes(int64_t m, int64_t n, int64_t k, int products) {
-  if (m <= kSkinnyRows) return input_gradient_skinny_bytes(m, n, k, products);
-  const LargePlan p = plan_gradient(m, n, k, products);
-  if (p.splits <= 1) return 0;
-  return round_up((size_t)p.splits * partial_slab(m, k) * sizeof(float), kWorkspaceAlign);
+  if (streams(kInputGradient, m, products * n * k)) return input_gradient_skinny_bytes(m, n, k, products);
+  return partial_bytes(plan_tiles(m, k, kBN, steps_of(n) * products, 1), m, k, 1);
 }
 
 hipError_t launch_input_gradient(const uint16_t* a, const uint8_t* q, const float* s, const uint16_t* a2,
                                  const uint8_t* q2, const float* s2, int64_t lda, uint16_t* dx,
                                  int64_t m, int64_t n, int64_t k, void* ws, size_t ws_bytes,
                                  hipStream_t stream) {
-  if (m <= kSkinnyRows)
+  if (streams(kInputGradient, m, (a2 ? 2 : 1) * n * k))
     return launch_input_gradient_skinny(a, q, s, a2, q2, s2, lda, dx, m, n, k, ws, ws_bytes, stream);
-  const int products = a2 ? 2 : 1;
-  const LargePlan p = plan_gradient(m, n, k, products);
-  const int tiles_m = (int)((m + kBM - 1) / kBM), tiles_c = (int)((k + kBN - 1) / kBN);
-  const int units = tiles_m * tiles_c * p.splits, grid = units < device_cus() ? units : device_cus();
+  const LayerPlan p = plan_tiles(m, k, kBN, steps_of(n) * (a2 ? 2 : 1), 1);
+  const Grid g = grid_of(p, m, k, kBN, k);
   LargeArgs la{};
   la.x2 = a2;
   la.ldx = (int)lda;
-  la.steps1 = (int)((n + kBK - 1) / kBK);
-  if (p.splits == 1) {
-    hipLaunchKernelGGL((input_gradient_kernel<false>), dim3((uint32_t)grid), dim3(kThreads), 0, stream, a, q, s,
-                       q2, s2, dx, nullptr, (int)m, (int)k, (int)n, blocks_of(k), tiles_m, tiles_c,
-                       p.kt_per_split, 1, la);
-    return hipGetLastError();
-  }
-  if (ws == nullptr || ws_bytes < input_gradient_bytes(m, n, k, products)) return hipErrorInvalidValue;
-  float* const part = static_cast<float*>(ws);
-  hipLaunchKernelGGL((input_gradient_kernel<true>), dim3((uint32_t)grid), dim3(kThreads), 0, stream, a, q, s, q2,
-                     s2, dx, part, (int)m, (int)k, (int)n, blocks_of(k), tiles_m, tiles_c, p.kt_per_split,
-                     p.splits, la);
+  la.steps1 = (int)steps_of(n);
+  const dim3 grid = blocks_for(p, g);
+  float* const part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
+  if (p.splits > 1 && (ws == nullptr || ws_bytes < partial_bytes(p, m, k, 1))) return hipErrorInvalidValue;
+  with_rows(p.mb, [&](auto mb) {
+    constexpr int MB = decltype(mb)::value;
+    if (part)
+      hipLaunchKernelGGL((input_gradient_kernel<true, MB>), grid, dim3(kThreads), 0, stream, a, q, s, q2, s2, dx,
+                         part, (int)m, (int)k, (int)n, g, la);
+    else
+      hipLaunchKernelGGL((input_gradient_kernel<false, MB>), grid, dim3(kThreads), 0, stream, a, q, s, q2, s2,
+                         dx, nullptr, (int)m, (int)k, (int)n, g, la);
+  });
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  return launch_reduce_partials(part, dx, p.splits, m, k, stream);
+  if (e != hipSuccess || !part) return e;
+  return launch_join_layer(part, dx, p.splits, m, k, LayerEpilogue{}, stream);
 }
 
 }  // namespace fp8bl

@@ -7,7 +7,7 @@ namespace fp8bl {
 namespace {
 
 template <int MT>
-__global__ __launch_bounds__(kWaves * 64)
+__global__ __launch_bounds__(kWaves * 64, 2)
 void linear_act_skinny_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ q,
                               const float* __restrict__ s, uint16_t* y, float* __restrict__ part, int M,
                               int N, int K, int gk, int ss_per_split, LayerEpilogue ep) {
@@ -16,7 +16,7 @@ void linear_act_skinny_kernel(const uint16_t* __restrict__ x, const uint8_t* __r
 }
 
 template <int MT>
-__global__ __launch_bounds__(kWaves * 64)
+__global__ __launch_bounds__(kWaves * 64, 2)
 void glu_skinny_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ qg,
                        const float* __restrict__ sg, const uint8_t* __restrict__ qu,
                        const float* __restrict__ su, uint16_t* h, float* __restrict__ part, int M, int N,
@@ -48,7 +48,7 @@ typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) i32x2* lds_i32x2_ptr_t;
 
 template <int MT>
-__global__ __launch_bounds__(kWaves * 64)
+__global__ __launch_bounds__(kWaves * 64, 2)
 void input_gradient_skinny_kernel(const uint16_t* __restrict__ a, const uint8_t* __restrict__ q,
                                   const float* __restrict__ s, const uint16_t* __restrict__ a2,
                                   const uint8_t* __restrict__ q2, const float* __restrict__ s2, int lda,
