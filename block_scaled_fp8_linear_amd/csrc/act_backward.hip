@@ -102,8 +102,16 @@ __global__ __launch_bounds__(kThreads)
 void column_sum_kernel(const float* __restrict__ part, float* __restrict__ out, int chunks, int64_t N) {
   const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (c >= N) return;
-  float t = 0.0f;
-  for (int i = 0; i < chunks; ++i) t += part[(int64_t)i * N + c];
+  float t = part[c];
+  int i = 1;
+  for (; i + 8 <= chunks; i += 8) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = part[(int64_t)(i + j) * N + c];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t += v[j];
+  }
+  for (; i < chunks; ++i) t += part[(int64_t)i * N + c];
   out[c] = t;
 }
 
@@ -160,14 +168,15 @@ constexpr int64_t kMaxBlocks = 1 << 22;   // threads of a launch stay below 2^32
 
 int64_t column_blocks(int64_t n, int vec) { return (n + kColThreads * vec - 1) / (kColThreads * vec); }
 
-// Rows per chunk: enough workgroups to fill the GPU (about four a CU), at
-// least 32 rows in a chunk and at most 256 chunks.
+// Rows per chunk: enough workgroups to fill the GPU (about eight a CU), at
+// most 256 chunks, and at least 128 rows in one, so that a short call needs no
+// second kernel for its column sums.
 int64_t chunk_rows(int64_t m, int64_t n) {
   const int64_t cols = column_blocks(n, n % 8 == 0 ? 8 : 1);
-  int64_t chunks = (1024 + cols - 1) / cols;
+  int64_t chunks = (2048 + cols - 1) / cols;
   if (chunks > 256) chunks = 256;
   int64_t rows = (m + chunks - 1) / chunks;
-  return rows < 32 ? 32 : rows;
+  return rows < 128 ? 128 : rows;
 }
 
 }  // namespace

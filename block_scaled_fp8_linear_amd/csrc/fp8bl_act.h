@@ -17,16 +17,41 @@ __device__ __forceinline__ float sigmoid_f32(float v) {
 
 constexpr float kTanhA2 = 1.59576912160573071f;       // 2 sqrt(2 / pi)
 constexpr float kTanhB = 0.044715f;
-constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+
+// The normal distribution's tail Phi(-a), a >= 0, with e = e^(-a^2/2):
+// Phi(-a) e^(a^2/2) is smooth and slowly varying, here a polynomial of degree
+// 7 in 1 / (1 + 0.35 a), fitted by reweighted least squares to the smallest
+// largest relative error on 0 <= a <= 14.5 (beyond, e is 0): 3.2e-7, 5.6e-7
+// evaluated in fp32. About 14 instructions with no branch; the library's erfcf
+// took 150 us of 894 us in the epilogue of 8192 x 12288 x 4096. It keeps its
+// relative precision where Phi is small, as (1 + erf) / 2 would not.
+__device__ __forceinline__ float normal_tail(float a, float& e) {
+  e = __builtin_amdgcn_exp2f(a * a * (-0.5f * 1.44269504088896341f));
+  const float s = __builtin_amdgcn_rcpf(__builtin_fmaf(0.35f, a, 1.0f));
+  float p = 0.04890687018632889f;
+  p = __builtin_fmaf(p, s, -0.2019839733839035f);
+  p = __builtin_fmaf(p, s, 0.2404298037290573f);
+  p = __builtin_fmaf(p, s, -0.016849324107170105f);
+  p = __builtin_fmaf(p, s, 0.15587973594665527f);
+  p = __builtin_fmaf(p, s, 0.1333768665790558f);
+  p = __builtin_fmaf(p, s, 0.14026731252670288f);
+  p = __builtin_fmaf(p, s, -2.7144789783051237e-05f);
+  return e * p;
+}
+__device__ __forceinline__ float normal_cdf(float t, float& e) {
+  const float tail = normal_tail(fabsf(t), e);
+  return t < 0.0f ? tail : 1.0f - tail;
+}
 
 template <int ACT>
 __device__ __forceinline__ float act_f32(float t) {
   if constexpr (ACT == kActRelu) return t > 0.0f ? t : (t != t ? t : 0.0f);
   if constexpr (ACT == kActSilu) return t * sigmoid_f32(t);
-  // Phi(t) = erfc(-t / sqrt 2) / 2 keeps its relative precision where Phi is
-  // small; (1 + erf) / 2 would cancel there.
-  if constexpr (ACT == kActGelu) return 0.5f * t * erfcf(-kSqrtHalf * t);
+  if constexpr (ACT == kActGelu) {
+    float e;
+    return t * normal_cdf(t, e);
+  }
   if constexpr (ACT == kActGeluTanh) return t * sigmoid_f32(kTanhA2 * (t + kTanhB * t * t * t));
   return t;
 }
@@ -38,9 +63,11 @@ __device__ __forceinline__ float act_grad_f32(float t) {
     const float p = sigmoid_f32(t);
     return p * (1.0f + t * (1.0f - p));
   }
-  if constexpr (ACT == kActGelu)
-    return 0.5f * erfcf(-kSqrtHalf * t) +
-           t * (kInvSqrt2Pi * __builtin_amdgcn_exp2f(t * t * (-0.5f * 1.44269504088896341f)));
+  if constexpr (ACT == kActGelu) {
+    float e;
+    const float c = normal_cdf(t, e);
+    return c + t * (kInvSqrt2Pi * e);
+  }
   if constexpr (ACT == kActGeluTanh) {
     // Past |t| = 30 the derivative is 0 or 1 in fp32; the clamp keeps t^2
     // finite there (0 * inf otherwise).

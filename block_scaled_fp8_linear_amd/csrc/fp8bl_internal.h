@@ -123,8 +123,8 @@ hipError_t launch_input_gradient(const uint16_t* a, const uint8_t* q, const floa
                                  int64_t m, int64_t n, int64_t k, void* ws, size_t ws_bytes,
                                  hipStream_t stream);
 // The three at few rows (m <= 32), and joins of split partials (slab stride
-// partial_slab(m, n)) with an epilogue; the pair's partials alternate gate and
-// up slabs.
+// partial_slab(m, n)) with an epilogue, over columns c0 .. n; the pair's
+// partials alternate gate and up slabs.
 size_t linear_act_skinny_bytes(int64_t m, int64_t n, int64_t k);
 hipError_t launch_linear_act_skinny(const uint16_t* x, const uint8_t* q, const float* s, uint16_t* y,
                                     const LayerEpilogue& ep, int64_t m, int64_t n, int64_t k, void* ws,
@@ -138,9 +138,9 @@ hipError_t launch_input_gradient_skinny(const uint16_t* a, const uint8_t* q, con
                                         const uint16_t* a2, const uint8_t* q2, const float* s2, int64_t lda,
                                         uint16_t* dx, int64_t m, int64_t n, int64_t k, void* ws,
                                         size_t ws_bytes, hipStream_t stream);
-hipError_t launch_join_layer(const float* part, uint16_t* y, int splits, int64_t m, int64_t n,
+hipError_t launch_join_layer(const float* part, uint16_t* y, int splits, int64_t m, int64_t n, int64_t c0,
                              const LayerEpilogue& ep, hipStream_t stream);
-hipError_t launch_join_glu(const float* part, uint16_t* h, int splits, int64_t m, int64_t n,
+hipError_t launch_join_glu(const float* part, uint16_t* h, int splits, int64_t m, int64_t n, int64_t c0,
                            const LayerEpilogue& ep, hipStream_t stream);
 // Elementwise gradients. `pad`: a copy with rows of ld elements for the
 // product above (null where n % 8 == 0 and the gradient itself serves).

@@ -64,6 +64,7 @@ struct LargeArgs {
   const uint16_t* x2;        // kGradient: the second product's left operand
   int ldx;                   // kGradient: row stride of x and x2, elements (a multiple of 8)
   int steps1;                // kGradient: steps of one product
+  int tile0;                 // first tile column of the launch (tiles_n counts from it)
 };
 
 // (q, s) is the weight; for GATED and kGlu it is the gate weight and (q2, s2)
@@ -77,7 +78,7 @@ template <bool SPLIT, bool GATED, Form FORM, int ACT, int MB = 8, int STAGES = 3
 __device__ __forceinline__
 void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__ q,
                      const float* __restrict__ s, const uint8_t* __restrict__ q2,
-                     const float* __restrict__ s2, uint16_t* __restrict__ y,
+                     const float* __restrict__ s2, uint16_t* y,
                      float* __restrict__ part, int M, int N, int K, int gk,
                      int tiles_m, int tiles_n, int kt_per_split, int splits, int steps_per_unit,
                      const LargeArgs& la) {
@@ -133,7 +134,7 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
     const int gsize = min(tiles_m - first_m, GM);
     const int in_group = id - group * GM * tiles_n;
     U.m0 = (first_m + in_group % gsize) * kTileM;
-    U.n0 = (in_group / gsize) * kTileN;
+    U.n0 = (in_group / gsize + (FORM == kPlain ? 0 : la.tile0)) * kTileN;
     U.kt0 = U.split * kt_per_split;
     U.nreal = min(kt_per_split, nkt - U.kt0);
     return U;

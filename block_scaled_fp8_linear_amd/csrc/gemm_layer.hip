@@ -110,10 +110,38 @@ LayerPlan plan_tiles(int64_t m, int64_t n, int cols, int64_t steps, int words) {
   return best;
 }
 
-Grid grid_of(const LayerPlan& p, int64_t m, int64_t n, int cols, int64_t k) {
+// A product as one or two launches over tile columns: where the tiles are a
+// little more than whole rounds of the chip, the whole rounds run unsplit and
+// only the columns left over are split (4096 x 12800 x 5120 backward, 320
+// tiles: 256 unsplit and 64 in four instead of all 320 in four).
+struct Part {
+  int tile0, tiles_n;       // tile columns
+  LayerPlan plan;
+};
+struct ProductPlan {
+  int parts;
+  Part part[2];
+};
+ProductPlan plan_product(int64_t m, int64_t n, int cols, int64_t steps, int words) {
+  const int tn = (int)((n + cols - 1) / cols);
+  ProductPlan best{1, {{0, tn, plan_tiles(m, n, cols, steps, words)}, {}}};
+  const TileCost& t = kTileCosts[0];
+  const int64_t tm = (m + 32 * t.mb - 1) / (32 * t.mb);
+  const int64_t rounds = tm * tn / t.slots, head = rounds * t.slots / tm;   // head: tile columns
+  if (rounds > 0 && head < tn) {
+    const LayerPlan h{t.mb, 1, (int)steps, t.fixed + (double)rounds * (steps * t.step_full + t.unit)};
+    const LayerPlan r = plan_tiles(m, n - head * cols, cols, steps, words);
+    if (h.cost + r.cost < 0.98 * best.part[0].plan.cost)
+      best = ProductPlan{2, {{0, (int)head, h}, {(int)head, (int)(tn - head), r}}};
+  }
+  return best;
+}
+
+Grid grid_of(const Part& part, int64_t m, int64_t k) {
+  const LayerPlan& p = part.plan;
   const int stages = p.mb == 4 ? Tile<4>::kStages : Tile<8>::kStages;
   static_assert(Tile<8>::kStages == Tile<2>::kStages, "two ring lengths");
-  return Grid{blocks_of(k), (int)((m + 32 * p.mb - 1) / (32 * p.mb)), (int)((n + cols - 1) / cols),
+  return Grid{blocks_of(k), (int)((m + 32 * p.mb - 1) / (32 * p.mb)), part.tiles_n,
               p.steps_per_split, p.splits, p.steps_per_split > stages - 1 ? p.steps_per_split : stages - 1};
 }
 
@@ -136,8 +164,27 @@ void with_rows(int mb, F&& f) {
   else f(Const<2>{});
 }
 
-size_t partial_bytes(const LayerPlan& p, int64_t m, int64_t n, int words) {
-  return p.splits <= 1 ? 0 : round_up((size_t)p.splits * words * partial_slab(m, n) * sizeof(float), kWorkspaceAlign);
+// Workspace: split partials of [m, n] (one part at most is split).
+size_t partial_bytes(const ProductPlan& p, int64_t m, int64_t n, int words) {
+  const int splits = p.part[p.parts - 1].plan.splits;
+  return splits <= 1 ? 0 : round_up((size_t)splits * words * partial_slab(m, n) * sizeof(float), kWorkspaceAlign);
+}
+
+// Runs a plan: `product(part, grid, partials or null)` launches one part,
+// `join(splits, partials, first column)` joins it where it is split.
+template <typename Launch, typename Join>
+hipError_t run_parts(const ProductPlan& p, int64_t m, int64_t k, int cols, size_t need, void* ws,
+                     size_t ws_bytes, Launch&& product, Join&& join) {
+  if (need > 0 && (ws == nullptr || ws_bytes < need)) return hipErrorInvalidValue;
+  for (int i = 0; i < p.parts; ++i) {
+    const Part& part = p.part[i];
+    float* const partials = part.plan.splits > 1 ? static_cast<float*>(ws) : nullptr;
+    product(part, grid_of(part, m, k), partials);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && partials) e = join(part.plan.splits, partials, (int64_t)part.tile0 * cols);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 int64_t steps_of(int64_t r) { return (r + kBK - 1) / kBK; }
@@ -168,104 +215,101 @@ bool streams(Product p, int64_t m, int64_t codes) {
 
 size_t linear_act_bytes(int64_t m, int64_t n, int64_t k) {
   if (streams(kLinear, m, n * k)) return linear_act_skinny_bytes(m, n, k);
-  return partial_bytes(plan_tiles(m, n, kBN, steps_of(k), 1), m, n, 1);
+  return partial_bytes(plan_product(m, n, kBN, steps_of(k), 1), m, n, 1);
 }
 
 hipError_t launch_linear_act(const uint16_t* x, const uint8_t* q, const float* s, uint16_t* y,
                              const LayerEpilogue& ep, int64_t m, int64_t n, int64_t k, void* ws,
                              size_t ws_bytes, hipStream_t stream) {
   if (streams(kLinear, m, n * k)) return launch_linear_act_skinny(x, q, s, y, ep, m, n, k, ws, ws_bytes, stream);
-  const LayerPlan p = plan_tiles(m, n, kBN, steps_of(k), 1);
-  const Grid g = grid_of(p, m, n, kBN, k);
-  const LargeArgs la{ep, nullptr, 0, 0};
-  const dim3 grid = blocks_for(p, g);
-  if (p.splits == 1) {
-    with_act(ep.act, [&](auto a) {
-      constexpr int A = decltype(a)::value;
-      with_rows(p.mb, [&](auto mb) {
-        hipLaunchKernelGGL((linear_act_kernel<false, A, decltype(mb)::value>), grid, dim3(kThreads), 0, stream,
-                           x, q, s, y, nullptr, (int)m, (int)n, (int)k, g, la);
+  const ProductPlan p = plan_product(m, n, kBN, steps_of(k), 1);
+  return run_parts(
+      p, m, k, kBN, partial_bytes(p, m, n, 1), ws, ws_bytes,
+      [&](const Part& part, const Grid& g, float* partials) {
+        const LargeArgs la{ep, nullptr, 0, 0, part.tile0};
+        const dim3 grid = blocks_for(part.plan, g);
+        with_rows(part.plan.mb, [&](auto rows) {
+          constexpr int MB = decltype(rows)::value;
+          if (partials) {
+            hipLaunchKernelGGL((linear_act_kernel<true, kActNone, MB>), grid, dim3(kThreads), 0, stream, x, q, s,
+                               y, partials, (int)m, (int)n, (int)k, g, la);
+            return;
+          }
+          with_act(ep.act, [&](auto a) {
+            hipLaunchKernelGGL((linear_act_kernel<false, decltype(a)::value, MB>), grid, dim3(kThreads), 0, stream,
+                               x, q, s, y, nullptr, (int)m, (int)n, (int)k, g, la);
+          });
+        });
+      },
+      [&](int splits, const float* partials, int64_t c0) {
+        return launch_join_layer(partials, y, splits, m, n, c0, ep, stream);
       });
-    });
-    return hipGetLastError();
-  }
-  if (ws == nullptr || ws_bytes < partial_bytes(p, m, n, 1)) return hipErrorInvalidValue;
-  float* const part = static_cast<float*>(ws);
-  with_rows(p.mb, [&](auto mb) {
-    hipLaunchKernelGGL((linear_act_kernel<true, kActNone, decltype(mb)::value>), grid, dim3(kThreads), 0, stream,
-                       x, q, s, y, part, (int)m, (int)n, (int)k, g, la);
-  });
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  return launch_join_layer(part, y, p.splits, m, n, ep, stream);
 }
 
 size_t glu_bytes(int64_t m, int64_t n, int64_t k) {
   if (streams(kPair, m, 2 * n * k)) return glu_skinny_bytes(m, n, k);
-  return partial_bytes(plan_tiles(m, n, kBN / 2, steps_of(k), 2), m, n, 2);
+  return partial_bytes(plan_product(m, n, kBN / 2, steps_of(k), 2), m, n, 2);
 }
 
 hipError_t launch_glu(const uint16_t* x, const uint8_t* qg, const float* sg, const uint8_t* qu,
                       const float* su, uint16_t* h, const LayerEpilogue& ep, int64_t m, int64_t n,
                       int64_t k, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (streams(kPair, m, 2 * n * k)) return launch_glu_skinny(x, qg, sg, qu, su, h, ep, m, n, k, ws, ws_bytes, stream);
-  const LayerPlan p = plan_tiles(m, n, kBN / 2, steps_of(k), 2);
-  const Grid g = grid_of(p, m, n, kBN / 2, k);
-  const LargeArgs la{ep, nullptr, 0, 0};
-  const dim3 grid = blocks_for(p, g);
-  if (p.splits == 1) {
-    with_act(ep.act, [&](auto a) {
-      constexpr int A = decltype(a)::value;
-      with_rows(p.mb, [&](auto mb) {
-        hipLaunchKernelGGL((glu_kernel<false, A, decltype(mb)::value>), grid, dim3(kThreads), 0, stream, x, qg,
-                           sg, qu, su, h, nullptr, (int)m, (int)n, (int)k, g, la);
+  const ProductPlan p = plan_product(m, n, kBN / 2, steps_of(k), 2);
+  return run_parts(
+      p, m, k, kBN / 2, partial_bytes(p, m, n, 2), ws, ws_bytes,
+      [&](const Part& part, const Grid& g, float* partials) {
+        const LargeArgs la{ep, nullptr, 0, 0, part.tile0};
+        const dim3 grid = blocks_for(part.plan, g);
+        with_rows(part.plan.mb, [&](auto rows) {
+          constexpr int MB = decltype(rows)::value;
+          if (partials) {
+            hipLaunchKernelGGL((glu_kernel<true, kActNone, MB>), grid, dim3(kThreads), 0, stream, x, qg, sg, qu,
+                               su, h, partials, (int)m, (int)n, (int)k, g, la);
+            return;
+          }
+          with_act(ep.act, [&](auto a) {
+            hipLaunchKernelGGL((glu_kernel<false, decltype(a)::value, MB>), grid, dim3(kThreads), 0, stream, x, qg,
+                               sg, qu, su, h, nullptr, (int)m, (int)n, (int)k, g, la);
+          });
+        });
+      },
+      [&](int splits, const float* partials, int64_t c0) {
+        return launch_join_glu(partials, h, splits, m, n, c0, ep, stream);
       });
-    });
-    return hipGetLastError();
-  }
-  if (ws == nullptr || ws_bytes < partial_bytes(p, m, n, 2)) return hipErrorInvalidValue;
-  float* const part = static_cast<float*>(ws);
-  with_rows(p.mb, [&](auto mb) {
-    hipLaunchKernelGGL((glu_kernel<true, kActNone, decltype(mb)::value>), grid, dim3(kThreads), 0, stream, x, qg,
-                       sg, qu, su, h, part, (int)m, (int)n, (int)k, g, la);
-  });
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  return launch_join_glu(part, h, p.splits, m, n, ep, stream);
 }
 
 size_t input_gradient_bytes(int64_t m, int64_t n, int64_t k, int products) {
   if (streams(kInputGradient, m, products * n * k)) return input_gradient_skinny_bytes(m, n, k, products);
-  return partial_bytes(plan_tiles(m, k, kBN, steps_of(n) * products, 1), m, k, 1);
+  return partial_bytes(plan_product(m, k, kBN, steps_of(n) * products, 1), m, k, 1);
 }
 
 hipError_t launch_input_gradient(const uint16_t* a, const uint8_t* q, const float* s, const uint16_t* a2,
                                  const uint8_t* q2, const float* s2, int64_t lda, uint16_t* dx,
                                  int64_t m, int64_t n, int64_t k, void* ws, size_t ws_bytes,
                                  hipStream_t stream) {
-  if (streams(kInputGradient, m, (a2 ? 2 : 1) * n * k))
+  const int products = a2 ? 2 : 1;
+  if (streams(kInputGradient, m, products * n * k))
     return launch_input_gradient_skinny(a, q, s, a2, q2, s2, lda, dx, m, n, k, ws, ws_bytes, stream);
-  const LayerPlan p = plan_tiles(m, k, kBN, steps_of(n) * (a2 ? 2 : 1), 1);
-  const Grid g = grid_of(p, m, k, kBN, k);
-  LargeArgs la{};
-  la.x2 = a2;
-  la.ldx = (int)lda;
-  la.steps1 = (int)steps_of(n);
-  const dim3 grid = blocks_for(p, g);
-  float* const part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
-  if (p.splits > 1 && (ws == nullptr || ws_bytes < partial_bytes(p, m, k, 1))) return hipErrorInvalidValue;
-  with_rows(p.mb, [&](auto mb) {
-    constexpr int MB = decltype(mb)::value;
-    if (part)
-      hipLaunchKernelGGL((input_gradient_kernel<true, MB>), grid, dim3(kThreads), 0, stream, a, q, s, q2, s2, dx,
-                         part, (int)m, (int)k, (int)n, g, la);
-    else
-      hipLaunchKernelGGL((input_gradient_kernel<false, MB>), grid, dim3(kThreads), 0, stream, a, q, s, q2, s2,
-                         dx, nullptr, (int)m, (int)k, (int)n, g, la);
-  });
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !part) return e;
-  return launch_join_layer(part, dx, p.splits, m, k, LayerEpilogue{}, stream);
+  const ProductPlan p = plan_product(m, k, kBN, steps_of(n) * products, 1);
+  return run_parts(
+      p, m, k, kBN, partial_bytes(p, m, k, 1), ws, ws_bytes,
+      [&](const Part& part, const Grid& g, float* partials) {
+        const LargeArgs la{LayerEpilogue{}, a2, (int)lda, (int)steps_of(n), part.tile0};
+        const dim3 grid = blocks_for(part.plan, g);
+        with_rows(part.plan.mb, [&](auto rows) {
+          constexpr int MB = decltype(rows)::value;
+          if (partials)
+            hipLaunchKernelGGL((input_gradient_kernel<true, MB>), grid, dim3(kThreads), 0, stream, a, q, s, q2, s2,
+                               dx, partials, (int)m, (int)k, (int)n, g, la);
+          else
+            hipLaunchKernelGGL((input_gradient_kernel<false, MB>), grid, dim3(kThreads), 0, stream, a, q, s, q2,
+                               s2, dx, nullptr, (int)m, (int)k, (int)n, g, la);
+        });
+      },
+      [&](int splits, const float* partials, int64_t c0) {
+        return launch_join_layer(partials, dx, splits, m, k, c0, LayerEpilogue{}, stream);
+      });
 }
 
 }  // namespace fp8bl

@@ -248,7 +248,7 @@ hipError_t launch_linear_act_skinny(const uint16_t* x, const uint8_t* q, const f
                        (int)k, gk, p.ss_per_split, ep);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  return launch_join_layer(part, y, p.splits, m, n, ep, stream);
+  return launch_join_layer(part, y, p.splits, m, n, 0, ep, stream);
 }
 
 size_t glu_skinny_bytes(int64_t m, int64_t n, int64_t k) {
@@ -272,7 +272,7 @@ hipError_t launch_glu_skinny(const uint16_t* x, const uint8_t* qg, const float* 
                        (int)n, (int)k, gk, p.ss_per_split, ep);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  return launch_join_glu(part, h, p.splits, m, n, ep, stream);
+  return launch_join_glu(part, h, p.splits, m, n, 0, ep, stream);
 }
 
 size_t input_gradient_skinny_bytes(int64_t m, int64_t n, int64_t k, int products) {
@@ -301,7 +301,7 @@ hipError_t launch_input_gradient_skinny(const uint16_t* a, const uint8_t* q, con
                        dx, part, (int)m, (int)k, (int)n, gk, p.strips, p.steps1, p.steps, p.steps_per_split);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  return launch_join_layer(part, dx, p.splits, m, k, LayerEpilogue{}, stream);
+  return launch_join_layer(part, dx, p.splits, m, k, 0, LayerEpilogue{}, stream);
 }
 
 }  // namespace fp8bl

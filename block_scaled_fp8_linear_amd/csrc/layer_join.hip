@@ -95,12 +95,18 @@ __device__ __forceinline__ Row<VEC> sum_splits(const float* p, size_t stride, in
   return t;
 }
 
+// Columns c0 .. n of every row (`count` outputs; width n - c0).
 template <int ACT, int VEC, bool GLU>
 __global__ __launch_bounds__(kThreads)
-void join_kernel(const float* __restrict__ part, uint16_t* y, int splits, size_t mn, size_t slab,
-                 uint32_t n, LayerEpilogue ep) {
-  for (size_t i = ((size_t)blockIdx.x * kThreads + threadIdx.x) * VEC; i < mn;
-       i += (size_t)gridDim.x * kThreads * VEC) {
+void join_kernel(const float* __restrict__ part, uint16_t* y, int splits, size_t count, size_t slab,
+                 uint32_t n, uint32_t c0, LayerEpilogue ep) {
+  const uint32_t width = n - c0;
+  for (size_t f = ((size_t)blockIdx.x * kThreads + threadIdx.x) * VEC; f < count;
+       f += (size_t)gridDim.x * kThreads * VEC) {
+    // (64-bit divisions only where 32 bits do not hold the count)
+    const size_t row = count >> 32 ? f / width : (uint32_t)f / width;
+    const uint32_t col = c0 + (uint32_t)(f - row * width);
+    const size_t i = row * n + col;
     if constexpr (GLU) {
       const Row<VEC> g = sum_splits<VEC>(part + i, 2 * slab, splits);
       const Row<VEC> u = sum_splits<VEC>(part + slab + i, 2 * slab, splits);
@@ -117,7 +123,7 @@ void join_kernel(const float* __restrict__ part, uint16_t* y, int splits, size_t
       if (ep.residual) res = load_bf16<VEC>(ep.residual + i);
       Row<VEC> t = sum_splits<VEC>(part + i, slab, splits);
       if (ep.bias) {
-        const Row<VEC> b = load_bf16<VEC>(ep.bias + (uint32_t)(i % n));
+        const Row<VEC> b = load_bf16<VEC>(ep.bias + col);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) t.v[e] += b.v[e];
       }
@@ -134,36 +140,37 @@ void join_kernel(const float* __restrict__ part, uint16_t* y, int splits, size_t
 }
 
 template <int VEC, bool GLU>
-hipError_t launch(const float* part, uint16_t* y, int splits, int64_t m, int64_t n, const LayerEpilogue& ep,
-                  hipStream_t stream) {
-  const size_t mn = (size_t)m * n, blocks = (mn + kThreads * VEC - 1) / (kThreads * VEC);
+hipError_t launch(const float* part, uint16_t* y, int splits, int64_t m, int64_t n, int64_t c0,
+                  const LayerEpilogue& ep, hipStream_t stream) {
+  const size_t count = (size_t)m * (n - c0), blocks = (count + kThreads * VEC - 1) / (kThreads * VEC);
   const dim3 grid((uint32_t)(blocks < (1u << 20) ? blocks : (1u << 20)));
   with_act(ep.act, [&](auto a) {
     hipLaunchKernelGGL((join_kernel<decltype(a)::value, VEC, GLU>), grid, dim3(kThreads), 0, stream, part, y,
-                       splits, mn, partial_slab((size_t)m, (size_t)n), (uint32_t)n, ep);
+                       splits, count, partial_slab((size_t)m, (size_t)n), (uint32_t)n, (uint32_t)c0, ep);
   });
   return hipGetLastError();
 }
 
 // Four outputs a thread where rows are whole quads and there are enough of
 // them for every CU (2^18 outputs are 256 workgroups of quads), else one.
+// (c0 is a multiple of 128.)
 template <bool GLU>
-hipError_t join(const float* part, uint16_t* y, int splits, int64_t m, int64_t n, const LayerEpilogue& ep,
-                hipStream_t stream) {
-  if (n % 4 == 0 && m * n >= (1 << 18)) return launch<4, GLU>(part, y, splits, m, n, ep, stream);
-  return launch<1, GLU>(part, y, splits, m, n, ep, stream);
+hipError_t join(const float* part, uint16_t* y, int splits, int64_t m, int64_t n, int64_t c0,
+                const LayerEpilogue& ep, hipStream_t stream) {
+  if (n % 4 == 0 && m * (n - c0) >= (1 << 18)) return launch<4, GLU>(part, y, splits, m, n, c0, ep, stream);
+  return launch<1, GLU>(part, y, splits, m, n, c0, ep, stream);
 }
 
 }  // namespace
 
-hipError_t launch_join_layer(const float* part, uint16_t* y, int splits, int64_t m, int64_t n,
+hipError_t launch_join_layer(const float* part, uint16_t* y, int splits, int64_t m, int64_t n, int64_t c0,
                              const LayerEpilogue& ep, hipStream_t stream) {
-  return join<false>(part, y, splits, m, n, ep, stream);
+  return join<false>(part, y, splits, m, n, c0, ep, stream);
 }
 
-hipError_t launch_join_glu(const float* part, uint16_t* h, int splits, int64_t m, int64_t n,
+hipError_t launch_join_glu(const float* part, uint16_t* h, int splits, int64_t m, int64_t n, int64_t c0,
                            const LayerEpilogue& ep, hipStream_t stream) {
-  return join<true>(part, h, splits, m, n, ep, stream);
+  return join<true>(part, h, splits, m, n, c0, ep, stream);
 }
 
 }  // namespace fp8bl

@@ -119,6 +119,65 @@ def test_glu_backward(shape):
         R.check_glu_backward(dh, g, u, qg, sg, qu, su, act, dx, dg, du, f"{shape} {act}")
 
 
+# Sizes whose tiles fill the chip: workgroups that walk several units, 256-row
+# tiles with and without K splits, and plans that run whole rounds unsplit and
+# the tile columns left over in splits. Compared in full.
+LARGE = [
+    (2304, 8200, 4112),     # 9 x 33 tiles of 256 rows, a ragged last column tile, 65 K steps
+    (700, 5120, 2576),      # row tiles partly filled
+    (4100, 1300, 400),      # many row tiles, few steps
+    (520, 10001, 1552),     # rows of odd length
+]
+
+
+@pytest.mark.parametrize("shape", LARGE, ids=["x".join(map(str, s)) for s in LARGE])
+def test_large(shape):
+    m, n, k = shape
+    gen = torch.Generator().manual_seed(n + k)
+    x, (qg, sg), (qu, su) = normal(gen, m, k), weight(gen, n, k, std=0.02), weight(gen, n, k, std=0.02)
+    dy, bias = normal(gen, m, n), normal(gen, n)
+    z, g, u = (torch.empty_like(dy) for _ in range(3))
+    dbias = torch.empty(n, device="cuda")
+    say("large linear", shape)
+    y = F.fp8_block_linear_act(x, qg, sg, bias=bias, residual=dy, act=F.ACT_GELU, z=z)
+    torch.cuda.synchronize()
+    R.check_linear_act(x, qg, sg, bias, dy, "gelu", y, z, f"{shape}")
+    say("large glu", shape)
+    h = F.fp8_block_glu(x, qg, sg, qu, su, g=g, u=u)
+    torch.cuda.synchronize()
+    R.check_glu(x, qg, sg, qu, su, "silu", h, g, u, f"{shape}")
+    say("large linear backward", shape)
+    dx, dz = F.fp8_block_linear_act_backward(dy, qg, sg, z=z, act=F.ACT_GELU_TANH, dbias=dbias)
+    torch.cuda.synchronize()
+    R.check_linear_act_backward(dy, z, qg, sg, "gelu_tanh", dx, dz, dbias, f"{shape}")
+    say("large glu backward", shape)
+    dx, dg, du = F.fp8_block_glu_backward(dy, g, u, qg, sg, qu, su)
+    torch.cuda.synchronize()
+    R.check_glu_backward(dy, g, u, qg, sg, qu, su, "silu", dx, dg, du, f"{shape}")
+
+
+def test_large_columns_left_over():
+    """The input gradient over 8448 columns (8 x 33 tiles, 33 columns of tiles
+    being one more than whole rounds hold) and its join beside columns that
+    are not split; the same for the forward over as many weight rows."""
+    m, n, k = 2048, 4096, 8448
+    gen = torch.Generator().manual_seed(4)
+    q, s = weight(gen, n, k, std=0.02)
+    dy = normal(gen, m, n)
+    assert F.layer_workspace_size("linear_act_backward", m, n, k) > 0
+    say("columns left over, gradient")
+    dx, _ = F.fp8_block_linear_act_backward(dy, q, s)
+    torch.cuda.synchronize()
+    R.check_linear_act_backward(dy, None, q, s, "none", dx, dy, None, "left over")
+    m, n, k = 2048, 8448, 4096
+    x, (q, s), res = normal(gen, m, k), weight(gen, n, k, std=0.02), normal(gen, m, n)
+    assert F.layer_workspace_size("linear_act", m, n, k) > 0
+    say("columns left over, forward")
+    y = F.fp8_block_linear_act(x, q, s, residual=res, act=F.ACT_SILU)
+    torch.cuda.synchronize()
+    R.check_linear_act(x, q, s, None, res, "silu", y, None, "left over")
+
+
 @pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
 def test_activation_values(act):
     """Each activation and derivative over the whole range of bf16: z walks
