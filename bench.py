@@ -76,8 +76,8 @@ KERNEL_SOURCES = {
     "gemm_tiled_kernel": ("gemm_tiled.hip",),
     "gemm_gated_kernel": ("gemm_tiled.hip",),
     "gemm_gated_paired_kernel": ("gemm_tiled.hip",),
-    "gemm_large_kernel": ("gemm_large.hip",),
-    "gemm_skinny_kernel": ("gemm_skinny.hip",),
+    "gemm_large_kernel": ("gemm_large.hip", "gemm_large_body.h", "fp8bl_act.h"),
+    "gemm_skinny_kernel": ("gemm_skinny.hip", "gemm_skinny_body.h", "fp8bl_act.h"),
     "reduce_partials_kernel": ("gemm_skinny.hip",),
     "dequant_kernel": ("dequant.hip",),
     "quantize_kernel": ("quantize.hip",),
@@ -85,8 +85,20 @@ KERNEL_SOURCES = {
     "gemm_w8a8_kernel": ("gemm_w8a8.hip",),
     "gemm_w8a8_large_kernel": ("gemm_w8a8_large.hip",),
     "stream_read_kernel": ("stream_read.hip",),
+    # the layer operators
+    "linear_act_kernel": ("fp8bl_layers.hip", "gemm_layer.hip", "gemm_large_body.h", "fp8bl_act.h"),
+    "glu_kernel": ("fp8bl_layers.hip", "gemm_layer.hip", "gemm_large_body.h", "fp8bl_act.h"),
+    "input_gradient_kernel": ("fp8bl_layers.hip", "gemm_layer.hip", "gemm_large_body.h", "fp8bl_act.h"),
+    "linear_act_skinny_kernel": ("fp8bl_layers.hip", "gemm_layer_skinny.hip", "gemm_skinny_body.h", "fp8bl_act.h"),
+    "glu_skinny_kernel": ("fp8bl_layers.hip", "gemm_layer_skinny.hip", "gemm_skinny_body.h", "fp8bl_act.h"),
+    "input_gradient_skinny_kernel": ("fp8bl_layers.hip", "gemm_layer_skinny.hip", "gemm_skinny_body.h",
+                                     "fp8bl_act.h"),
+    "join_kernel": ("layer_join.hip", "fp8bl_act.h"),
+    "act_backward_kernel": ("act_backward.hip", "fp8bl_act.h"),
+    "glu_backward_kernel": ("act_backward.hip", "fp8bl_act.h"),
+    "column_sum_kernel": ("act_backward.hip", "fp8bl_act.h"),
 }
-SHARED_SOURCES = ("fp8bl_api.hip", "fp8bl_device.h", "fp8bl_internal.h")
+SHARED_SOURCES = ("fp8bl_api.hip", "fp8bl_checks.h", "fp8bl_device.h", "fp8bl_internal.h")
 
 
 def code_only(src):

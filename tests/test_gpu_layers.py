@@ -420,6 +420,119 @@ def test_feed_forward_block_and_its_gradient(m):
         assert abs(got - want) <= 7 * R.HALF * 6 * norm, (i, got, want, norm)
 
 
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own (implicit) workspace, overlap
+    without touching each other: several rounds against results alone."""
+    gen = torch.Generator().manual_seed(12)
+    (qg, sg), (qu, su) = weight(gen, 1032, 2064), weight(gen, 1032, 2064)
+    xs = [normal(gen, m, 2064) for m in (70, 200)]
+    dys = [normal(gen, m, 1032) for m in (70, 200)]
+
+    def step(i):
+        g, u = torch.empty_like(dys[i]), torch.empty_like(dys[i])
+        h = F.fp8_block_glu(xs[i], qg, sg, qu, su, g=g, u=u)
+        y = F.fp8_block_linear_act(xs[i], qg, sg, residual=h, act=F.ACT_GELU)
+        return (h, y) + F.fp8_block_glu_backward(dys[i], g, u, qg, sg, qu, su)
+
+    say("two streams")
+    alone = [step(0), step(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = []
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got.append(step(i))
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert all(torch.equal(p, r) for p, r in zip(a, b))
+
+
+@pytest.mark.parametrize("n", [32776, 32771])
+def test_offsets_past_32_bits(n):
+    """Arrays of more than 2^32 bytes (and 2^31 elements), rows of whole
+    chunks and of odd length: rows at both ends and around 2^31 bytes and
+    elements against the formulas, and the column sums in full."""
+    m, k = 67000, 64
+    gen = torch.Generator().manual_seed(n)
+    (qg, sg), (qu, su) = weight(gen, n, k), weight(gen, n, k)
+    x = normal(gen, m, k)
+    rows = sorted({0, 1, 255, 256, (1 << 30) // n, (1 << 30) // n + 1, (1 << 31) // n, (1 << 31) // n + 1, m - 2, m - 1})
+    at = torch.tensor(rows, device="cuda")
+    z, g, u = (torch.empty(m, n, dtype=BF, device="cuda") for _ in range(3))
+    say("past 32 bits", n, "forward")
+    y = F.fp8_block_linear_act(x, qg, sg, act=F.ACT_SILU, z=z)
+    h = F.fp8_block_glu(x, qg, sg, qu, su, g=g, u=u)
+    torch.cuda.synchronize()
+    R.check_linear_act(x[at], qg, sg, None, None, "silu", y[at], z[at], "past 32 bits")
+    R.check_glu(x[at], qg, sg, qu, su, "silu", h[at], g[at], u[at], "past 32 bits")
+    del y
+    say("past 32 bits", n, "backward")
+    dbias = torch.empty(n, device="cuda")
+    dx, dz = F.fp8_block_linear_act_backward(h, qg, sg, z=z, act=F.ACT_SILU, dbias=dbias)
+    torch.cuda.synchronize()
+    R.check_linear_act_backward(h[at], z[at], qg, sg, "silu", dx[at], dz[at], None, "past 32 bits")
+    # dz as returned, summed in 64 bits; each of its roundings is a half step
+    total = torch.zeros(n, dtype=torch.float64, device="cuda")
+    size = torch.zeros_like(total)
+    for part in dz.split(4096):
+        total += part.double().sum(0)
+        size += part.double().abs().sum(0)
+    assert bool(((dbias.double() - total).abs() <= (R.HALF + (m + 8) * 2.0 ** -23) * size + R.TINY).all())
+    del dz, z
+    dx, dg, du = F.fp8_block_glu_backward(h, g, u, qg, sg, qu, su)
+    torch.cuda.synchronize()
+    R.check_glu_backward(h[at], g[at], u[at], qg, sg, qu, su, "silu", dx[at], dg[at], du[at], "past 32 bits")
+
+
+def test_long_rows():
+    """x and dx of more than 2^32 bytes (long rows of the reduction)."""
+    m, n, k = 70000, 24, 32768
+    gen = torch.Generator().manual_seed(3)
+    q, s = weight(gen, n, k)
+    x = normal(gen, 1000, k).repeat(70, 1)
+    at = torch.tensor([0, 999, 32767, 32768, 65535, 65536, m - 1], device="cuda")
+    say("long rows")
+    y = F.fp8_block_linear_act(x, q, s, act=F.ACT_RELU)
+    dx, _ = F.fp8_block_linear_act_backward(y, q, s)
+    torch.cuda.synchronize()
+    R.check_linear_act(x[at], q, s, None, None, "relu", y[at], None, "long rows")
+    R.check_linear_act_backward(y[at], None, q, s, "none", dx[at], y[at], None, "long rows")
+
+
+def test_everything_given_allocates_nothing_and_dx_is_optional():
+    """With outputs and workspaces given a call allocates nothing; the C entry
+    points take a null dx (an adapter's first layer needs none)."""
+    m, n, k = 100, 1003, 656
+    gen = torch.Generator().manual_seed(8)
+    (qg, sg), (qu, su) = weight(gen, n, k), weight(gen, n, k)
+    x, dy, z = normal(gen, m, k), normal(gen, m, n), normal(gen, m, n)
+    ws = torch.empty(max(F.layer_workspace_size(op, m, n, k) for op in
+                         ("linear_act", "linear_act_backward", "glu", "glu_backward")), dtype=torch.uint8, device="cuda")
+    y, dz, du, dx, db = torch.empty_like(dy), torch.empty_like(dy), torch.empty_like(dy), torch.empty_like(x), torch.empty(n, device="cuda")
+    say("no allocation")
+    before = torch.cuda.memory_stats()["allocation.all.allocated"]
+    F.fp8_block_linear_act(x, qg, sg, act=F.ACT_SILU, out=y, workspace=ws)
+    F.fp8_block_glu(x, qg, sg, qu, su, out=y, workspace=ws)
+    F.fp8_block_linear_act_backward(dy, qg, sg, z=z, act=F.ACT_SILU, dz=dz, dx=dx, dbias=db, workspace=ws)
+    F.fp8_block_glu_backward(dy, z, y, qg, sg, qu, su, dg=dz, du=du, dx=dx, workspace=ws)
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+    torch.cuda.synchronize()
+    R.check_glu_backward(dy, z, y, qg, sg, qu, su, "silu", dx, dz, du, "given")
+    want, wantb = dz.clone(), db.clone()
+    F.fp8_block_linear_act_backward(dy, qg, sg, z=z, act=F.ACT_SILU, dz=want, dx=dx, dbias=wantb, workspace=ws)
+    L, st = F._lib, torch.cuda.current_stream().cuda_stream
+    dz.zero_()
+    db.zero_()
+    assert L.linear_act_backward_raw(dy.data_ptr(), z.data_ptr(), 0, 0, dz.data_ptr(), db.data_ptr(), 0, m, n, k,
+                                     F.ACT_SILU, ws.data_ptr(), ws.numel(), st) == 0
+    du2, dg2 = torch.empty_like(du), torch.empty_like(du)
+    assert L.glu_backward_raw(dy.data_ptr(), z.data_ptr(), y.data_ptr(), 0, 0, 0, 0, dg2.data_ptr(), du2.data_ptr(), 0,
+                              m, n, k, F.ACT_SILU, ws.data_ptr(), ws.numel(), st) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(dz, want) and torch.equal(db, wantb) and torch.equal(du2, du)
+
+
 def test_refusals_on_the_device():
     x = torch.zeros(4, 32, dtype=BF, device="cuda")
     q = torch.zeros(24, 32, dtype=torch.uint8, device="cuda")
