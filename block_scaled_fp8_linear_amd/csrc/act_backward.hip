@@ -3,9 +3,15 @@
 //   linear: dz = dy act'(z), dbias[c] = sum over rows of dz[r, c]
 //   gated:  dg = dh u act'(g), du = dh act(g)
 //
-// The products that follow read the gradients in rows of whole 16-byte
-// chunks. Where N is no multiple of 8 the kernels also write a copy with
-// padded rows (`ld` elements, the padding zero).
+// A thread handles eight consecutive columns of a row. Where N is no multiple
+// of 8 rows start at any 2-byte address: the accesses stay 16 bytes wide (the
+// hardware takes global ones at any alignment), the last columns of a row go
+// one by one, and the kernels also write a copy with padded rows (`ld`
+// elements, the padding zero), which is what the product that follows reads
+// in whole 16-byte chunks. (4096 x 12288 with GELU and the column sums 57 us
+// and 5 for their join, 5.3 TB/s; the gated pair at 4096 x 12800 83 us, 6.3
+// TB/s; odd rows, 809 x 8449 with GELU and sums, 13 us against 23 with one
+// element a thread.)
 #include "fp8bl_act.h"
 #include "fp8bl_device.h"
 #include "fp8bl_internal.h"
@@ -17,85 +23,92 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kColThreads = 32;                      // threads side by side along a row
 constexpr int kRowLanes = kThreads / kColThreads;    // rows in hand at once
+constexpr int kVec = 8;
 
-template <int VEC>
-struct Vec;
-template <>
-struct Vec<8> {
-  u32x4 v;
-  __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const u32x4*>(p); }
-  __device__ __forceinline__ float get(int i) const {
-    const uint32_t w = v[i >> 1];
-    return __uint_as_float((i & 1) ? (w & 0xFFFF0000u) : (w << 16));
+// Eight columns of a row from `col`, or the `left` < 8 that exist (the others
+// read as zero and are not written).
+__device__ __forceinline__ void load8(const uint16_t* p, int left, float (&f)[kVec]) {
+  if (left >= kVec) {
+    u32x4 v;
+    __builtin_memcpy(&v, p, 16);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      f[i] = __uint_as_float((i & 1) ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) f[i] = i < left ? bf16_f32(p[i]) : 0.0f;
   }
-  __device__ __forceinline__ static void store(uint16_t* p, const float (&f)[8]) {
-    const u32x4 o = {pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                     pack_bf16x2(f[6], f[7])};
-    *reinterpret_cast<u32x4*>(p) = o;
+}
+__device__ __forceinline__ u32x4 pack8(const float (&f)[kVec]) {
+  return u32x4{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+               pack_bf16x2(f[6], f[7])};
+}
+__device__ __forceinline__ void store8(uint16_t* p, int left, const float (&f)[kVec]) {
+  if (left >= kVec) {
+    const u32x4 v = pack8(f);
+    __builtin_memcpy(p, &v, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      if (i < left) p[i] = f32_bf16(f[i]);
   }
-};
-template <>
-struct Vec<1> {
-  uint16_t v;
-  __device__ __forceinline__ void load(const uint16_t* p) { v = *p; }
-  __device__ __forceinline__ float get(int) const { return __uint_as_float((uint32_t)v << 16); }
-  __device__ __forceinline__ static void store(uint16_t* p, const float (&f)[1]) {
-    *p = __builtin_bit_cast(uint16_t, (__bf16)f[0]);
-  }
-};
+}
 
-// A workgroup covers 32 * VEC columns and one chunk of rows: thread (rl, cl)
-// takes rows rl, rl + 8, ... of the chunk. The column sums of the eight row
-// lanes meet in LDS and are added in lane order; the chunks' sums go to
-// `part` [chunks, N] and are added in order by the second kernel (no atomics:
-// the same bits on every call). dz may be null (act none: dz is dy), the
-// padded copy too.
-template <int ACT, int VEC>
+// A workgroup covers 256 columns and one chunk of rows: thread (rl, cl) takes
+// rows rl, rl + 8, ... of the chunk. The column sums of the eight row lanes
+// meet in LDS and are added in lane order; the chunks' sums go to `sums`
+// [chunks, N] and are added in order by the second kernel (no atomics: the
+// same bits on every call). dz may be null (act none: dz is dy), the padded
+// copy and the sums too.
+template <int ACT>
 __global__ __launch_bounds__(kThreads)
 void act_backward_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z,
                          uint16_t* __restrict__ dz, uint16_t* __restrict__ pad, int64_t ld,
                          float* __restrict__ sums, int64_t M, int64_t N, int64_t rows_per_chunk,
                          int col_blocks) {
-  __shared__ float red[kRowLanes][kColThreads * VEC + 1];
+  __shared__ float red[kRowLanes][kColThreads * kVec + 1];
   const int cl = threadIdx.x % kColThreads, rl = threadIdx.x / kColThreads;
   const int64_t chunk = blockIdx.x / (uint32_t)col_blocks;
-  const int64_t col = ((int64_t)(blockIdx.x % (uint32_t)col_blocks) * kColThreads + cl) * VEC;
+  const int64_t c0 = (int64_t)(blockIdx.x % (uint32_t)col_blocks) * kColThreads * kVec;
+  const int64_t col = c0 + cl * kVec;
   const int64_t r1 = min((chunk + 1) * rows_per_chunk, M);
-  float sum[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) sum[i] = 0.0f;
-  if (col < N) {
-#pragma unroll 4
+  const int left = (int)min(N - col, (int64_t)kVec);
+  float sum[kVec] = {};
+  // whole chunks and a row's last columns in loops of their own: no branch
+  // between the loads of several rows
+  auto rows = [&](auto full) {
+    const int n8 = decltype(full)::value ? kVec : left;
+#pragma unroll 2
     for (int64_t r = chunk * rows_per_chunk + rl; r < r1; r += kRowLanes) {
-      Vec<VEC> a, b;
-      a.load(dy + r * N + col);
-      if constexpr (ACT != kActNone) b.load(z + r * N + col);
-      float d[VEC];
+      float d[kVec], t[kVec];
+      load8(dy + r * N + col, n8, d);
+      if constexpr (ACT != kActNone) {
+        load8(z + r * N + col, n8, t);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        d[i] = a.get(i);
-        if constexpr (ACT != kActNone) d[i] *= act_grad_f32<ACT>(b.get(i));
-        sum[i] += d[i];
+        for (int i = 0; i < kVec; ++i) d[i] *= act_grad_f32<ACT>(t[i]);
+        if (dz) store8(dz + r * N + col, n8, d);
       }
-      if (ACT != kActNone && dz) Vec<VEC>::store(dz + r * N + col, d);
-      if (VEC == 1 && pad) Vec<VEC>::store(pad + r * ld + col, d);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) sum[i] += d[i];
+      // (columns past N hold zero: 0 from load8 times a finite derivative)
+      if (pad) *reinterpret_cast<u32x4*>(pad + r * ld + col) = pack8(d);
     }
-  }
-  // the padding of the chunk's rows, by the workgroup that has the last columns
-  if (VEC == 1 && pad && col >= N && col < ld)
-    for (int64_t r = chunk * rows_per_chunk + rl; r < r1; r += kRowLanes) pad[r * ld + col] = 0;
+  };
+  if (left >= kVec)
+    rows(ActTag<1>{});
+  else if (left > 0)
+    rows(ActTag<0>{});
   if (!sums) return;
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) red[rl][cl * VEC + i] = sum[i];
+  for (int i = 0; i < kVec; ++i) red[rl][cl * kVec + i] = sum[i];
   __syncthreads();
-  const int64_t c0 = (int64_t)(blockIdx.x % (uint32_t)col_blocks) * kColThreads * VEC;
-  for (int c = threadIdx.x; c < kColThreads * VEC; c += kThreads) {
-    if (c0 + c >= N) continue;
-    float t = red[0][c];
+  const int c = threadIdx.x;
+  static_assert(kColThreads * kVec == kThreads, "one column a thread");
+  if (c0 + c >= N) return;
+  float t = red[0][c];
 #pragma unroll
-    for (int i = 1; i < kRowLanes; ++i) t += red[i][c];
-    sums[chunk * N + c0 + c] = t;
-  }
+  for (int i = 1; i < kRowLanes; ++i) t += red[i][c];
+  sums[chunk * N + c0 + c] = t;
 }
 
 __global__ __launch_bounds__(kThreads)
@@ -115,44 +128,38 @@ void column_sum_kernel(const float* __restrict__ part, float* __restrict__ out, 
   out[c] = t;
 }
 
-// The gated pair's: flat over 8 elements a thread where N is a multiple of 8
-// (the arrays are contiguous), else one element a thread with the padded
-// copies at their own row stride.
-template <int ACT, int VEC>
+// The gated pair's: one 8-column chunk of a row a thread, `chunks` to a row,
+// grid-stride (where N is a multiple of 8 the chunks of all rows are
+// contiguous).
+template <int ACT>
 __global__ __launch_bounds__(kThreads)
 void glu_backward_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ g,
                          const uint16_t* __restrict__ u, uint16_t* __restrict__ dg,
                          uint16_t* __restrict__ du, uint16_t* __restrict__ pad_g,
-                         uint16_t* __restrict__ pad_u, int64_t ld, int64_t M, int64_t N) {
-  const int64_t total = VEC == 1 ? M * ld : M * N;
-  for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * VEC; i < total;
-       i += (int64_t)gridDim.x * kThreads * VEC) {
-    int64_t at = i;
-    if constexpr (VEC == 1) {
-      // over the padded rows: columns past N only write the copies' padding
-      const int64_t r = i / ld, c = i - r * ld;
-      if (c >= N) {
-        if (pad_g) pad_g[i] = pad_u[i] = 0;
-        continue;
-      }
-      at = r * N + c;
+                         uint16_t* __restrict__ pad_u, int64_t M, int64_t N, int64_t chunks) {
+  const int64_t total = M * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+    int64_t at = i * kVec;
+    int left = kVec;
+    if (pad_g || chunks * kVec != N) {
+      const int64_t r = i / chunks, col = (i - r * chunks) * kVec;
+      at = r * N + col;
+      left = (int)min(N - col, (int64_t)kVec);
     }
-    Vec<VEC> a, b, c;
-    a.load(dh + at);
-    b.load(g + at);
-    c.load(u + at);
-    float eg[VEC], eu[VEC];
+    float a[kVec], b[kVec], c[kVec], eg[kVec], eu[kVec];
+    load8(dh + at, left, a);
+    load8(g + at, left, b);
+    load8(u + at, left, c);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float d = a.get(j), t = b.get(j);
-      eg[j] = d * c.get(j) * act_grad_f32<ACT>(t);
-      eu[j] = d * act_f32<ACT>(t);
+    for (int j = 0; j < kVec; ++j) {
+      eg[j] = a[j] * c[j] * act_grad_f32<ACT>(b[j]);
+      eu[j] = a[j] * act_f32<ACT>(b[j]);
     }
-    Vec<VEC>::store(dg + at, eg);
-    Vec<VEC>::store(du + at, eu);
-    if (VEC == 1 && pad_g) {
-      Vec<VEC>::store(pad_g + i, eg);
-      Vec<VEC>::store(pad_u + i, eu);
+    store8(dg + at, left, eg);
+    store8(du + at, left, eu);
+    if (pad_g) {
+      *reinterpret_cast<u32x4*>(pad_g + i * kVec) = pack8(eg);
+      *reinterpret_cast<u32x4*>(pad_u + i * kVec) = pack8(eu);
     }
   }
 }
@@ -166,17 +173,17 @@ void fill_zero_kernel(uint32_t* __restrict__ p, size_t words, uint16_t* __restri
 
 constexpr int64_t kMaxBlocks = 1 << 22;   // threads of a launch stay below 2^32
 
-int64_t column_blocks(int64_t n, int vec) { return (n + kColThreads * vec - 1) / (kColThreads * vec); }
+int64_t column_blocks(int64_t n) { return (n + kThreads - 1) / kThreads; }
 
-// Rows per chunk: enough workgroups to fill the GPU (about eight a CU), at
-// most 256 chunks, and at least 128 rows in one, so that a short call needs no
-// second kernel for its column sums.
+// Rows per chunk: one chunk up to 128 rows, so that a short call needs no
+// second kernel for its column sums; else enough workgroups to fill the GPU
+// (about eight a CU), at least 32 rows and at most 256 chunks.
 int64_t chunk_rows(int64_t m, int64_t n) {
-  const int64_t cols = column_blocks(n, n % 8 == 0 ? 8 : 1);
-  int64_t chunks = (2048 + cols - 1) / cols;
+  if (m <= 128) return 128;
+  int64_t chunks = (2048 + column_blocks(n) - 1) / column_blocks(n);
   if (chunks > 256) chunks = 256;
-  int64_t rows = (m + chunks - 1) / chunks;
-  return rows < 128 ? 128 : rows;
+  const int64_t rows = (m + chunks - 1) / chunks;
+  return rows < 32 ? 32 : rows;
 }
 
 }  // namespace
@@ -193,18 +200,11 @@ hipError_t launch_act_backward(const uint16_t* dy, const uint16_t* z, uint16_t* 
   const int64_t rows = chunk_rows(m, n);
   const int64_t chunks = (m + rows - 1) / rows;
   float* sums = dbias == nullptr ? nullptr : chunks > 1 ? part : dbias;
-  const bool wide = n % 8 == 0;
-  // the narrow form also covers the padding columns
-  const int64_t cols = wide ? column_blocks(n, 8) : column_blocks(pad ? ld : n, 1);
+  const int64_t cols = column_blocks(n);
   const dim3 grid((uint32_t)(cols * chunks));
   with_act(act, [&](auto a) {
-    constexpr int A = decltype(a)::value;
-    if (wide)
-      hipLaunchKernelGGL((act_backward_kernel<A, 8>), grid, dim3(kThreads), 0, stream, dy, z, dz, pad,
-                         ld, sums, m, n, rows, (int)cols);
-    else
-      hipLaunchKernelGGL((act_backward_kernel<A, 1>), grid, dim3(kThreads), 0, stream, dy, z, dz, pad,
-                         ld, sums, m, n, rows, (int)cols);
+    hipLaunchKernelGGL((act_backward_kernel<decltype(a)::value>), grid, dim3(kThreads), 0, stream, dy, z, dz,
+                       pad, ld, sums, m, n, rows, (int)cols);
   });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || dbias == nullptr || chunks == 1) return e;
@@ -214,19 +214,14 @@ hipError_t launch_act_backward(const uint16_t* dy, const uint16_t* z, uint16_t* 
 }
 
 hipError_t launch_glu_backward(const uint16_t* dh, const uint16_t* g, const uint16_t* u, uint16_t* dg,
-                               uint16_t* du, uint16_t* pad_g, uint16_t* pad_u, int64_t ld, int64_t m,
-                               int64_t n, int act, hipStream_t stream) {
-  const bool wide = n % 8 == 0;
-  const int64_t blocks = ((wide ? m * n / 8 : m * ld) + kThreads - 1) / kThreads;
+                               uint16_t* du, uint16_t* pad_g, uint16_t* pad_u, int64_t m, int64_t n, int act,
+                               hipStream_t stream) {
+  const int64_t chunks = (n + kVec - 1) / kVec;        // ld / 8 where there are padded copies
+  const int64_t blocks = (m * chunks + kThreads - 1) / kThreads;
   const dim3 grid((uint32_t)(blocks < kMaxBlocks ? blocks : kMaxBlocks));
   with_act(act, [&](auto a) {
-    constexpr int A = decltype(a)::value;
-    if (wide)
-      hipLaunchKernelGGL((glu_backward_kernel<A, 8>), grid, dim3(kThreads), 0, stream, dh, g, u, dg, du,
-                         pad_g, pad_u, ld, m, n);
-    else
-      hipLaunchKernelGGL((glu_backward_kernel<A, 1>), grid, dim3(kThreads), 0, stream, dh, g, u, dg, du,
-                         pad_g, pad_u, ld, m, n);
+    hipLaunchKernelGGL((glu_backward_kernel<decltype(a)::value>), grid, dim3(kThreads), 0, stream, dh, g, u, dg,
+                       du, pad_g, pad_u, m, n, chunks);
   });
   return hipGetLastError();
 }

@@ -149,8 +149,8 @@ hipError_t launch_act_backward(const uint16_t* dy, const uint16_t* z, uint16_t* 
                                int64_t ld, float* dbias, float* part, int64_t m, int64_t n, int act,
                                hipStream_t stream);
 hipError_t launch_glu_backward(const uint16_t* dh, const uint16_t* g, const uint16_t* u, uint16_t* dg,
-                               uint16_t* du, uint16_t* pad_g, uint16_t* pad_u, int64_t ld, int64_t m,
-                               int64_t n, int act, hipStream_t stream);
+                               uint16_t* du, uint16_t* pad_g, uint16_t* pad_u, int64_t m, int64_t n, int act,
+                               hipStream_t stream);
 hipError_t launch_fill_zero(void* p, size_t bytes, hipStream_t stream);
 
 // Checks shared by the two ABI files.

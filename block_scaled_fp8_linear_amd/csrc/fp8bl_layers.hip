@@ -238,7 +238,7 @@ FP8BL_EXPORT int fp8_block_glu_backward(const uint16_t* dh, const uint16_t* g, c
   const bool pad = n % 8 != 0 && product;
   uint16_t* const cg = pad ? at<uint16_t>(workspace, 0) : nullptr;
   uint16_t* const cu = pad ? at<uint16_t>(workspace, pad_bytes(m, n)) : nullptr;
-  const hipError_t e = fp8bl::launch_glu_backward(dh, g, u, dg, du, cg, cu, padded(n), m, n, act, stream);
+  const hipError_t e = fp8bl::launch_glu_backward(dh, g, u, dg, du, cg, cu, m, n, act, stream);
   if (e != hipSuccess) return FP8BL_HIP_ERROR;
   if (!product) return FP8BL_OK;
   const size_t off = 2 * pad_bytes(m, n);
