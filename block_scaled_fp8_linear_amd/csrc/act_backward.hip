@@ -21,8 +21,6 @@ namespace fp8bl {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kColThreads = 32;                      // threads side by side along a row
-constexpr int kRowLanes = kThreads / kColThreads;    // rows in hand at once
 constexpr int kVec = 8;
 
 // Eight columns of a row from `col`, or the `left` < 8 that exist (the others
@@ -54,22 +52,23 @@ __device__ __forceinline__ void store8(uint16_t* p, int left, const float (&f)[k
   }
 }
 
-// A workgroup covers 256 columns and one chunk of rows: thread (rl, cl) takes
-// rows rl, rl + 8, ... of the chunk. The column sums of the eight row lanes
-// meet in LDS and are added in lane order; the chunks' sums go to `sums`
-// [chunks, N] and are added in order by the second kernel (no atomics: the
-// same bits on every call). dz may be null (act none: dz is dy), the padded
-// copy and the sums too.
-template <int ACT>
+// A workgroup of CT threads along a row and 256 / CT rows covers 8 CT columns
+// and one chunk of rows: thread (rl, cl) takes rows rl, rl + 256 / CT, ... of
+// the chunk. The column sums of the row lanes meet in LDS and are added in
+// lane order; the chunks' sums go to `sums` [chunks, N] and are added in order
+// by the second kernel (no atomics: the same bits on every call). dz may be
+// null (act none: dz is dy), the padded copy and the sums too.
+template <int ACT, int CT>
 __global__ __launch_bounds__(kThreads)
 void act_backward_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z,
                          uint16_t* __restrict__ dz, uint16_t* __restrict__ pad, int64_t ld,
                          float* __restrict__ sums, int64_t M, int64_t N, int64_t rows_per_chunk,
                          int col_blocks) {
-  __shared__ float red[kRowLanes][kColThreads * kVec + 1];
-  const int cl = threadIdx.x % kColThreads, rl = threadIdx.x / kColThreads;
+  constexpr int kRowLanes = kThreads / CT;
+  __shared__ float red[kRowLanes][kVec][CT + 1];
+  const int cl = threadIdx.x % CT, rl = threadIdx.x / CT;
   const int64_t chunk = blockIdx.x / (uint32_t)col_blocks;
-  const int64_t c0 = (int64_t)(blockIdx.x % (uint32_t)col_blocks) * kColThreads * kVec;
+  const int64_t c0 = (int64_t)(blockIdx.x % (uint32_t)col_blocks) * CT * kVec;
   const int64_t col = c0 + cl * kVec;
   const int64_t r1 = min((chunk + 1) * rows_per_chunk, M);
   const int left = (int)min(N - col, (int64_t)kVec);
@@ -100,14 +99,14 @@ void act_backward_kernel(const uint16_t* __restrict__ dy, const uint16_t* __rest
     rows(ActTag<0>{});
   if (!sums) return;
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) red[rl][cl * kVec + i] = sum[i];
+  for (int i = 0; i < kVec; ++i) red[rl][i][cl] = sum[i];
   __syncthreads();
   const int c = threadIdx.x;
-  static_assert(kColThreads * kVec == kThreads, "one column a thread");
-  if (c0 + c >= N) return;
-  float t = red[0][c];
+  static_assert(CT * kVec <= kThreads, "one column a thread");
+  if (c >= CT * kVec || c0 + c >= N) return;
+  float t = red[0][c % kVec][c / kVec];
 #pragma unroll
-  for (int i = 1; i < kRowLanes; ++i) t += red[i][c];
+  for (int i = 1; i < kRowLanes; ++i) t += red[i][c % kVec][c / kVec];
   sums[chunk * N + c0 + c] = t;
 }
 
@@ -173,38 +172,48 @@ void fill_zero_kernel(uint32_t* __restrict__ p, size_t words, uint16_t* __restri
 
 constexpr int64_t kMaxBlocks = 1 << 22;   // threads of a launch stay below 2^32
 
-int64_t column_blocks(int64_t n) { return (n + kThreads - 1) / kThreads; }
-
-// Rows per chunk: one chunk up to 128 rows, so that a short call needs no
-// second kernel for its column sums; else enough workgroups to fill the GPU
-// (about eight a CU), at least 32 rows and at most 256 chunks.
-int64_t chunk_rows(int64_t m, int64_t n) {
-  if (m <= 128) return 128;
-  int64_t chunks = (2048 + column_blocks(n) - 1) / column_blocks(n);
+// Up to 256 rows narrow workgroups (8 threads along a row) take all rows as
+// one chunk, so that a short call needs no second kernel for its column sums
+// and still has workgroups enough; else wide ones (32 threads), about eight a
+// CU, with at least 32 rows in a chunk and at most 256 chunks. (77 x 1003 with
+// SiLU and sums: 6.4 us; as four wide workgroups 18.)
+struct RowPlan {
+  int ct;
+  int64_t rows, chunks;
+};
+int64_t column_blocks(int64_t n, int ct) { return (n + ct * kVec - 1) / (ct * kVec); }
+RowPlan plan_rows(int64_t m, int64_t n) {
+  if (m <= 256) return RowPlan{8, 256, 1};
+  int64_t chunks = (2048 + column_blocks(n, 32) - 1) / column_blocks(n, 32);
   if (chunks > 256) chunks = 256;
-  const int64_t rows = (m + chunks - 1) / chunks;
-  return rows < 32 ? 32 : rows;
+  int64_t rows = (m + chunks - 1) / chunks;
+  rows = rows < 32 ? 32 : rows;
+  return RowPlan{32, rows, (m + rows - 1) / rows};
 }
 
 }  // namespace
 
 size_t column_sum_bytes(int64_t m, int64_t n) {
-  const int64_t rows = chunk_rows(m, n);
-  const int64_t chunks = (m + rows - 1) / rows;
+  const int64_t chunks = plan_rows(m, n).chunks;
   return chunks > 1 ? round_up((size_t)(chunks * n) * 4, kWorkspaceAlign) : 0;
 }
 
 hipError_t launch_act_backward(const uint16_t* dy, const uint16_t* z, uint16_t* dz, uint16_t* pad,
                                int64_t ld, float* dbias, float* part, int64_t m, int64_t n, int act,
                                hipStream_t stream) {
-  const int64_t rows = chunk_rows(m, n);
-  const int64_t chunks = (m + rows - 1) / rows;
+  const RowPlan p = plan_rows(m, n);
+  const int64_t chunks = p.chunks;
   float* sums = dbias == nullptr ? nullptr : chunks > 1 ? part : dbias;
-  const int64_t cols = column_blocks(n);
+  const int64_t cols = column_blocks(n, p.ct);
   const dim3 grid((uint32_t)(cols * chunks));
   with_act(act, [&](auto a) {
-    hipLaunchKernelGGL((act_backward_kernel<decltype(a)::value>), grid, dim3(kThreads), 0, stream, dy, z, dz,
-                       pad, ld, sums, m, n, rows, (int)cols);
+    constexpr int A = decltype(a)::value;
+    if (p.ct == 8)
+      hipLaunchKernelGGL((act_backward_kernel<A, 8>), grid, dim3(kThreads), 0, stream, dy, z, dz, pad, ld, sums, m,
+                         n, p.rows, (int)cols);
+    else
+      hipLaunchKernelGGL((act_backward_kernel<A, 32>), grid, dim3(kThreads), 0, stream, dy, z, dz, pad, ld, sums,
+                         m, n, p.rows, (int)cols);
   });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || dbias == nullptr || chunks == 1) return e;
