@@ -11,16 +11,13 @@ namespace fp8bl {
 
 namespace {
 
-constexpr int kBK = 64;                     // K per step
+constexpr int kBK = 64;                     // K per step (of the plain kernels), and of an LDS row of X
 constexpr int kBM = 256;                    // X rows per tile (the plain kernels' and the tallest)
 constexpr int kBN = 256;                    // weight rows per tile
 constexpr int kWaves = 4;
 constexpr int kThreads = kWaves * 64;
-constexpr int kWBytes = kBN * kBK;          // bytes of one stage's codes (16 KB)
-constexpr int kWLoads = kWBytes / 16 / kThreads;       // 16-byte code loads per lane per step
 constexpr uint32_t kOob = 0x80000000u;      // buffer offset past every valid range
 
-static_assert(kWLoads == 4, "one wave's code loads cover its 64 rows of a stage");
 static_assert(kBK == 64, "the X chunk permutation assumes 128-byte LDS rows");
 
 // s_waitcnt immediates (gfx9 encoding: vmcnt[3:0] + vmcnt_hi[15:14],
@@ -71,10 +68,13 @@ struct LargeArgs {
 // the up weight, and y receives the product of the pair. For kGradient N is
 // the weight's row length and K the number of its rows.
 // MB: 32-row blocks of X per tile (8, 4 or 2), STAGES: ring length. Fewer rows
-// make a step shorter, so that the codes of a weight stream through at the
-// rate of HBM when there are not 256 rows to multiply: with MB = 2 two
-// workgroups share a CU.
-template <bool SPLIT, bool GATED, Form FORM, int ACT, int MB = 8, int STAGES = 3>
+// make a step shorter, so that the codes of a weight stream through faster
+// when there are not 256 rows to multiply. KS: 64-wide blocks of K per step. With 2 a code load
+// reads 128 bytes of 8 weight rows instead of 64 of 16, which HBM streams
+// faster (the codes of a row then lie 128 bytes apart in LDS, swizzled as X),
+// and there are half the barriers. kGradient's loads stay 16 rows x 64 bytes:
+// the four waves read 256 bytes of a row between them.
+template <bool SPLIT, bool GATED, Form FORM, int ACT, int MB = 8, int STAGES = 3, int KS = 1>
 __device__ __forceinline__
 void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__ q,
                      const float* __restrict__ s, const uint8_t* __restrict__ q2,
@@ -87,9 +87,15 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   static_assert(MB == 8 || MB == 4 || MB == 2, "row blocks go in pairs, a ring of eight fragments");
   constexpr int kStages = STAGES;
   constexpr int kTileM = 32 * MB;
-  constexpr int kXElems = kTileM * kBK;                         // bf16 elements of one stage's X tile
+  static_assert(KS == (MB == 2 ? 2 : 1), "the load slots of the steps built");
+  constexpr int kStep = kBK * KS;                               // K per step
+  constexpr int kXBlock = kTileM * kBK;                         // bf16 elements of a 64-wide block of X
+  constexpr int kXElems = KS * kXBlock;                         // and of one stage's X tile
   constexpr int kXLoads = kXElems * 2 / 16 / kThreads;          // 16-byte X loads per lane per step
-  static_assert(kXLoads == MB, "one wave's X loads cover a quarter of a stage's rows");
+  constexpr int kWBytes = kBN * kStep;                          // bytes of one stage's codes
+  constexpr int kWLoads = kWBytes / 16 / kThreads;              // 16-byte code loads per lane per step
+  static_assert(kXLoads == MB * KS, "one wave's X loads cover a quarter of a stage's rows");
+  static_assert(kWLoads == 4 * KS, "one wave's code loads cover its 64 rows of a stage");
   constexpr int kScales = FORM == kGlu ? 2 : 1;                 // scale words per wave and step
   constexpr int kSElems = kScales * kWaves * 64 * 4 / 2;        // their slots (256 B each)
   constexpr int kStageElems = kXElems + kWBytes / 2 + kSElems;  // stage size in bf16 elements (MB = 8: 49 KB)
@@ -116,7 +122,7 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   const int ntiles = tiles_m * tiles_n;
   const int units = ntiles * splits;
   const int my_units = (units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
-  const int nkt = FORM == kGradient && la.x2 ? 2 * la.steps1 : (K + kBK - 1) / kBK;
+  const int nkt = FORM == kGradient && la.x2 ? 2 * la.steps1 : (K + kStep - 1) / kStep;
   const int ldx = FORM == kGradient ? la.ldx : K;    // row stride of X
   struct Unit {
     int m0, n0, kt0, nreal, split;
@@ -151,9 +157,9 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   // offset of a real chunk stays inside its row.)
   const int xc_even = (lane & 7) ^ (lane >> 4);
   const int xc_odd = (lane & 7) ^ (4 + (lane >> 4));
-  uint32_t xvo[kXLoads];
+  uint32_t xvo[MB];
 #pragma unroll
-  for (int i = 0; i < kXLoads; ++i)
+  for (int i = 0; i < MB; ++i)
     xvo[i] = (uint32_t)((8 * MB * wave + 8 * i + (lane >> 3)) * ldx * 2 + ((i & 1) ? xc_odd : xc_even) * 16);
   // codes: load i of wave w fills the stage's code rows 64w + 16i .. +16
   // (64 bytes each, the step's K range) from its weight rows wrow + 16i ..;
@@ -173,6 +179,9 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   for (int i = 0; i < kWLoads; ++i) {
     if constexpr (FORM == kGradient)
       wvo[i] = (uint32_t)((16 * i + (lane >> 2)) * N + 64 * wave + 16 * wc);
+    else if constexpr (KS == 2)
+      wvo[i] = (uint32_t)((wrow + 8 * (FORM == kGlu ? i & 3 : i) + (lane >> 3)) * K +
+                          16 * ((i & 1) ? xc_odd : xc_even));
     else
       wvo[i] = (uint32_t)((wrow + 16 * (FORM == kGlu ? i & 1 : i) + (lane >> 2)) * K + 16 * wc);
   }
@@ -211,36 +220,39 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   // product; `kbase` counts within it.
   auto second = [&](int kt) -> bool { return FORM == kGradient && LU.kt0 + kt >= la.steps1; };
   auto base_of = [&](int kt) -> int {
-    return (LU.kt0 + kt - (second(kt) ? la.steps1 : 0)) * kBK;
+    return (LU.kt0 + kt - (second(kt) ? la.steps1 : 0)) * kStep;
   };
   auto issue_x = [&](int sb, int kt, int i) {
     const int kbase = base_of(kt);
     // K left in this step (0 past the unit's range): a chunk is read iff it
     // starts below it
     const int klim = kt < LU.nreal ? K - kbase : 0;
-    const bool in = ((i & 1) ? xc_odd : xc_even) * 8 < klim;
-    lds_ptr_t to = (lds_ptr_t)&xs[sb + (8 * MB * wave + 8 * i) * kBK];
+    const int b = i / MB, ib = i % MB;              // 64-wide block, load within it
+    const bool in = ((ib & 1) ? xc_odd : xc_even) * 8 + kBK * b < klim;
+    lds_ptr_t to = (lds_ptr_t)&xs[sb + b * kXBlock + (8 * MB * wave + 8 * ib) * kBK];
+    const uint32_t koff = (uint32_t)((kbase + kBK * b) * 2);
     if (FORM == kGradient && second(kt))
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(xrs2, to, 16, in ? xvo[i] : kOob, (uint32_t)(kbase * 2), 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xrs2, to, 16, in ? xvo[ib] : kOob, koff, 0, 0);
     else
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(xrs, to, 16, in ? xvo[i] : kOob, (uint32_t)(kbase * 2), 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xrs, to, 16, in ? xvo[ib] : kOob, koff, 0, 0);
   };
   auto issue_w = [&](int sb, int kt, int i) {
     const int kbase = base_of(kt);
     const int klim = kt < LU.nreal ? K - kbase : 0;
-    lds_ptr_t to = (lds_ptr_t)&xs[sb + kXElems + (64 * wave + 16 * i) * kBK / 2];
+    // (a load fills 1 KB: 16 rows of 64 bytes or 8 of 128)
+    lds_ptr_t to = (lds_ptr_t)&xs[sb + kXElems + (64 * wave * KS + 16 * i) * kBK / 2];
     if constexpr (FORM == kGradient) {
       // weight rows kbase.. (at most 64, fewer at the end), columns from the
       // tile's first: rows past the last lie past the range, columns past N
       // are pushed out of it
       const uint8_t* const base = (second(kt) ? q2 : q) + (size_t)kbase * N + LU.n0;
-      const int rows = max(min(klim, kBK), 0);
+      const int rows = max(min(klim, kStep), 0);
       const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, (uint32_t)(rows > 0 ? rows * N - LU.n0 : 0));
       const bool in = LU.n0 + 64 * wave + 16 * wc < N;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, to, 16, in ? wvo[i] : kOob, 0, 0, 0);
     } else {
-      const bool kin = 16 * wc < klim;
-      if (FORM == kGlu && i >= 2)
+      const bool kin = 16 * (KS == 2 ? ((i & 1) ? xc_odd : xc_even) : wc) < klim;
+      if (FORM == kGlu && i >= 2 * KS)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(wrs2, to, 16, kin ? wvo[i] : kOob, (uint32_t)kbase, 0, 0);
       else
         __builtin_amdgcn_raw_ptr_buffer_load_lds(wrs, to, 16, kin ? wvo[i] : kOob, (uint32_t)kbase, 0, 0);
@@ -265,7 +277,7 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
       else
         __builtin_amdgcn_raw_ptr_buffer_load_lds(srs, to, 4, off, 0, 0, 0);
     } else {
-      const int kb = min(((LU.kt0 + kt) * kBK) / kBlock, gk - 1);
+      const int kb = min(((LU.kt0 + kt) * kStep) / kBlock, gk - 1);
       const uint32_t off = (uint32_t)((lsrow * gk + kb) * 4) + (live ? 0u : kOob);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(srs, to, 4, off, 0, 0, 0);
       if constexpr (FORM == kGlu)
@@ -287,7 +299,9 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   // Codes of weight block nb, K half j of a stage (the 16 codes of sub-steps
   // 2j and 2j+1): lane l reads row 64w + 32nb + l%32, logical chunk
   // l/32 + 2j, stored at chunk (l/32 + 2j) ^ ((l%32 / 4) % 4).
-  const int crow = (64 * wave + (lane & 31)) * kBK;     // byte offset of the lane's row
+  // (KS = 2: rows of 128 bytes, chunk c of row r at c ^ ((r / 2) % 8).)
+  const int crow = (64 * wave + (lane & 31)) * kStep;   // byte offset of the lane's row
+  const int crd = crow + (((lane >> 5) ^ (((lane & 31) >> 1) & 7)) << 4);
   const int cswz = ((lane & 31) >> 2) & 3;
   const int crd0 = crow + ((((lane >> 5) + 0) ^ cswz) << 4);
   const int crd1 = crow + ((((lane >> 5) + 2) ^ cswz) << 4);
@@ -298,7 +312,7 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   // its X chunk (16h + 32(t/2) + 8(t%2) .. +8), its group of 16 lanes the
   // columns 16 ((l / 16) % 2) .. of the block.
   const int trow = (lane & 15) >> 1;
-  const int tr0 = 64 * wave * kBK + (16 * (lane >> 5) + trow) * 64 + 8 * (lane & 1) + 16 * ((lane >> 4) & 1);
+  const int tr0 = 64 * wave * kStep + (16 * (lane >> 5) + trow) * 64 + 8 * (lane & 1) + 16 * ((lane >> 4) & 1);
   const int trc[2] = {tr0 + 32 * (trow >> 2), tr0 + 32 * (1 ^ (trow >> 2))};
   auto read_w = [&](u32x4 (&c)[2], int sb, int j) {
     const uint8_t* const codes = reinterpret_cast<const uint8_t*>(&xs[sb + kXElems]);
@@ -313,9 +327,9 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
           c[nb][2 * e + 1] = (uint32_t)v[1];
         }
     } else {
-      const uint8_t* base = codes + (j ? crd1 : crd0);
+      const uint8_t* base = codes + (KS == 2 ? crd ^ (32 * j) : j ? crd1 : crd0);
 #pragma unroll
-      for (int nb = 0; nb < 2; ++nb) c[nb] = *reinterpret_cast<const u32x4*>(base + nb * 32 * kBK);
+      for (int nb = 0; nb < 2; ++nb) c[nb] = *reinterpret_cast<const u32x4*>(base + nb * 32 * kStep);
     }
   };
   // X fragment f of a stage (sub-step t = f / 8, row block mb = f % 8): the
@@ -325,8 +339,9 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   const int aswz = (arow >> 1) & 7;
   auto read_xf = [&](int sb, int f) -> bf16x8 {
     const int t = f / MB, mb = f % MB;
-    const int c = 2 * ahalf + 4 * (t >> 1) + (t & 1);
-    return *reinterpret_cast<const bf16x8*>(&xs[sb + arow * kBK + ((c ^ aswz) << 3) + mb * 32 * kBK]);
+    const int c = 2 * ahalf + 4 * ((t & 3) >> 1) + (t & 1);
+    return *reinterpret_cast<const bf16x8*>(
+        &xs[sb + (t >> 2) * kXBlock + arow * kBK + ((c ^ aswz) << 3) + mb * 32 * kBK]);
   };
 
   f32x16 acc[2][MB];
@@ -361,14 +376,15 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   // slot of a fragment the same in every step (32 fragments a step)
   constexpr int kRing = 8;
   constexpr int kAhead = 4;
-  constexpr int kFrags = 4 * MB;
+  constexpr int kSubs = 4 * KS;           // sub-steps of 16 K
+  constexpr int kFrags = kSubs * MB;
   static_assert(kFrags % kRing == 0, "a fragment's slot is the same in every step");
   // Fragment at which the next step's loads are waited for and its codes
   // read, and the one with the barrier, before the first read of the next
   // stage. Loads of the step STAGES - 1 ahead that are out by then.
   constexpr int kFragBar = kFrags - kAhead;
-  constexpr int kFragWait = MB == 8 ? 24 : MB == 4 ? 8 : 4;
-  constexpr int kIssued = MB == 8 ? kXLoads + kWLoads : MB == 4 ? kXLoads + 2 : kXLoads + 2;
+  constexpr int kFragWait = MB == 8 ? 24 : MB == 4 ? 8 : kFragBar;
+  constexpr int kIssued = kXLoads + (MB == 4 ? 2 : kWLoads);
   constexpr int kInFlight = (kStages - 3) * kLoadsPerStep + kIssued;
   static_assert(kInFlight <= 63 && (kStages - 2) * kLoadsPerStep <= 63, "vmcnt holds the loads in flight");
   bf16x8 xr[kRing];
@@ -406,8 +422,8 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
     const int sb = S * kStageElems, sbn = Sn * kStageElems, sbl = L * kStageElems;
 
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      if (t == 0) read_w(cB, sb, 1);
+    for (int t = 0; t < kSubs; ++t) {
+      if ((t & 1) == 0 && t + 2 < kSubs) read_w(t & 2 ? cA : cB, sb, t / 2 + 1);
 #pragma unroll
       for (int mb = 0; mb < MB; mb += 2) {
         // one region: the MFMAs of fragments f, f+1 with their share of the
@@ -445,10 +461,9 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
           if (f >= 4 && f <= 10) issue_w(sbl, lkt, (f - 4) >> 1);
           if (f == 12) issue_s(sbl, lkt);
         } else {
-          if (f == 0) { issue_x(sbl, lkt, 0); issue_x(sbl, lkt, 1); }
-          if (f == 2) { issue_w(sbl, lkt, 0); issue_w(sbl, lkt, 1); }
-          if (f == 4) { issue_w(sbl, lkt, 2); issue_w(sbl, lkt, 3); }
-          if (f == 6) issue_s(sbl, lkt);
+          if (f <= 2) { issue_x(sbl, lkt, f); issue_x(sbl, lkt, f + 1); }
+          if (f >= 4 && f <= 10) { issue_w(sbl, lkt, f - 4); issue_w(sbl, lkt, f - 3); }
+          if (f == 12) issue_s(sbl, lkt);
         }
         // the next sub-step's weight operands, a quarter (one block's half
         // K of the sub-step: four codes to bf16) per region: sub-steps 1..3
@@ -456,20 +471,20 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
         // read at fragment 24, in the two regions after the barrier
         auto piece = [&](int q4) {
           const int nb = q4 >> 1, half = q4 & 1;
-          const int tn = (t + 1) & 3;          // sub-step being prepared
-          const u32x4 (&c)[2] = tn <= 1 ? cA : cB;
+          const int tn = (t + 1) % kSubs;      // sub-step being prepared
+          const u32x4 (&c)[2] = tn & 2 ? cB : cA;
           const u32x2 v = dequant4(c[nb][2 * (tn & 1) + half], tn == 0 ? scn[nb] : sc[nb]);
           wdh[tn & 1][nb][2 * half] = v[0];
           wdh[tn & 1][nb][2 * half + 1] = v[1];
         };
-        if (t < 3) {
+        if (t < kSubs - 1) {
           constexpr int kPieces = 8 / MB;
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) piece((mb >> 1) * kPieces + i);
         } else if (f >= kFragBar) {
           constexpr int kPieces = MB == 2 ? 4 : 2;
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) piece((f - (MB == 2 ? 6 : kFragBar)) + i);
+          for (int i = 0; i < kPieces; ++i) piece((f - (MB == 2 ? kFrags - 2 : kFragBar)) + i);
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -592,11 +607,11 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
       // 128-byte pieces of rows (kGlu: chunks 0..7 of a row are its 32 gate
       // columns, 8..15 the up columns, and a lane reads four of each). One
       // rounding per output. The LDS is the wave's own part of the stage the
-      // last step used, X rows (8 KB) for MB = 8, else codes (4 KB): every
+      // last step used, X rows (8 KB) for MB = 8, else codes (4 or 8 KB): every
       // wave finished reading that stage before the last barrier, and only
       // this wave refills its part, with loads it issues after these reads
       // have returned.
-      constexpr int kHalves = MB == 8 ? 1 : 2;
+      constexpr int kHalves = MB == 4 ? 2 : 1;
       constexpr int kEpiRows = 32 / kHalves;
       constexpr int kLanesRow = FORM == kGlu ? 8 : 16;        // lanes side by side on a row
       constexpr int kRowsRead = 64 / kLanesRow;
@@ -608,7 +623,7 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
       const int col4 = CU.n0 + (FORM == kGlu ? 32 : 64) * wave + 4 * cc;
       const int last = (S == 0 ? kStages - 1 : S - 1) * kStageElems;
       uint8_t* const buf = reinterpret_cast<uint8_t*>(
-          &xs[last + (MB == 8 ? wave * 64 * kBK : kXElems + wave * 64 * kBK / 2)]);
+          &xs[last + (MB == 8 ? wave * 64 * kBK : kXElems + wave * 64 * kStep / 2)]);
       // The lanes of one half write while the others wait: without the wave
       // barriers the compiler may run the two halves' lanes through the whole
       // epilogue one after the other, and reads would miss their writes.

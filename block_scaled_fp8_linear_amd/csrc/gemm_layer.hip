@@ -7,42 +7,46 @@ namespace fp8bl {
 
 namespace {
 
-// Tile heights (32-row blocks of X, ring stages, workgroups a CU).
-template <int MB>
+// The tiles built: 32-row blocks of X, ring stages, 64-wide blocks of K per
+// step; one workgroup a CU. (64 rows with 64 of K a step and two workgroups a
+// CU: 64 x 25600 x 5120 47.4 us against 42.0, 64 x 5120 x 25600 45.3 against
+// 38.2, 333 x 4304 x 1168 20.2 against 20.5.)
+enum TileId { k256, k128, k64 };
+template <int ID>
 struct Tile;
 template <>
-struct Tile<8> {
-  static constexpr int kStages = 3, kPerCu = 1;
+struct Tile<k256> {
+  static constexpr int kMB = 8, kStages = 3, kKS = 1;
 };
 template <>
-struct Tile<4> {
-  static constexpr int kStages = 4, kPerCu = 1;
+struct Tile<k128> {
+  static constexpr int kMB = 4, kStages = 4, kKS = 1;
 };
 template <>
-struct Tile<2> {
-  static constexpr int kStages = 3, kPerCu = 2;
+struct Tile<k64> {
+  static constexpr int kMB = 2, kStages = 3, kKS = 2;
 };
 
 struct Grid {
   int gk, tiles_m, tiles_n, steps, splits, steps_per_unit;
 };
 
-template <bool SPLIT, int ACT, int MB>
-__global__ __launch_bounds__(kThreads, Tile<MB>::kPerCu)
+template <bool SPLIT, int ACT, int ID>
+__global__ __launch_bounds__(kThreads, 1)
 void linear_act_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ q,
                        const float* __restrict__ s, uint16_t* y, float* __restrict__ part, int M, int N,
                        int K, Grid g, LargeArgs la) {
-  gemm_large_body<SPLIT, false, kLayer, ACT, MB, Tile<MB>::kStages>(
+  gemm_large_body<SPLIT, false, kLayer, ACT, Tile<ID>::kMB, Tile<ID>::kStages, Tile<ID>::kKS>(
       x, q, s, nullptr, nullptr, y, part, M, N, K, g.gk, g.tiles_m, g.tiles_n, g.steps, g.splits,
       g.steps_per_unit, la);
 }
 
-template <bool SPLIT, int ACT, int MB>
-__global__ __launch_bounds__(kThreads, Tile<MB>::kPerCu)
+template <bool SPLIT, int ACT, int ID>
+__global__ __launch_bounds__(kThreads, 1)
 void glu_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ qg, const float* __restrict__ sg,
                 const uint8_t* __restrict__ qu, const float* __restrict__ su, uint16_t* __restrict__ h,
                 float* __restrict__ part, int M, int N, int K, Grid g, LargeArgs la) {
-  gemm_large_body<SPLIT, false, kGlu, ACT, MB, Tile<MB>::kStages>(
+  gemm_large_body<SPLIT, false, kGlu, ACT, Tile<ID>::kMB, Tile<ID>::kStages, Tile<ID>::kKS>(
       x, qg, sg, qu, su, h, part, M, N, K, g.gk, g.tiles_m, g.tiles_n, g.steps, g.splits, g.steps_per_unit, la);
 }
 
@@ -51,62 +55,67 @@ void glu_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ qg, 
 // (ds_read_b64_tr_b8) hand each lane eight rows of its column, so neither a
 // transposed copy of the weight nor a shuffle is needed, and one decode per
 // code feeds the tile's rows as in the forward.
-template <bool SPLIT, int MB>
-__global__ __launch_bounds__(kThreads, Tile<MB>::kPerCu)
+template <bool SPLIT, int ID>
+__global__ __launch_bounds__(kThreads, 1)
 void input_gradient_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ q,
                            const float* __restrict__ s, const uint8_t* __restrict__ q2,
                            const float* __restrict__ s2, uint16_t* __restrict__ dx,
                            float* __restrict__ part, int M, int C, int R, Grid g, LargeArgs la) {
-  gemm_large_body<SPLIT, false, kGradient, kActNone, MB, Tile<MB>::kStages>(
+  gemm_large_body<SPLIT, false, kGradient, kActNone, Tile<ID>::kMB, Tile<ID>::kStages, Tile<ID>::kKS>(
       x, q, s, q2, s2, dx, part, M, C, R, g.gk, g.tiles_m, g.tiles_n, g.steps, g.splits, g.steps_per_unit, la);
 }
 
 int blocks_of(int64_t v) { return (int)((v + kBlock - 1) / kBlock); }
 
-// Tile height and K splits of one of the three products: tiles of `cols`
-// output columns, `steps` 64-wide steps of the reduction, `words` fp32 partials
-// an output (two for the gated pair). The model, in microseconds, was fitted
-// to 900 measurements of the three products on MI355X (48 to 512 rows, six
-// weights from 1024 x 1024 to 25600 x 5120, every tile height, 1 to 12
-// splits; rms 7%, and the plan it picks is 2% slower than the best measured
-// one on average, 19% at worst): a fixed part, then rounds of units over the
-// chip, a step taking longer the more of the chip runs, then the join.
-//   64 x 5120 x 5120    64-row tiles, 12 splits 20.2   256-row tiles 25.2
-//   128 x 25600 x 5120  64 rows 71, 128 rows, 2 splits 58.5, 256 rows 72
-//   512 x 25600 x 5120  64 rows 194, 128 rows 156, 256 rows, unsplit 122
+// Tile and K splits of one of the three products: tiles of `cols` output
+// columns, `products` sums over r, `words` fp32 partials an output (two for
+// the gated pair). The model, in microseconds, was fitted to 3200 measurements
+// of the three products on MI355X (48 to 512 rows, seven weights from 1024 x
+// 1024 to 25600 x 5120, every tile, 1 to 24 splits; rms 6.5%, and the plan it
+// picks is 2% slower than the best measured one on average, 16% at worst): a
+// fixed part, then rounds of units over the chip, a step taking longer the
+// more of the chip runs, then the join. Best of each tile, linear, us:
+//    64 x 5120 x 5120   k64 19.2   k128 22.8   k256 25.2
+//    64 x 5120 x 25600  k64 38.2   k128 45.3   k256 57.3
+//   128 x 25600 x 5120  k64 56.7   k128 58.5   k256 72
+//   512 x 25600 x 5120             k128 156    k256 122
 struct LayerPlan {
-  int mb, splits, steps_per_split;
+  int tile;                                  // TileId
+  int splits, steps_per_split;
   double cost;
 };
 struct TileCost {
-  int mb, slots;                             // slots: units at once on 256 CUs
+  int tile, rows, k_step, stages;
   double fixed, step_few, step_full, unit;   // step_few: when few CUs run
 };
-constexpr TileCost kTileCosts[] = {{8, 256, 8.8, 1.07, 1.20, 1.2},
-                                   {4, 256, 8.7, 0.77, 0.84, 0.4},
-                                   {2, 512, 7.3, 0.71, 1.15, 0.0}};
+template <int ID>
+constexpr TileCost tile_cost(double fixed, double few, double full, double unit) {
+  return TileCost{ID, 32 * Tile<ID>::kMB, kBK * Tile<ID>::kKS, Tile<ID>::kStages, fixed, few, full, unit};
+}
+constexpr TileCost kTileCosts[] = {tile_cost<k256>(9.3, 1.07, 1.20, 0.5), tile_cost<k128>(8.9, 0.77, 0.84, 0.0),
+                                   tile_cost<k64>(8.1, 1.03, 1.27, 0.0)};
+constexpr int kCus = 256;
 constexpr int kMaxSplits = 32;
 
-LayerPlan plan_tiles(int64_t m, int64_t n, int cols, int64_t steps, int words) {
-  LayerPlan best{8, 1, (int)steps, 1e300};
+// Steps of `products` sums over r, each padded to whole steps.
+int64_t steps_of(int64_t r, int products, int k_step) { return (r + k_step - 1) / k_step * products; }
+
+LayerPlan plan_tiles(int64_t m, int64_t n, int cols, int64_t r, int products, int words) {
+  LayerPlan best{k256, 1, 0, 1e300};
   for (const TileCost& t : kTileCosts) {
-    const int64_t tiles = ((m + 32 * t.mb - 1) / (32 * t.mb)) * ((n + cols - 1) / cols);
+    const int64_t tiles = ((m + t.rows - 1) / t.rows) * ((n + cols - 1) / cols);
+    const int64_t steps = steps_of(r, products, t.k_step);
     for (int sp = 1; sp <= kMaxSplits; ++sp) {
       const int64_t per = (steps + sp - 1) / sp;
-      if (sp > 1 && per < 4) break;
+      if (sp > 1 && per * t.k_step < 4 * kBK) break;
       const int64_t units = tiles * sp;
-      const int64_t rest = units % t.slots;
-      double cost = t.fixed + (double)(units / t.slots) * (per * t.step_full + t.unit);
-      if (rest > 0) {
-        // where two workgroups share a CU, one CU with two sets the time
-        const double fill = t.slots == 256 ? (double)rest / 256 : rest <= 256 ? 0.0 : 0.7 + 0.3 * (rest - 256) / 256;
-        cost += per * (t.step_few + (t.step_full - t.step_few) * fill) + t.unit;
-      }
-      if (sp > 1) cost += 1.0 + 1.2e-6 * (double)(m * n) * (sp * words + 1);
-      if (cost < best.cost) best = LayerPlan{t.mb, sp, (int)per, cost};
+      const int64_t rest = units % kCus;
+      double cost = t.fixed + (double)(units / kCus) * (per * t.step_full + t.unit);
+      if (rest > 0) cost += per * (t.step_few + (t.step_full - t.step_few) * (double)rest / kCus) + t.unit;
+      if (sp > 1) cost += 1.1 + 1e-6 * (double)(m * n) * (1.3 * sp * words + 1.0);
+      if (cost < best.cost) best = LayerPlan{t.tile, (int)((steps + per - 1) / per), (int)per, cost};
     }
   }
-  best.splits = (int)((steps + best.steps_per_split - 1) / best.steps_per_split);
   return best;
 }
 
@@ -122,46 +131,48 @@ struct ProductPlan {
   int parts;
   Part part[2];
 };
-ProductPlan plan_product(int64_t m, int64_t n, int cols, int64_t steps, int words) {
+ProductPlan plan_product(int64_t m, int64_t n, int cols, int64_t r, int products, int words) {
   const int tn = (int)((n + cols - 1) / cols);
-  ProductPlan best{1, {{0, tn, plan_tiles(m, n, cols, steps, words)}, {}}};
-  const TileCost& t = kTileCosts[0];
-  const int64_t tm = (m + 32 * t.mb - 1) / (32 * t.mb);
-  const int64_t rounds = tm * tn / t.slots, head = rounds * t.slots / tm;   // head: tile columns
+  ProductPlan best{1, {{0, tn, plan_tiles(m, n, cols, r, products, words)}, {}}};
+  const TileCost& t = kTileCosts[k256];
+  static_assert(kTileCosts[k256].tile == k256 && kTileCosts[k64].tile == k64, "the table is in the tiles' order");
+  const int64_t steps = steps_of(r, products, t.k_step);
+  const int64_t tm = (m + t.rows - 1) / t.rows;
+  const int64_t rounds = tm * tn / kCus, head = rounds * kCus / tm;   // head: tile columns
   if (rounds > 0 && head < tn) {
-    const LayerPlan h{t.mb, 1, (int)steps, t.fixed + (double)rounds * (steps * t.step_full + t.unit)};
-    const LayerPlan r = plan_tiles(m, n - head * cols, cols, steps, words);
-    if (h.cost + r.cost < 0.98 * best.part[0].plan.cost)
-      best = ProductPlan{2, {{0, (int)head, h}, {(int)head, (int)(tn - head), r}}};
+    const LayerPlan h{t.tile, 1, (int)steps, t.fixed + (double)rounds * (steps * t.step_full + t.unit)};
+    const LayerPlan rest = plan_tiles(m, n - head * cols, cols, r, products, words);
+    if (h.cost + rest.cost < 0.98 * best.part[0].plan.cost)
+      best = ProductPlan{2, {{0, (int)head, h}, {(int)head, (int)(tn - head), rest}}};
   }
   return best;
 }
 
 Grid grid_of(const Part& part, int64_t m, int64_t k) {
   const LayerPlan& p = part.plan;
-  const int stages = p.mb == 4 ? Tile<4>::kStages : Tile<8>::kStages;
-  static_assert(Tile<8>::kStages == Tile<2>::kStages, "two ring lengths");
-  return Grid{blocks_of(k), (int)((m + 32 * p.mb - 1) / (32 * p.mb)), part.tiles_n,
-              p.steps_per_split, p.splits, p.steps_per_split > stages - 1 ? p.steps_per_split : stages - 1};
+  const TileCost& t = kTileCosts[p.tile];
+  return Grid{blocks_of(k), (int)((m + t.rows - 1) / t.rows), part.tiles_n, p.steps_per_split, p.splits,
+              p.steps_per_split > t.stages - 1 ? p.steps_per_split : t.stages - 1};
 }
 
-// One persistent workgroup per slot walks its (tile, split) units.
-dim3 blocks_for(const LayerPlan& p, const Grid& g) {
+// One persistent workgroup a CU walks its (tile, split) units.
+dim3 blocks_for(const Grid& g) {
   const int64_t units = (int64_t)g.tiles_m * g.tiles_n * g.splits;
-  const int64_t slots = (int64_t)device_cus() * (p.mb == 2 ? Tile<2>::kPerCu : 1);
-  return dim3((uint32_t)(units < slots ? units : slots));
+  return dim3((uint32_t)(units < device_cus() ? units : device_cus()));
 }
 
-// Calls f with the tile height as a compile-time constant.
+// Calls f with the tile as a compile-time constant.
 template <int V>
 struct Const {
   static constexpr int value = V;
 };
 template <typename F>
-void with_rows(int mb, F&& f) {
-  if (mb == 8) f(Const<8>{});
-  else if (mb == 4) f(Const<4>{});
-  else f(Const<2>{});
+void with_tile(int tile, F&& f) {
+  switch (tile) {
+    case k256: return f(Const<k256>{});
+    case k128: return f(Const<k128>{});
+    default: return f(Const<k64>{});
+  }
 }
 
 // Workspace: split partials of [m, n] (one part at most is split).
@@ -187,56 +198,54 @@ hipError_t run_parts(const ProductPlan& p, int64_t m, int64_t k, int cols, size_
   return hipSuccess;
 }
 
-int64_t steps_of(int64_t r) { return (r + kBK - 1) / kBK; }
-
 }  // namespace
 
 // Which of a product's two kernels runs: the streams of gemm_layer_skinny.hip
 // (up to 32 rows) or the tiles. The streams start and end faster and keep more
 // codes in flight; the tiles read X once a workgroup instead of once a wave.
 // Measured on MI355X, stream against tiles, microseconds:
-//   linear  16 x 25600 x 5120  38.0  39.4    32 x 5120 x 5120  16.6  17.5
-//           32 x 12288 x 4096  24.8  21.3    32 x 25600 x 5120  53.1  40.5
-//   gated    4 x 25600 x 5120  39.3  49.9    16 x 12288 x 4096  22.8  26.9
-//           16 x 5120 x 25600  71.8  50.8    32 x 5120 x 2560  16.2  17.2
-//           32 x 5120 x 5120   27.6  21.1
+//   linear  16 x 25600 x 5120  38.2  38.1    32 x 5120 x 5120   16.7  17.6
+//           24 x 12288 x 4096  24    21.2    32 x 25600 x 5120  53    40.8
+//   gated    8 x 25600 x 5120  43    51.4    16 x 12288 x 4096  22.9  26.5
+//           16 x 5120 x 25600  72    51.1    32 x 5120 x 2560   16.6  17.3
+//           32 x 5120 x 5120   27.6  19.7
 //   input gradient (rows x weight rows x columns)
-//           16 x 12288 x 4096  17.9  22.0    16 x 25600 x 5120  40.5  37.4
-//           32 x 2048 x 4096   10.4  12.2    32 x 5120 x 5120   18.9  16.6
+//           16 x 12288 x 4096  17.7  21.1    16 x 25600 x 5120  40.5  36
+//           32 x 2048 x 4096   10.6  12.2    32 x 5120 x 5120   18.9  16.7
 enum Product { kLinear, kPair, kInputGradient };
 bool streams(Product p, int64_t m, int64_t codes) {
   if (m > 32) return false;
   switch (p) {
     case kLinear: return m <= 16 || codes <= (1 << 25);
-    case kPair: return m <= 4 || codes <= (m <= 16 ? 1 << 27 : 1 << 25);
+    case kPair: return m <= 8 || codes <= (m <= 16 ? 1 << 27 : 1 << 25);
     default: return codes <= (m <= 16 ? 1 << 26 : 1 << 23);
   }
 }
 
 size_t linear_act_bytes(int64_t m, int64_t n, int64_t k) {
   if (streams(kLinear, m, n * k)) return linear_act_skinny_bytes(m, n, k);
-  return partial_bytes(plan_product(m, n, kBN, steps_of(k), 1), m, n, 1);
+  return partial_bytes(plan_product(m, n, kBN, k, 1, 1), m, n, 1);
 }
 
 hipError_t launch_linear_act(const uint16_t* x, const uint8_t* q, const float* s, uint16_t* y,
                              const LayerEpilogue& ep, int64_t m, int64_t n, int64_t k, void* ws,
                              size_t ws_bytes, hipStream_t stream) {
   if (streams(kLinear, m, n * k)) return launch_linear_act_skinny(x, q, s, y, ep, m, n, k, ws, ws_bytes, stream);
-  const ProductPlan p = plan_product(m, n, kBN, steps_of(k), 1);
+  const ProductPlan p = plan_product(m, n, kBN, k, 1, 1);
   return run_parts(
       p, m, k, kBN, partial_bytes(p, m, n, 1), ws, ws_bytes,
       [&](const Part& part, const Grid& g, float* partials) {
         const LargeArgs la{ep, nullptr, 0, 0, part.tile0};
-        const dim3 grid = blocks_for(part.plan, g);
-        with_rows(part.plan.mb, [&](auto rows) {
-          constexpr int MB = decltype(rows)::value;
+        const dim3 grid = blocks_for(g);
+        with_tile(part.plan.tile, [&](auto tile) {
+          constexpr int ID = decltype(tile)::value;
           if (partials) {
-            hipLaunchKernelGGL((linear_act_kernel<true, kActNone, MB>), grid, dim3(kThreads), 0, stream, x, q, s,
+            hipLaunchKernelGGL((linear_act_kernel<true, kActNone, ID>), grid, dim3(kThreads), 0, stream, x, q, s,
                                y, partials, (int)m, (int)n, (int)k, g, la);
             return;
           }
           with_act(ep.act, [&](auto a) {
-            hipLaunchKernelGGL((linear_act_kernel<false, decltype(a)::value, MB>), grid, dim3(kThreads), 0, stream,
+            hipLaunchKernelGGL((linear_act_kernel<false, decltype(a)::value, ID>), grid, dim3(kThreads), 0, stream,
                                x, q, s, y, nullptr, (int)m, (int)n, (int)k, g, la);
           });
         });
@@ -248,28 +257,28 @@ hipError_t launch_linear_act(const uint16_t* x, const uint8_t* q, const float* s
 
 size_t glu_bytes(int64_t m, int64_t n, int64_t k) {
   if (streams(kPair, m, 2 * n * k)) return glu_skinny_bytes(m, n, k);
-  return partial_bytes(plan_product(m, n, kBN / 2, steps_of(k), 2), m, n, 2);
+  return partial_bytes(plan_product(m, n, kBN / 2, k, 1, 2), m, n, 2);
 }
 
 hipError_t launch_glu(const uint16_t* x, const uint8_t* qg, const float* sg, const uint8_t* qu,
                       const float* su, uint16_t* h, const LayerEpilogue& ep, int64_t m, int64_t n,
                       int64_t k, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (streams(kPair, m, 2 * n * k)) return launch_glu_skinny(x, qg, sg, qu, su, h, ep, m, n, k, ws, ws_bytes, stream);
-  const ProductPlan p = plan_product(m, n, kBN / 2, steps_of(k), 2);
+  const ProductPlan p = plan_product(m, n, kBN / 2, k, 1, 2);
   return run_parts(
       p, m, k, kBN / 2, partial_bytes(p, m, n, 2), ws, ws_bytes,
       [&](const Part& part, const Grid& g, float* partials) {
         const LargeArgs la{ep, nullptr, 0, 0, part.tile0};
-        const dim3 grid = blocks_for(part.plan, g);
-        with_rows(part.plan.mb, [&](auto rows) {
-          constexpr int MB = decltype(rows)::value;
+        const dim3 grid = blocks_for(g);
+        with_tile(part.plan.tile, [&](auto tile) {
+          constexpr int ID = decltype(tile)::value;
           if (partials) {
-            hipLaunchKernelGGL((glu_kernel<true, kActNone, MB>), grid, dim3(kThreads), 0, stream, x, qg, sg, qu,
+            hipLaunchKernelGGL((glu_kernel<true, kActNone, ID>), grid, dim3(kThreads), 0, stream, x, qg, sg, qu,
                                su, h, partials, (int)m, (int)n, (int)k, g, la);
             return;
           }
           with_act(ep.act, [&](auto a) {
-            hipLaunchKernelGGL((glu_kernel<false, decltype(a)::value, MB>), grid, dim3(kThreads), 0, stream, x, qg,
+            hipLaunchKernelGGL((glu_kernel<false, decltype(a)::value, ID>), grid, dim3(kThreads), 0, stream, x, qg,
                                sg, qu, su, h, nullptr, (int)m, (int)n, (int)k, g, la);
           });
         });
@@ -281,7 +290,7 @@ hipError_t launch_glu(const uint16_t* x, const uint8_t* qg, const float* sg, con
 
 size_t input_gradient_bytes(int64_t m, int64_t n, int64_t k, int products) {
   if (streams(kInputGradient, m, products * n * k)) return input_gradient_skinny_bytes(m, n, k, products);
-  return partial_bytes(plan_product(m, k, kBN, steps_of(n) * products, 1), m, k, 1);
+  return partial_bytes(plan_product(m, k, kBN, n, products, 1), m, k, 1);
 }
 
 hipError_t launch_input_gradient(const uint16_t* a, const uint8_t* q, const float* s, const uint16_t* a2,
@@ -291,19 +300,20 @@ hipError_t launch_input_gradient(const uint16_t* a, const uint8_t* q, const floa
   const int products = a2 ? 2 : 1;
   if (streams(kInputGradient, m, products * n * k))
     return launch_input_gradient_skinny(a, q, s, a2, q2, s2, lda, dx, m, n, k, ws, ws_bytes, stream);
-  const ProductPlan p = plan_product(m, k, kBN, steps_of(n) * products, 1);
+  const ProductPlan p = plan_product(m, k, kBN, n, products, 1);
   return run_parts(
       p, m, k, kBN, partial_bytes(p, m, k, 1), ws, ws_bytes,
       [&](const Part& part, const Grid& g, float* partials) {
-        const LargeArgs la{LayerEpilogue{}, a2, (int)lda, (int)steps_of(n), part.tile0};
-        const dim3 grid = blocks_for(part.plan, g);
-        with_rows(part.plan.mb, [&](auto rows) {
-          constexpr int MB = decltype(rows)::value;
+        const LargeArgs la{LayerEpilogue{}, a2, (int)lda,
+                           (int)steps_of(n, 1, kTileCosts[part.plan.tile].k_step), part.tile0};
+        const dim3 grid = blocks_for(g);
+        with_tile(part.plan.tile, [&](auto tile) {
+          constexpr int ID = decltype(tile)::value;
           if (partials)
-            hipLaunchKernelGGL((input_gradient_kernel<true, MB>), grid, dim3(kThreads), 0, stream, a, q, s, q2, s2,
+            hipLaunchKernelGGL((input_gradient_kernel<true, ID>), grid, dim3(kThreads), 0, stream, a, q, s, q2, s2,
                                dx, partials, (int)m, (int)k, (int)n, g, la);
           else
-            hipLaunchKernelGGL((input_gradient_kernel<false, MB>), grid, dim3(kThreads), 0, stream, a, q, s, q2,
+            hipLaunchKernelGGL((input_gradient_kernel<false, ID>), grid, dim3(kThreads), 0, stream, a, q, s, q2,
                                s2, dx, nullptr, (int)m, (int)k, (int)n, g, la);
         });
       },
