@@ -58,9 +58,16 @@ constexpr int vm_wait(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
 // gate (q, s) and the up (q2, s2) rows of the same 16 output columns, so both
 // sums of an output meet in one lane. With K splits that form writes the gate
 // partials to slabs 0, 2, .. and the up partials to slabs 1, 3, ..
+//
+// XLDS: X goes through LDS like the codes, whole 512-byte rows at a time, and
+// comes back in the operand's layout. Loaded straight into the operand's
+// registers, each 16 lanes touch 16 rows, and with 16 rows of X its loads take
+// as long as the codes'. The slots are twice as large (128 KB a workgroup), so
+// it is for grids of one workgroup a CU; the layer operators take it there
+// from five rows of X (gemm_layer_skinny.hip).
 enum SkinnyForm { kSkinnyPlain, kSkinnyLayer, kSkinnyGlu };
 
-template <int MT, int NT, int WAVES, int D, SkinnyForm FORM>
+template <int MT, int NT, int WAVES, int D, SkinnyForm FORM, bool XLDS = false>
 __device__ __forceinline__
 void gemm_skinny_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__ q,
                       const float* __restrict__ s, const uint8_t* __restrict__ q2,
@@ -73,7 +80,8 @@ void gemm_skinny_body(const uint16_t* __restrict__ x, const uint8_t* __restrict_
   static_assert((D - 1) * kLoads <= 63, "outstanding loads fit the vmcnt counter");
   static_assert(NT == 1 || NT == 2, "one or two 16-row tiles per workgroup");
   static_assert(kBlock % (16 * NT) == 0, "a workgroup's rows share one scale row");
-  __shared__ __attribute__((aligned(16))) uint8_t ring[WAVES][D][kSlot];
+  constexpr int kXSlot = XLDS ? MT * 16 * kSuper * 2 : 0;   // one super-step's X rows, where they go through LDS
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[WAVES][D][kSlot + kXSlot];
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
@@ -138,9 +146,23 @@ void gemm_skinny_body(const uint16_t* __restrict__ x, const uint8_t* __restrict_
   };
 
   u32x4 xv[D][MT][4][2];
+  // XLDS: load r brings X rows 2r and 2r + 1, 512 bytes each; 16-byte chunk c
+  // of row b is stored at c ^ (b % 16), so the reads (one chunk of 16 rows at a
+  // time) hit 16 distinct chunks of 256 bytes.
+  const int xr2 = lane >> 5, xp = lane & 31;
   auto issue = [&](int ss, int slot, u32x4 (&xa)[MT][4][2]) {
     const bool live = ss < ss1;
     const uint32_t kb = (uint32_t)(ss * kSuper);
+    uint8_t* base = wring + slot * (kSlot + kXSlot);
+    if constexpr (XLDS) {
+#pragma unroll
+      for (int r = 0; r < 8 * MT; ++r) {
+        const int row = 2 * r + xr2, c = xp ^ (row & 15);
+        const bool kin = live && (int)kb + c * 8 < K;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(xrs, (lds_ptr_t)(base + kSlot + r * 1024), 16,
+                                                 kin ? (uint32_t)((row * K + (int)kb + c * 8) * 2) : kOob, 0, 0, 0);
+      }
+    } else
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -150,7 +172,6 @@ void gemm_skinny_body(const uint16_t* __restrict__ x, const uint8_t* __restrict_
         xa[i][h][0] = buf_load16(xrs, kin ? o : kOob);
         xa[i][h][1] = buf_load16(xrs, kin ? o + 16 : kOob);
       }
-    uint8_t* base = wring + slot * kSlot;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 4 * r + lrow4;
@@ -177,7 +198,19 @@ void gemm_skinny_body(const uint16_t* __restrict__ x, const uint8_t* __restrict_
       t0 = kb < gk ? srow2[kb] : 0.0f;
       t1 = kb + 1 < gk ? srow2[kb + 1] : 0.0f;
     }
-    const uint8_t* base = wring + slot * kSlot;
+    const uint8_t* base = wring + slot * (kSlot + kXSlot);
+    u32x4 xl[MT][4][2];
+    if constexpr (XLDS) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            xl[i][h][e] = *reinterpret_cast<const u32x4*>(base + kSlot + (16 * i + bn) * 512 +
+                                                          (((2 * (bg + 4 * h) + e) ^ bn) << 4));
+    }
+    const u32x4 (&xo)[MT][4][2] = XLDS ? xl : xa;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const bool tl = j == 0 || live1;
@@ -190,8 +223,8 @@ void gemm_skinny_body(const uint16_t* __restrict__ x, const uint8_t* __restrict_
         const bf16x8 b1 = dequant8(c[2], c[3], sc);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-          ac[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xa[i][h][0]), b0, ac[i][j], 0, 0, 0);
-          ac[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xa[i][h][1]), b1, ac[i][j], 0, 0, 0);
+          ac[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xo[i][h][0]), b0, ac[i][j], 0, 0, 0);
+          ac[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xo[i][h][1]), b1, ac[i][j], 0, 0, 0);
         }
       }
     }
@@ -236,7 +269,7 @@ void gemm_skinny_body(const uint16_t* __restrict__ x, const uint8_t* __restrict_
   __syncthreads();
 
   f32x4* red = reinterpret_cast<f32x4*>(&ring[0][0][0]);   // [WAVES][MT * NT][64]
-  static_assert(WAVES * MT * NT * 64 * 16 <= WAVES * D * kSlot, "the cross-wave sum fits the ring");
+  static_assert(WAVES * MT * NT * 64 * 16 <= WAVES * D * (kSlot + kXSlot), "the cross-wave sum fits the ring");
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
