@@ -1,7 +1,7 @@
 // Activations of the layer operators and their derivatives, in fp32 (the
 // formulas are in fp8bl_layers.h). Exponentials and quotients run on the
 // hardware exp2 and reciprocal: a sigmoid is off by a relative
-// (|v| + 4) 2^-23 at most, far below the half step of the bf16 results
+// (2 |v| + 4) 2^-23 at most, far below the half step of the bf16 results
 // (2^-9) and of the same size as the fp32 sums' own rounding.
 #pragma once
 
@@ -11,12 +11,21 @@ namespace fp8bl {
 
 enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4 };
 
+constexpr float kLog2E = 1.44269504088896341f;
 __device__ __forceinline__ float sigmoid_f32(float v) {
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504088896341f));
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -kLog2E));
 }
 
 constexpr float kTanhA2 = 1.59576912160573071f;       // 2 sqrt(2 / pi)
 constexpr float kTanhB = 0.044715f;
+// The tanh form's p = 1 / (1 + e^-v), v = A2 t (1 + B t^2), with -A2 log2(e)
+// folded into the polynomial: the epilogue of many rows is bound by these
+// instructions.
+__device__ __forceinline__ float tanh_cdf(float t) {
+  constexpr double a = -1.59576912160573071 * 1.44269504088896341;
+  const float e = t * __builtin_fmaf(t * t, (float)(a * 0.044715), (float)a);
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(e));
+}
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 
 // The normal distribution's tail Phi(-a), a >= 0, with e = e^(-a^2/2):
@@ -27,7 +36,7 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 // took 150 us of 894 us in the epilogue of 8192 x 12288 x 4096. It keeps its
 // relative precision where Phi is small, as (1 + erf) / 2 would not.
 __device__ __forceinline__ float normal_tail(float a, float& e) {
-  e = __builtin_amdgcn_exp2f(a * a * (-0.5f * 1.44269504088896341f));
+  e = __builtin_amdgcn_exp2f(a * a * (-0.5f * kLog2E));
   const float s = __builtin_amdgcn_rcpf(__builtin_fmaf(0.35f, a, 1.0f));
   float p = 0.04890687018632889f;
   p = __builtin_fmaf(p, s, -0.2019839733839035f);
@@ -52,7 +61,7 @@ __device__ __forceinline__ float act_f32(float t) {
     float e;
     return t * normal_cdf(t, e);
   }
-  if constexpr (ACT == kActGeluTanh) return t * sigmoid_f32(kTanhA2 * (t + kTanhB * t * t * t));
+  if constexpr (ACT == kActGeluTanh) return t * tanh_cdf(t);
   return t;
 }
 
@@ -72,8 +81,9 @@ __device__ __forceinline__ float act_grad_f32(float t) {
     // Past |t| = 30 the derivative is 0 or 1 in fp32; the clamp keeps t^2
     // finite there (0 * inf otherwise).
     const float c = fminf(fmaxf(t, -30.0f), 30.0f);
-    const float p = sigmoid_f32(kTanhA2 * (c + kTanhB * c * c * c));
-    const float r = p + c * p * (1.0f - p) * (kTanhA2 * (1.0f + 3.0f * kTanhB * c * c));
+    const float p = tanh_cdf(c);
+    const float dv = __builtin_fmaf(c * c, 3.0f * kTanhB * kTanhA2, kTanhA2);
+    const float r = __builtin_fmaf(c * p, (1.0f - p) * dv, p);
     return t != t ? t : r;                              // fmin and fmax drop a NaN
   }
   return 1.0f;
