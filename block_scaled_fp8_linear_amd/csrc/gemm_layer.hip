@@ -4,9 +4,9 @@
 // weight's rows.
 //
 // All three are products of m rows with the decoded weight, sums in fp32. With
-// many rows the matrix instructions bound them, at 1.2 to 1.28 PFLOP/s, where
+// many rows the matrix instructions bound them, at 1.2 to 1.3 PFLOP/s, where
 // the plain linear on the same loop reaches 1.29 and a bf16 library product of
-// 8192^3 1.46: the MFMAs are busy 64 to 70% of the cycles (the issue of the
+// 8192^3 1.46: the MFMAs are busy 64 to 73% of the cycles (the issue of the
 // loads takes the rest) and the clock falls to 1.5 - 1.7 GHz. At some hundred
 // rows it is what a launch cannot spread: a tile costs about 9 us before its
 // first and after its last step, and tiles rarely fill whole rounds of 256 CUs.
@@ -44,7 +44,7 @@ struct Grid {
 // y = act(x W^T + bias) + residual, and z = x W^T + bias where it is saved:
 // bias, activation and residual on the fp32 sums in the epilogue, so that z is
 // written once and nothing is read back. (8192 x 12288 x 4096 with bias, tanh
-// GELU and z saved 688 us, 1.20 PFLOP/s; y alone, plain, 640. 512 x 5120 x
+// GELU and z saved 672 us, 1.23 PFLOP/s; y alone, plain, 630. 512 x 5120 x
 // 25600 with residual 129 us, 1.04 PFLOP/s; 512 x 5120 x 5120 41 us, of which
 // the join of its splits is 7.)
 template <bool SPLIT, int ACT, int ID>
@@ -77,7 +77,7 @@ void glu_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ qg, 
 // transposed copy of the weight nor a shuffle is needed, and one decode per
 // code feeds the tile's rows as in the forward. The two products of the gated
 // backward are one reduction of twice the length: one launch, one rounding.
-// (dx of 4096 x 12288 x 4096 323 us, 1.28 PFLOP/s; of the pair 4096 x 12800 x
+// (dx of 4096 x 12288 x 4096 311 - 323 us, 1.28 PFLOP/s and more; of the pair 4096 x 12800 x
 // 5120 851 us with the join, 1.26 PFLOP/s.)
 template <bool SPLIT, int ID>
 __global__ __launch_bounds__(kThreads, 1)
