@@ -228,33 +228,35 @@ hipError_t run_parts(const ProductPlan& p, int64_t m, int64_t k, int cols, size_
 // (up to 32 rows) or the tiles. The streams start and end faster and keep more
 // codes in flight; the tiles read X once a workgroup instead of once a wave.
 // Measured on MI355X, stream against tiles, microseconds:
-//   linear  16 x 25600 x 5120  38.2  38.1    32 x 5120 x 5120   16.7  17.6
-//           24 x 12288 x 4096  24    21.2    32 x 25600 x 5120  53    40.8
-//   gated    8 x 25600 x 5120  43    51.4    16 x 12288 x 4096  22.9  26.5
-//           16 x 5120 x 25600  72    51.1    32 x 5120 x 2560   16.6  17.3
-//           32 x 5120 x 5120   27.6  19.7
+//   linear  16 x 25600 x 5120  33.8  38.1    32 x 5120 x 5120   13.3  17.6
+//           32 x 8000 x 8192   20.4  22.5    32 x 25600 x 5120  46.4  39.1
+//   gated    8 x 25600 x 5120  42.4  51.4    16 x 25600 x 5120  47.5  55.5
+//           16 x 5120 x 25600  62.4  51.4    32 x 8192 x 2048   12.4    -
+//           32 x 5120 x 5120   21.9  19.9
 //   input gradient (rows x weight rows x columns)
 //           16 x 12288 x 4096  17.7  21.1    16 x 25600 x 5120  40.5  36
 //           32 x 2048 x 4096   10.6  12.2    32 x 5120 x 5120   18.9  16.7
+// (Pairs of nine to sixteen rows: past 2^27 codes the stream needs workgroups
+// for two a CU, one per 16 columns.)
 enum Product { kLinear, kPair, kInputGradient };
-bool streams(Product p, int64_t m, int64_t codes) {
+bool streams(Product p, int64_t m, int64_t n, int64_t codes) {
   if (m > 32) return false;
   switch (p) {
-    case kLinear: return m <= 16 || codes <= (1 << 25);
-    case kPair: return m <= 8 || codes <= (m <= 16 ? 1 << 27 : 1 << 25);
+    case kLinear: return m <= 16 || codes <= (1 << 26);
+    case kPair: return m <= 8 || codes <= (m <= 16 ? 1 << 27 : 1 << 25) || (m <= 16 && n >= 8192);
     default: return codes <= (m <= 16 ? 1 << 26 : 1 << 23);
   }
 }
 
 size_t linear_act_bytes(int64_t m, int64_t n, int64_t k) {
-  if (streams(kLinear, m, n * k)) return linear_act_skinny_bytes(m, n, k);
+  if (streams(kLinear, m, n, n * k)) return linear_act_skinny_bytes(m, n, k);
   return partial_bytes(plan_product(m, n, kBN, k, 1, 1), m, n, 1);
 }
 
 hipError_t launch_linear_act(const uint16_t* x, const uint8_t* q, const float* s, uint16_t* y,
                              const LayerEpilogue& ep, int64_t m, int64_t n, int64_t k, void* ws,
                              size_t ws_bytes, hipStream_t stream) {
-  if (streams(kLinear, m, n * k)) return launch_linear_act_skinny(x, q, s, y, ep, m, n, k, ws, ws_bytes, stream);
+  if (streams(kLinear, m, n, n * k)) return launch_linear_act_skinny(x, q, s, y, ep, m, n, k, ws, ws_bytes, stream);
   const ProductPlan p = plan_product(m, n, kBN, k, 1, 1);
   return run_parts(
       p, m, k, kBN, partial_bytes(p, m, n, 1), ws, ws_bytes,
@@ -280,14 +282,14 @@ hipError_t launch_linear_act(const uint16_t* x, const uint8_t* q, const float* s
 }
 
 size_t glu_bytes(int64_t m, int64_t n, int64_t k) {
-  if (streams(kPair, m, 2 * n * k)) return glu_skinny_bytes(m, n, k);
+  if (streams(kPair, m, n, 2 * n * k)) return glu_skinny_bytes(m, n, k);
   return partial_bytes(plan_product(m, n, kBN / 2, k, 1, 2), m, n, 2);
 }
 
 hipError_t launch_glu(const uint16_t* x, const uint8_t* qg, const float* sg, const uint8_t* qu,
                       const float* su, uint16_t* h, const LayerEpilogue& ep, int64_t m, int64_t n,
                       int64_t k, void* ws, size_t ws_bytes, hipStream_t stream) {
-  if (streams(kPair, m, 2 * n * k)) return launch_glu_skinny(x, qg, sg, qu, su, h, ep, m, n, k, ws, ws_bytes, stream);
+  if (streams(kPair, m, n, 2 * n * k)) return launch_glu_skinny(x, qg, sg, qu, su, h, ep, m, n, k, ws, ws_bytes, stream);
   const ProductPlan p = plan_product(m, n, kBN / 2, k, 1, 2);
   return run_parts(
       p, m, k, kBN / 2, partial_bytes(p, m, n, 2), ws, ws_bytes,
@@ -313,7 +315,7 @@ hipError_t launch_glu(const uint16_t* x, const uint8_t* qg, const float* sg, con
 }
 
 size_t input_gradient_bytes(int64_t m, int64_t n, int64_t k, int products) {
-  if (streams(kInputGradient, m, products * n * k)) return input_gradient_skinny_bytes(m, n, k, products);
+  if (streams(kInputGradient, m, n, products * n * k)) return input_gradient_skinny_bytes(m, n, k, products);
   return partial_bytes(plan_product(m, k, kBN, n, products, 1), m, k, 1);
 }
 
@@ -322,7 +324,7 @@ hipError_t launch_input_gradient(const uint16_t* a, const uint8_t* q, const floa
                                  int64_t m, int64_t n, int64_t k, void* ws, size_t ws_bytes,
                                  hipStream_t stream) {
   const int products = a2 ? 2 : 1;
-  if (streams(kInputGradient, m, products * n * k))
+  if (streams(kInputGradient, m, n, products * n * k))
     return launch_input_gradient_skinny(a, q, s, a2, q2, s2, lda, dx, m, n, k, ws, ws_bytes, stream);
   const ProductPlan p = plan_product(m, k, kBN, n, products, 1);
   return run_parts(

@@ -8,32 +8,59 @@ namespace fp8bl {
 
 namespace {
 
-// y = act(x W^T + bias) + residual on the sums that meet in LDS. Two workgroups
-// a CU (64 KB of LDS each) hold the registers to 256, which the loop's two
-// slots of codes and X need. (1 x 8000 x 8192 12.6 us, 5.2 TB/s of codes,
-// partly from the last-level cache; 16 x 5120 x 5120 with residual 10.8 us.
-// Eight waves where no CU has two workgroups, so half the iterations a wave:
-// 9.3 against 9.1 us at 1 x 5120 x 5120, 15.9 against 15.0 at 1 x 8000 x 8192.)
-template <int MT, bool XLDS>
-__global__ __launch_bounds__(kWaves * 64, XLDS ? 1 : 2)
+// How X is brought in (gemm_skinny_body.h), the K of a super-step, the ring's
+// slots and the workgroups a CU holds. X goes through LDS, but for up to four
+// rows of a gated pair or a small grid, where it is too little to matter.
+// Half-width super-steps keep such a workgroup at 64 KB, two to a CU, where the
+// grid has them, and leave 32 rows of X room for three slots. Microseconds, X
+// in registers / through LDS in steps of 256 K / of 128 K, two to a CU:
+//   linear   1 x 12288 x 4096  13.6    -   12.3    1 x 5120 x 25600  30.0    -   28.5
+//           16 x 12288 x 4096  17.3  17.5  15.1   16 x 25600 x 5120  37.5  37.9  33.8
+//           16 x 5120 x 5120   12.4  10.7  11.5   16 x 8000 x 8192   18.6  17.3  17.6
+//            1 x 5120 x 5120    9.1   9.2    -     8 x 5120 x 5120   11.1  10.2  10.9
+//   gated    1 x 25600 x 5120  36.8    -   38.4   16 x 12288 x 4096  22.1  23.1  19.2
+//            8 x 25600 x 5120  43.1  53.1  42.4   16 x 2560 x 5120   11.0   9.4   9.6
+// and of 17 to 32 rows, registers / LDS: linear 32 x 5120 x 5120 16.8 / 13.3,
+// 32 x 4096 x 8192 22.2 / 17.1, gated 32 x 2560 x 5120 15.6 / 11.9,
+// 32 x 8192 x 2048 14.4 / 12.4. (Four slots of 128 K: 12.3 at 16 x 5120 x 5120.)
+template <int MT_, bool LDS_, int KW_, int D_, int RESIDENT_>
+struct Path {
+  static constexpr int MT = MT_, KW = KW_, D = D_, kResident = RESIDENT_;
+  static constexpr bool kLds = LDS_;
+};
+template <typename F>
+void with_path(int64_t m, int64_t workgroups, bool gated, F&& f) {
+  if (m > 16) return f(Path<2, true, 128, 3, 1>{});
+  const bool many = workgroups > 256;          // CUs get two
+  if (m <= 4 && (gated || !many)) return f(Path<1, false, kSuper, kRing, 2>{});
+  return many ? f(Path<1, true, 128, 2, 2>{}) : f(Path<1, true, kSuper, kRing, 1>{});
+}
+
+// y = act(x W^T + bias) + residual on the sums that meet in LDS.
+// (1 x 8000 x 8192 12.6 us, 5.2 TB/s of codes, partly from the last-level
+// cache; 16 x 5120 x 5120 with residual 10.7 us. Eight waves where no CU has
+// two workgroups, so half the iterations a wave: 9.3 against 9.1 us at 1 x
+// 5120 x 5120, 15.9 against 15.0 at 1 x 8000 x 8192.)
+template <typename P>
+__global__ __launch_bounds__(kWaves * 64, P::kResident)
 void linear_act_skinny_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ q,
                               const float* __restrict__ s, uint16_t* y, float* __restrict__ part, int M,
                               int N, int K, int gk, int ss_per_split, LayerEpilogue ep) {
-  gemm_skinny_body<MT, 2, kWaves, kRing, kSkinnyLayer, XLDS>(x, q, s, nullptr, nullptr, y, part, M, N, K,
-                                                             gk, ss_per_split, ep);
+  gemm_skinny_body<P::MT, 2, kWaves, P::D, kSkinnyLayer, P::kLds, P::KW>(x, q, s, nullptr, nullptr, y, part, M, N,
+                                                                         K, gk, ss_per_split, ep);
 }
 
 // h = act(x Wg^T) (x Wu^T): of a workgroup's two 16-row tiles one is gate rows
 // and the other the up rows of the same 16 columns, so a lane ends with both
 // sums of its outputs. (1 x 25600 x 5120 43 us, 6.1 TB/s of codes.)
-template <int MT, bool XLDS>
-__global__ __launch_bounds__(kWaves * 64, XLDS ? 1 : 2)
+template <typename P>
+__global__ __launch_bounds__(kWaves * 64, P::kResident)
 void glu_skinny_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ qg,
                        const float* __restrict__ sg, const uint8_t* __restrict__ qu,
                        const float* __restrict__ su, uint16_t* h, float* __restrict__ part, int M, int N,
                        int K, int gk, int ss_per_split, LayerEpilogue ep) {
-  gemm_skinny_body<MT, 2, kWaves, kRing, kSkinnyGlu, XLDS>(x, qg, sg, qu, su, h, part, M, N, K, gk,
-                                                           ss_per_split, ep);
+  gemm_skinny_body<P::MT, 2, kWaves, P::D, kSkinnyGlu, P::kLds, P::KW>(x, qg, sg, qu, su, h, part, M, N, K, gk,
+                                                                       ss_per_split, ep);
 }
 
 // ---- Input gradient, dx[M,C] = a W (+ a2 W2), few rows: bound by the codes'
@@ -238,16 +265,6 @@ LayerPlan plan_layer(int64_t groups, int64_t k) {
   return p;
 }
 
-// X through LDS where no CU has two workgroups and X is a good part of the
-// bytes loaded (up to 16 rows). Microseconds, through registers and LDS:
-//   linear   1 x 5120 x 5120    9.1   9.2     16 x 5120 x 5120  12.4  10.8
-//            4 x 8000 x 8192   16.0  16.3     16 x 8000 x 8192  18.6  17.4
-//            8 x 5120 x 5120   11.1  10.3     16 x 4096 x 4096   9.7   8.7
-//   gated   16 x 2560 x 5120   11.0   9.4
-// and where CUs would have two: linear 16 x 12288 x 4096 17.7 and 17.5, gated
-// 8 x 25600 x 5120 43.1 and 53.1.
-bool x_through_lds(int64_t m, const dim3& grid) { return m > 4 && grid.x * grid.y <= 256; }
-
 }  // namespace
 
 size_t linear_act_skinny_bytes(int64_t m, int64_t n, int64_t k) {
@@ -263,16 +280,11 @@ hipError_t launch_linear_act_skinny(const uint16_t* x, const uint8_t* q, const f
   float* const part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
   const dim3 grid((uint32_t)((n + 31) / 32), (uint32_t)p.splits), block(kWaves * 64);
   const int gk = (int)((k + kBlock - 1) / kBlock);
-  const auto run = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, block, 0, stream, x, q, s, y, part, (int)m, (int)n, (int)k, gk, p.ss_per_split,
-                       ep);
-  };
-  if (m > 16)
-    run(linear_act_skinny_kernel<2, false>);
-  else if (x_through_lds(m, grid))
-    run(linear_act_skinny_kernel<1, true>);
-  else
-    run(linear_act_skinny_kernel<1, false>);
+  with_path(m, (int64_t)grid.x * grid.y, false, [&](auto path) {
+    using P = decltype(path);
+    hipLaunchKernelGGL((linear_act_skinny_kernel<P>), grid, block, 0, stream, x, q, s, y, part, (int)m, (int)n,
+                       (int)k, gk, p.ss_per_split * (kSuper / P::KW), ep);
+  });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   return launch_join_layer(part, y, p.splits, m, n, 0, ep, stream);
@@ -291,16 +303,11 @@ hipError_t launch_glu_skinny(const uint16_t* x, const uint8_t* qg, const float* 
   float* const part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
   const dim3 grid((uint32_t)((n + 15) / 16), (uint32_t)p.splits), block(kWaves * 64);
   const int gk = (int)((k + kBlock - 1) / kBlock);
-  const auto run = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, block, 0, stream, x, qg, sg, qu, su, h, part, (int)m, (int)n, (int)k, gk,
-                       p.ss_per_split, ep);
-  };
-  if (m > 16)
-    run(glu_skinny_kernel<2, false>);
-  else if (x_through_lds(m, grid))
-    run(glu_skinny_kernel<1, true>);
-  else
-    run(glu_skinny_kernel<1, false>);
+  with_path(m, (int64_t)grid.x * grid.y, true, [&](auto path) {
+    using P = decltype(path);
+    hipLaunchKernelGGL((glu_skinny_kernel<P>), grid, block, 0, stream, x, qg, sg, qu, su, h, part, (int)m, (int)n,
+                       (int)k, gk, p.ss_per_split * (kSuper / P::KW), ep);
+  });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   return launch_join_glu(part, h, p.splits, m, n, 0, ep, stream);

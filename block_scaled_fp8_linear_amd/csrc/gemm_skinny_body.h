@@ -62,12 +62,12 @@ constexpr int vm_wait(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
 // XLDS: X goes through LDS like the codes, whole 512-byte rows at a time, and
 // comes back in the operand's layout. Loaded straight into the operand's
 // registers, each 16 lanes touch 16 rows, and with 16 rows of X its loads take
-// as long as the codes'. The slots are twice as large (128 KB a workgroup), so
-// it is for grids of one workgroup a CU; the layer operators take it there
-// from five rows of X (gemm_layer_skinny.hip).
+// as long as the codes'. KW is the K of a super-step: 256, or 128 (128 bytes of
+// eight rows a code load) to halve the slots that then hold X too
+// (gemm_layer_skinny.hip has what the choices measured).
 enum SkinnyForm { kSkinnyPlain, kSkinnyLayer, kSkinnyGlu };
 
-template <int MT, int NT, int WAVES, int D, SkinnyForm FORM, bool XLDS = false>
+template <int MT, int NT, int WAVES, int D, SkinnyForm FORM, bool XLDS = false, int KW = kSuper>
 __device__ __forceinline__
 void gemm_skinny_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__ q,
                       const float* __restrict__ s, const uint8_t* __restrict__ q2,
@@ -75,12 +75,13 @@ void gemm_skinny_body(const uint16_t* __restrict__ x, const uint8_t* __restrict_
                       float* __restrict__ part, int M, int N, int K, int gk,
                       int ss_per_split, const LayerEpilogue& ep) {
   static_assert(FORM != kSkinnyGlu || NT == 2, "gate and up tiles");
-  constexpr int kSlot = NT * 16 * kSuper;         // one super-step's codes of the wave's tiles
-  constexpr int kLoads = NT * 4 + MT * 8;         // code and X loads per super-step
+  constexpr int kSlot = NT * 16 * KW;         // one super-step's codes of the wave's tiles
+  constexpr int kTileLoads = KW / 64;             // code loads of a 16-row tile, and its 64-wide K blocks
+  constexpr int kLoads = (NT + 2 * MT) * kTileLoads;         // code and X loads per super-step
   static_assert((D - 1) * kLoads <= 63, "outstanding loads fit the vmcnt counter");
   static_assert(NT == 1 || NT == 2, "one or two 16-row tiles per workgroup");
   static_assert(kBlock % (16 * NT) == 0, "a workgroup's rows share one scale row");
-  constexpr int kXSlot = XLDS ? MT * 16 * kSuper * 2 : 0;   // one super-step's X rows, where they go through LDS
+  constexpr int kXSlot = XLDS ? MT * 16 * KW * 2 : 0;   // one super-step's X rows, where they go through LDS
   __shared__ __attribute__((aligned(1024))) uint8_t ring[WAVES][D][kSlot + kXSlot];
 
   const int tid = threadIdx.x;
@@ -88,7 +89,7 @@ void gemm_skinny_body(const uint16_t* __restrict__ x, const uint8_t* __restrict_
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   constexpr int kCols = FORM == kSkinnyGlu ? 16 : 16 * NT;   // output columns of the workgroup
   const int n0 = blockIdx.x * kCols;
-  const int nss = (K + kSuper - 1) / kSuper;
+  const int nss = (K + KW - 1) / KW;
   const int ss0 = blockIdx.y * ss_per_split;
   const int ss1 = min(ss0 + ss_per_split, nss);
   // No lambda below captures an array whose size is a template parameter
@@ -109,13 +110,17 @@ void gemm_skinny_body(const uint16_t* __restrict__ x, const uint8_t* __restrict_
   // Code loads: instruction r of tile j brings rows 4r..4r+3, 256 bytes
   // each; lane i lands at byte 16*i of the instruction's 1 KB of the slot
   // and fetches logical chunk (i & 15) ^ row.
-  const int lrow4 = lane >> 4;
-  const int lchk = lane & 15;
-  uint32_t woff[4];       // tile 0's; tile j adds j * 16 rows
+  constexpr int kRowsLoad = 1024 / KW;            // rows of a load
+  constexpr int kChunks = KW / 16;                // 16-byte chunks of a row
+  const int lrow4 = lane / kChunks;
+  const int lchk = lane % kChunks;
+  // (the swizzle's key of a row: 16 rows of one chunk in 16 distinct chunks of 256 bytes)
+  auto wkey = [](int row) { return KW == 256 ? row : (row >> 1) & 7; };
+  uint32_t woff[4];       // (the first kTileLoads) tile 0's; tile j adds j * 16 rows
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int row = 4 * r + lrow4;
-    woff[r] = (uint32_t)(row * K + (lchk ^ row) * 16);
+  for (int r = 0; r < kTileLoads; ++r) {
+    const int row = kRowsLoad * r + lrow4;
+    woff[r] = (uint32_t)(row * K + (lchk ^ wkey(row)) * 16);
   }
   const uint32_t tile_stride = (uint32_t)(16 * K);
   const int bn = lane & 15;
@@ -145,19 +150,20 @@ void gemm_skinny_body(const uint16_t* __restrict__ x, const uint8_t* __restrict_
     return ss0 + (r >= count ? r - count : r);
   };
 
-  u32x4 xv[D][MT][4][2];
-  // XLDS: load r brings X rows 2r and 2r + 1, 512 bytes each; 16-byte chunk c
-  // of row b is stored at c ^ (b % 16), so the reads (one chunk of 16 rows at a
-  // time) hit 16 distinct chunks of 256 bytes.
-  const int xr2 = lane >> 5, xp = lane & 31;
-  auto issue = [&](int ss, int slot, u32x4 (&xa)[MT][4][2]) {
+  u32x4 xv[D][MT][kTileLoads][2];
+  // XLDS: a load brings 1 KB of X rows of 2 KW bytes; 16-byte chunk c of row b
+  // is stored at c ^ (b % 16), so the reads (one chunk of 16 rows at a time)
+  // hit 16 distinct chunks of 256 bytes.
+  constexpr int kXRow = 2 * KW, kXChunks = KW / 8;
+  const int xr2 = lane / kXChunks, xp = lane % kXChunks;
+  auto issue = [&](int ss, int slot, u32x4 (&xa)[MT][kTileLoads][2]) {
     const bool live = ss < ss1;
-    const uint32_t kb = (uint32_t)(ss * kSuper);
+    const uint32_t kb = (uint32_t)(ss * KW);
     uint8_t* base = wring + slot * (kSlot + kXSlot);
     if constexpr (XLDS) {
 #pragma unroll
-      for (int r = 0; r < 8 * MT; ++r) {
-        const int row = 2 * r + xr2, c = xp ^ (row & 15);
+      for (int r = 0; r < 2 * kTileLoads * MT; ++r) {
+        const int row = (1024 / kXRow) * r + xr2, c = xp ^ (row & 15);
         const bool kin = live && (int)kb + c * 8 < K;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(xrs, (lds_ptr_t)(base + kSlot + r * 1024), 16,
                                                  kin ? (uint32_t)((row * K + (int)kb + c * 8) * 2) : kOob, 0, 0, 0);
@@ -166,59 +172,59 @@ void gemm_skinny_body(const uint16_t* __restrict__ x, const uint8_t* __restrict_
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
+      for (int h = 0; h < kTileLoads; ++h) {
         const bool kin = live && (int)kb + (bg + 4 * h) * 16 < K;
         const uint32_t o = xoff + i * xtile_stride + (kb + (uint32_t)(64 * h)) * 2;
         xa[i][h][0] = buf_load16(xrs, kin ? o : kOob);
         xa[i][h][1] = buf_load16(xrs, kin ? o + 16 : kOob);
       }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 4 * r + lrow4;
-      const bool kin = live && (int)kb + ((lchk ^ row) * 16) < K;
+    for (int r = 0; r < kTileLoads; ++r) {
+      const int row = kRowsLoad * r + lrow4;
+      const bool kin = live && (int)kb + ((lchk ^ wkey(row)) * 16) < K;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
         if (FORM == kSkinnyGlu && j == 1)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(wrs2, (lds_ptr_t)(base + j * 16 * kSuper + r * 1024), 16,
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(wrs2, (lds_ptr_t)(base + j * 16 * KW + r * 1024), 16,
                                                    kin ? woff[r] + kb : kOob, 0, 0, kNonTemporal);
         else
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(wrs, (lds_ptr_t)(base + j * 16 * kSuper + r * 1024), 16,
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(wrs, (lds_ptr_t)(base + j * 16 * KW + r * 1024), 16,
                                                    kin ? woff[r] + j * tile_stride + kb : kOob, 0, 0, kNonTemporal);
     }
   };
-  auto compute = [&](int ss, int slot, const u32x4 (&xa)[MT][4][2], f32x4 (&ac)[MT][NT]) {
+  auto compute = [&](int ss, int slot, const u32x4 (&xa)[MT][kTileLoads][2], f32x4 (&ac)[MT][NT]) {
     // A super-step spans two 128-column scale blocks: logical chunks 0..7
     // (h = 0, 1) take the first, chunks 8..15 (h = 2, 3) the second. A K
     // tail never reads the second block's scale unless it exists.
-    const int kb = 2 * ss;
+    const int kb = KW / kBlock * ss;
     const float s0 = kb < gk ? srow[kb] : 0.0f;
-    const float s1 = kb + 1 < gk ? srow[kb + 1] : 0.0f;
+    const float s1 = KW > kBlock && kb + 1 < gk ? srow[kb + 1] : 0.0f;
     float t0 = s0, t1 = s1;          // tile 1's
     if constexpr (FORM == kSkinnyGlu) {
       t0 = kb < gk ? srow2[kb] : 0.0f;
-      t1 = kb + 1 < gk ? srow2[kb + 1] : 0.0f;
+      t1 = KW > kBlock && kb + 1 < gk ? srow2[kb + 1] : 0.0f;
     }
     const uint8_t* base = wring + slot * (kSlot + kXSlot);
-    u32x4 xl[MT][4][2];
+    u32x4 xl[MT][kTileLoads][2];
     if constexpr (XLDS) {
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
+        for (int h = 0; h < kTileLoads; ++h)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            xl[i][h][e] = *reinterpret_cast<const u32x4*>(base + kSlot + (16 * i + bn) * 512 +
+            xl[i][h][e] = *reinterpret_cast<const u32x4*>(base + kSlot + (16 * i + bn) * kXRow +
                                                           (((2 * (bg + 4 * h) + e) ^ bn) << 4));
     }
-    const u32x4 (&xo)[MT][4][2] = XLDS ? xl : xa;
+    const u32x4 (&xo)[MT][kTileLoads][2] = XLDS ? xl : xa;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const bool tl = j == 0 || live1;
-      const uint8_t* slab = base + j * 16 * kSuper;
+      const uint8_t* slab = base + j * 16 * KW;
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
+      for (int h = 0; h < kTileLoads; ++h) {
         const float sc = tl ? (h < 2 ? (j ? t0 : s0) : (j ? t1 : s1)) : 0.0f;
-        const u32x4 c = *reinterpret_cast<const u32x4*>(slab + bn * kSuper + (((bg + 4 * h) ^ bn) << 4));
+        const u32x4 c = *reinterpret_cast<const u32x4*>(slab + bn * KW + (((bg + 4 * h) ^ wkey(bn)) << 4));
         const bf16x8 b0 = dequant8(c[0], c[1], sc);
         const bf16x8 b1 = dequant8(c[2], c[3], sc);
 #pragma unroll

@@ -54,8 +54,9 @@ SHAPES = [
     (16, 520, 1040), (17, 64, 4096), (31, 300, 8208), (32, 257, 512), (33, 256, 528), (64, 384, 256),
     (77, 1003, 656), (128, 128, 128), (130, 300, 1040), (200, 1288, 144), (257, 520, 784),
     (300, 36, 2320), (513, 1028, 336), (1025, 264, 80),
-    # five to sixteen rows: X through LDS in grids of up to 256 workgroups, else through registers
-    (4, 72, 1296), (6, 299, 1168), (11, 4112, 336), (15, 33, 4368), (16, 8193, 144), (16, 8225, 272),
+    # few rows in grids of up to and past 256 workgroups, whose X takes different ways
+    (3, 8200, 400), (4, 72, 1296), (6, 299, 1168), (11, 4112, 336), (15, 33, 4368), (16, 8193, 144),
+    (16, 8225, 272), (18, 8225, 144), (29, 4112, 912), (32, 40, 2064),
 ]
 IDS = ["x".join(map(str, s)) for s in SHAPES]
 
@@ -212,7 +213,7 @@ def test_activation_values(act):
     assert bool((off <= R.HALF * want.abs() + R.EVAL * t.abs().clamp_max(100) + R.TINY).all()), float(off.max())
 
 
-ROUTES = [(1, 264, 512), (7, 299, 1168), (20, 136, 1040), (77, 1003, 656), (300, 264, 528)]
+ROUTES = [(1, 264, 512), (7, 299, 1168), (3, 8200, 144), (20, 136, 1040), (77, 1003, 656), (300, 264, 528)]
 
 
 @pytest.mark.parametrize("shape", ROUTES, ids=["x".join(map(str, s)) for s in ROUTES])
