@@ -175,9 +175,11 @@ void input_gradient_skinny_kernel(const uint16_t* __restrict__ a, const uint8_t*
   issue(iters > 0 ? st_of(0) : st1, 0, xv[0]);
   int i0 = 0;
   for (; i0 + 2 <= iters; i0 += 2) {
+    __builtin_amdgcn_s_waitcnt(kLgkmWait0);        // the slot's reads have returned
     issue(st_of(i0 + 1), 1, xv[1]);
     __builtin_amdgcn_s_waitcnt(vm_wait(kLoads));
     compute(st_of(i0), 0, xv[0], acc);
+    __builtin_amdgcn_s_waitcnt(kLgkmWait0);        // the slot's reads have returned
     issue(i0 + 2 < iters ? st_of(i0 + 2) : st1, 0, xv[0]);
     __builtin_amdgcn_s_waitcnt(vm_wait(kLoads));
     compute(st_of(i0 + 1), 1, xv[1], acc);

@@ -35,6 +35,7 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 // expcnt[6:4], lgkmcnt[11:8]): at most n vector-memory operations of this
 // wave outstanding, no wait on the others.
 constexpr int vm_wait(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
+constexpr int kLgkmWait0 = 0xC07F;         // lgkmcnt(0) only
 
 // The codes go global -> LDS directly into a ring of D slots per wave, X
 // into D register sets, and each super-step's X loads are issued ahead of
@@ -253,6 +254,9 @@ void gemm_skinny_body(const uint16_t* __restrict__ x, const uint8_t* __restrict_
 #pragma unroll
     for (int u = 0; u < D; ++u) {
       const int nslot = (u + kAhead) % D;
+      // Its last reads have returned: the loads write LDS on their own, and
+      // the compiler orders a read before them, not its data.
+      __builtin_amdgcn_s_waitcnt(kLgkmWait0);
       issue(ss_of(wave + (i0 + u + kAhead) * WAVES), nslot, xv[nslot]);
       __builtin_amdgcn_s_waitcnt(vm_wait(kAhead * kLoads));
       compute(ss_of(wave + (i0 + u) * WAVES), u, xv[u], acc);
