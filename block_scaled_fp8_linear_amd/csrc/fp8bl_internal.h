@@ -122,9 +122,9 @@ hipError_t launch_input_gradient(const uint16_t* a, const uint8_t* q, const floa
                                  const uint8_t* q2, const float* s2, int64_t lda, uint16_t* dx,
                                  int64_t m, int64_t n, int64_t k, void* ws, size_t ws_bytes,
                                  hipStream_t stream);
-// The three at few rows (m <= 32), and joins of split partials (slab stride
-// partial_slab(m, n)) with an epilogue, over columns c0 .. n; the pair's
-// partials alternate gate and up slabs.
+// The three at few rows (m <= 32), and joins of split partials with an
+// epilogue, over columns c0 .. n: the partials are [m, n - c0] slabs of those
+// columns, partial_slab(m, n - c0) apart; the pair's alternate gate and up.
 size_t linear_act_skinny_bytes(int64_t m, int64_t n, int64_t k);
 hipError_t launch_linear_act_skinny(const uint16_t* x, const uint8_t* q, const float* s, uint16_t* y,
                                     const LayerEpilogue& ep, int64_t m, int64_t n, int64_t k, void* ws,

@@ -61,7 +61,8 @@ struct LargeArgs {
   const uint16_t* x2;        // kGradient: the second product's left operand
   int ldx;                   // kGradient: row stride of x and x2, elements (a multiple of 8)
   int steps1;                // kGradient: steps of one product
-  int tile0;                 // first tile column of the launch (tiles_n counts from it)
+  int tile0;                 // first tile column of the launch (tiles_n counts from it); split
+                             // partials hold the columns from it on
 };
 
 // (q, s) is the weight; for GATED and kGlu it is the gate weight and (q2, s2)
@@ -124,6 +125,9 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
   const int my_units = (units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
   const int nkt = FORM == kGradient && la.x2 ? 2 * la.steps1 : (K + kStep - 1) / kStep;
   const int ldx = FORM == kGradient ? la.ldx : K;    // row stride of X
+  // Split partials are [M, PN] slabs of the launch's columns, pc0 .. N.
+  const int pc0 = FORM == kPlain ? 0 : la.tile0 * kTileN;
+  const int PN = N - pc0;
   struct Unit {
     int m0, n0, kt0, nreal, split;
   };
@@ -651,13 +655,12 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
       auto get = [&](int r, int c) -> u32x4 {
         return *reinterpret_cast<const u32x4*>(buf + r * 256 + ((c ^ (r & 15)) << 4));
       };
-      const size_t tile = (size_t)CU.m0 * N;
       const bool quad = FORM == kGradient || (N & 3) == 0;    // (kGradient: a multiple of 16 always)
       if constexpr (SPLIT) {
         // fp32 partials: slab `split`, for kGlu slabs 2 split (gate) and 2 split + 1 (up)
-        const size_t slab = partial_slab(M, N);
-        float* const p0 = part + (size_t)(FORM == kGlu ? 2 * CU.split : CU.split) * slab + tile;
-        const uint32_t range = (uint32_t)(rows * N * 4);
+        const size_t slab = partial_slab(M, PN);
+        float* const p0 = part + (size_t)(FORM == kGlu ? 2 * CU.split : CU.split) * slab + (size_t)CU.m0 * PN;
+        const uint32_t range = (uint32_t)(rows * PN * 4);
         const __amdgpu_buffer_rsrc_t prs = make_rsrc(p0, range);
         const __amdgpu_buffer_rsrc_t prs2 = make_rsrc(p0 + slab, FORM == kGlu ? range : 0);
 #pragma unroll
@@ -671,7 +674,7 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
               const u32x4 v = get(r, cc);
               u32x4 v2 = {};
               if (FORM == kGlu) v2 = get(r, cc + 8);
-              const uint32_t at = (uint32_t)(((32 * mb + kEpiRows * hf + r) * N + col4) * 4);
+              const uint32_t at = (uint32_t)(((32 * mb + kEpiRows * hf + r) * PN + col4 - pc0) * 4);
               if (quad) {
                 const uint32_t off = col4 < N ? at : kOob;
                 __builtin_amdgcn_raw_buffer_store_b128(v, prs, off, 0, 0);
@@ -688,6 +691,7 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
             }
           }
       } else {
+        const size_t tile = (size_t)CU.m0 * N;
         const uint32_t range = (uint32_t)(rows * N * 2);
         const __amdgpu_buffer_rsrc_t yrs = make_rsrc(y + tile, range);
         // (an absent array: no range, so nothing is read or written)
@@ -852,8 +856,8 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
       }
     } else {
       const __amdgpu_buffer_rsrc_t prs =
-          make_rsrc(part + (size_t)CU.split * partial_slab(M, N) + (size_t)CU.m0 * N,
-                    (uint32_t)(rows * N * 4));
+          make_rsrc(part + (size_t)CU.split * partial_slab(M, PN) + (size_t)CU.m0 * PN,
+                    (uint32_t)(rows * PN * 4));
       if (FORM == kGradient || (N & 3) == 0) {   // (kGradient: a multiple of 16 always)
         // fp32 partials through the same LDS slice, as whole lines: each
         // 32-row block of this wave's 256 x 64 slice row-major in its 8 KB
@@ -884,7 +888,7 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
           for (int j = 0; j < 8; ++j) {
             const int r = 4 * j + rq;
             const u32x4 v = *reinterpret_cast<const u32x4*>(buf + r * 256 + ((cc ^ (r & 15)) << 4));
-            const uint32_t off = col4 < N ? (uint32_t)(((32 * mb + r) * N + col4) * 4) : kOob;
+            const uint32_t off = col4 < N ? (uint32_t)(((32 * mb + r) * PN + col4 - pc0) * 4) : kOob;
             __builtin_amdgcn_raw_buffer_store_b128(v, prs, off, 0, 0);
           }
         }
@@ -896,7 +900,7 @@ void gemm_large_body(const uint16_t* __restrict__ x, const uint8_t* __restrict__
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
               const int col = col_base + 32 * nb + 8 * (r >> 2) + (r & 3);
-              const uint32_t off = col < N ? (uint32_t)(((arow + 32 * mb) * N + col) * 4) : kOob;
+              const uint32_t off = col < N ? (uint32_t)(((arow + 32 * mb) * PN + col - pc0) * 4) : kOob;
               __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[nb][mb][r]), prs, off, 0, 0);
               __builtin_amdgcn_sched_barrier(0);
             }

@@ -199,10 +199,14 @@ void with_tile(int tile, F&& f) {
   }
 }
 
-// Workspace: split partials of [m, n] (one part at most is split).
-size_t partial_bytes(const ProductPlan& p, int64_t m, int64_t n, int words) {
-  const int splits = p.part[p.parts - 1].plan.splits;
-  return splits <= 1 ? 0 : round_up((size_t)splits * words * partial_slab(m, n) * sizeof(float), kWorkspaceAlign);
+// Workspace: split partials of the last part's columns (no other part is
+// split; 4096 x 12800 x 5120 backward needs 64 MiB so, and 320 for all columns).
+size_t partial_bytes(const ProductPlan& p, int64_t m, int64_t n, int cols, int words) {
+  const Part& last = p.part[p.parts - 1];
+  const int64_t width = n - (int64_t)last.tile0 * cols;
+  return last.plan.splits <= 1
+             ? 0
+             : round_up((size_t)last.plan.splits * words * partial_slab(m, width) * sizeof(float), kWorkspaceAlign);
 }
 
 // Runs a plan: `product(part, grid, partials or null)` launches one part,
@@ -250,7 +254,7 @@ bool streams(Product p, int64_t m, int64_t n, int64_t codes) {
 
 size_t linear_act_bytes(int64_t m, int64_t n, int64_t k) {
   if (streams(kLinear, m, n, n * k)) return linear_act_skinny_bytes(m, n, k);
-  return partial_bytes(plan_product(m, n, kBN, k, 1, 1), m, n, 1);
+  return partial_bytes(plan_product(m, n, kBN, k, 1, 1), m, n, kBN, 1);
 }
 
 hipError_t launch_linear_act(const uint16_t* x, const uint8_t* q, const float* s, uint16_t* y,
@@ -259,7 +263,7 @@ hipError_t launch_linear_act(const uint16_t* x, const uint8_t* q, const float* s
   if (streams(kLinear, m, n, n * k)) return launch_linear_act_skinny(x, q, s, y, ep, m, n, k, ws, ws_bytes, stream);
   const ProductPlan p = plan_product(m, n, kBN, k, 1, 1);
   return run_parts(
-      p, m, k, kBN, partial_bytes(p, m, n, 1), ws, ws_bytes,
+      p, m, k, kBN, partial_bytes(p, m, n, kBN, 1), ws, ws_bytes,
       [&](const Part& part, const Grid& g, float* partials) {
         const LargeArgs la{ep, nullptr, 0, 0, part.tile0};
         const dim3 grid = blocks_for(g);
@@ -283,7 +287,7 @@ hipError_t launch_linear_act(const uint16_t* x, const uint8_t* q, const float* s
 
 size_t glu_bytes(int64_t m, int64_t n, int64_t k) {
   if (streams(kPair, m, n, 2 * n * k)) return glu_skinny_bytes(m, n, k);
-  return partial_bytes(plan_product(m, n, kBN / 2, k, 1, 2), m, n, 2);
+  return partial_bytes(plan_product(m, n, kBN / 2, k, 1, 2), m, n, kBN / 2, 2);
 }
 
 hipError_t launch_glu(const uint16_t* x, const uint8_t* qg, const float* sg, const uint8_t* qu,
@@ -292,7 +296,7 @@ hipError_t launch_glu(const uint16_t* x, const uint8_t* qg, const float* sg, con
   if (streams(kPair, m, n, 2 * n * k)) return launch_glu_skinny(x, qg, sg, qu, su, h, ep, m, n, k, ws, ws_bytes, stream);
   const ProductPlan p = plan_product(m, n, kBN / 2, k, 1, 2);
   return run_parts(
-      p, m, k, kBN / 2, partial_bytes(p, m, n, 2), ws, ws_bytes,
+      p, m, k, kBN / 2, partial_bytes(p, m, n, kBN / 2, 2), ws, ws_bytes,
       [&](const Part& part, const Grid& g, float* partials) {
         const LargeArgs la{ep, nullptr, 0, 0, part.tile0};
         const dim3 grid = blocks_for(g);
@@ -316,7 +320,7 @@ hipError_t launch_glu(const uint16_t* x, const uint8_t* qg, const float* sg, con
 
 size_t input_gradient_bytes(int64_t m, int64_t n, int64_t k, int products) {
   if (streams(kInputGradient, m, n, products * n * k)) return input_gradient_skinny_bytes(m, n, k, products);
-  return partial_bytes(plan_product(m, k, kBN, n, products, 1), m, k, 1);
+  return partial_bytes(plan_product(m, k, kBN, n, products, 1), m, k, kBN, 1);
 }
 
 hipError_t launch_input_gradient(const uint16_t* a, const uint8_t* q, const float* s, const uint16_t* a2,
@@ -328,7 +332,7 @@ hipError_t launch_input_gradient(const uint16_t* a, const uint8_t* q, const floa
     return launch_input_gradient_skinny(a, q, s, a2, q2, s2, lda, dx, m, n, k, ws, ws_bytes, stream);
   const ProductPlan p = plan_product(m, k, kBN, n, products, 1);
   return run_parts(
-      p, m, k, kBN, partial_bytes(p, m, k, 1), ws, ws_bytes,
+      p, m, k, kBN, partial_bytes(p, m, k, kBN, 1), ws, ws_bytes,
       [&](const Part& part, const Grid& g, float* partials) {
         const LargeArgs la{LayerEpilogue{}, a2, (int)lda,
                            (int)steps_of(n, 1, kTileCosts[part.plan.tile].k_step), part.tile0};

@@ -1,5 +1,5 @@
-// Joins of split partials ([splits][M,N] fp32 slabs) with the layer operators'
-// epilogues: the partials are added in split order, then bias, activation,
+// Joins of split partials (fp32 slabs of the split columns) with the layer
+// operators' epilogues: the partials are added in split order, then bias, activation,
 // residual (or the gate's product) and one rounding of each output. Bound by
 // the partials' bytes, or with few rows by the latency of one thread's loads:
 // eight splits' loads are in flight at once, and small outputs use narrower
@@ -96,7 +96,8 @@ __device__ __forceinline__ Row<VEC> sum_splits(const float* p, size_t stride, in
   return t;
 }
 
-// Columns c0 .. n of every row (`count` outputs; width n - c0).
+// Columns c0 .. n of every row (`count` outputs). The partials are [m, n - c0]
+// slabs: output f of the columns is element f of each.
 template <int ACT, int VEC, bool GLU>
 __global__ __launch_bounds__(kThreads)
 void join_kernel(const float* __restrict__ part, uint16_t* y, int splits, size_t count, size_t slab,
@@ -109,8 +110,8 @@ void join_kernel(const float* __restrict__ part, uint16_t* y, int splits, size_t
     const uint32_t col = c0 + (uint32_t)(f - row * width);
     const size_t i = row * n + col;
     if constexpr (GLU) {
-      const Row<VEC> g = sum_splits<VEC>(part + i, 2 * slab, splits);
-      const Row<VEC> u = sum_splits<VEC>(part + slab + i, 2 * slab, splits);
+      const Row<VEC> g = sum_splits<VEC>(part + f, 2 * slab, splits);
+      const Row<VEC> u = sum_splits<VEC>(part + slab + f, 2 * slab, splits);
       if (ep.g) {
         store_bf16<VEC>(ep.g + i, g);
         store_bf16<VEC>(ep.u + i, u);
@@ -122,7 +123,7 @@ void join_kernel(const float* __restrict__ part, uint16_t* y, int splits, size_t
     } else {
       Row<VEC> res;
       if (ep.residual) res = load_bf16<VEC>(ep.residual + i);
-      Row<VEC> t = sum_splits<VEC>(part + i, slab, splits);
+      Row<VEC> t = sum_splits<VEC>(part + f, slab, splits);
       if (ep.bias) {
         const Row<VEC> b = load_bf16<VEC>(ep.bias + col);
 #pragma unroll
@@ -147,7 +148,7 @@ hipError_t launch(const float* part, uint16_t* y, int splits, int64_t m, int64_t
   const dim3 grid((uint32_t)(blocks < (1u << 20) ? blocks : (1u << 20)));
   with_act(ep.act, [&](auto a) {
     hipLaunchKernelGGL((join_kernel<decltype(a)::value, VEC, GLU>), grid, dim3(kThreads), 0, stream, part, y,
-                       splits, count, partial_slab((size_t)m, (size_t)n), (uint32_t)n, (uint32_t)c0, ep);
+                       splits, count, partial_slab((size_t)m, (size_t)(n - c0)), (uint32_t)n, (uint32_t)c0, ep);
   });
   return hipGetLastError();
 }
