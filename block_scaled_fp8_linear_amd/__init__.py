@@ -356,6 +356,15 @@ def _matrix(t: torch.Tensor, name: str) -> tuple:
     return t.shape
 
 
+def _input_gradient(dx: torch.Tensor | None, need_dx: bool, like: torch.Tensor,
+                    shape: tuple) -> torch.Tensor | None:
+    if need_dx:
+        return like.new_empty(shape) if dx is None else dx
+    if dx is not None:
+        raise ValueError("dx is given but need_dx is false")
+    return None
+
+
 def _layer_call(op: str, pointers: tuple, m: int, n: int, k: int, act: int,
                 workspace: torch.Tensor | None, idx: int) -> None:
     """Workspace, stream and the call itself, on the arrays' device."""
@@ -413,13 +422,15 @@ def fp8_block_linear_act_backward(dy: torch.Tensor, q: torch.Tensor, s: torch.Te
                                   z: torch.Tensor | None = None, act: int = ACT_NONE,
                                   dx: torch.Tensor | None = None, dz: torch.Tensor | None = None,
                                   dbias: torch.Tensor | None = None,
-                                  workspace: torch.Tensor | None = None) -> tuple:
+                                  workspace: torch.Tensor | None = None, need_dx: bool = True) -> tuple:
     """Backward pass of ``fp8_block_linear_act``: bf16 dy [M,N] -> (dx, dz) with
     dz = dy act'(z) bf16 [M,N] and dx = dz W_hat bf16 [M,K].
 
     ``z`` is the saved pre-activation (None with ``ACT_NONE``, where dz is dy
     itself). ``dbias``, when given, is an fp32 [N] tensor that receives the sum
-    of dz over rows. The residual's gradient is dy; the weight is a constant."""
+    of dz over rows. With ``need_dx`` false (the first layer that has something
+    to train) dx is None and its product does not run. The residual's gradient
+    is dy; the weight is a constant."""
     idx = _device_index(dy, "dy")
     m, n = mn = _matrix(dy, "dy")
     k = _matrix(q, "q")[1]
@@ -430,15 +441,14 @@ def fp8_block_linear_act_backward(dy: torch.Tensor, q: torch.Tensor, s: torch.Te
         raise ValueError("z is needed for the activation's derivative")
     elif dz is None:
         dz = dy.new_empty(mn)
-    if dx is None:
-        dx = dy.new_empty((m, k))
+    dx = _input_gradient(dx, need_dx, dy, (m, k))
     pointers = (_array(dy, _BF16, mn, idx, "dy"),
                 _optional(z, _BF16, mn, idx, "z"),
                 _array(q, torch.uint8, (n, k), idx, "q"),
                 _array(s, torch.float32, scale_grid_shape(n, k), idx, "s"),
                 _optional(dz, _BF16, mn, idx, "dz"),
                 _optional(dbias, torch.float32, (n,), idx, "dbias"),
-                _array(dx, _BF16, (m, k), idx, "dx"))
+                _optional(dx, _BF16, (m, k), idx, "dx"))
     _layer_call("linear_act_backward", pointers, m, n, k, act, workspace, idx)
     return dx, (dy if act == ACT_NONE else dz)
 
@@ -475,10 +485,10 @@ def fp8_block_glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, q
                            s_gate: torch.Tensor, q_up: torch.Tensor, s_up: torch.Tensor,
                            act: int = ACT_SILU, dx: torch.Tensor | None = None,
                            dg: torch.Tensor | None = None, du: torch.Tensor | None = None,
-                           workspace: torch.Tensor | None = None) -> tuple:
+                           workspace: torch.Tensor | None = None, need_dx: bool = True) -> tuple:
     """Backward pass of ``fp8_block_glu``: bf16 dh [M,N] and the saved g, u ->
     (dx, dg, du) with dg = dh u act'(g), du = dh act(g) and
-    dx = dg Wg_hat + du Wu_hat."""
+    dx = dg Wg_hat + du Wu_hat (None, and no product, with ``need_dx`` false)."""
     idx = _device_index(dh, "dh")
     m, n = mn = _matrix(dh, "dh")
     k = _matrix(q_gate, "q_gate")[1]
@@ -487,8 +497,7 @@ def fp8_block_glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, q
         dg = dh.new_empty(mn)
     if du is None:
         du = dh.new_empty(mn)
-    if dx is None:
-        dx = dh.new_empty((m, k))
+    dx = _input_gradient(dx, need_dx, dh, (m, k))
     pointers = (_array(dh, _BF16, mn, idx, "dh"),
                 _array(g, _BF16, mn, idx, "g"),
                 _array(u, _BF16, mn, idx, "u"),
@@ -498,6 +507,6 @@ def fp8_block_glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, q
                 _array(s_up, torch.float32, grid, idx, "s_up"),
                 _array(dg, _BF16, mn, idx, "dg"),
                 _array(du, _BF16, mn, idx, "du"),
-                _array(dx, _BF16, (m, k), idx, "dx"))
+                _optional(dx, _BF16, (m, k), idx, "dx"))
     _layer_call("glu_backward", pointers, m, n, k, act, workspace, idx)
     return dx, dg, du
