@@ -356,6 +356,16 @@ def _matrix(t: torch.Tensor, name: str) -> tuple:
     return t.shape
 
 
+def _outside_autograd(where: str, *inputs: torch.Tensor | None) -> None:
+    """The layer operators record nothing for autograd: an input that asks for a
+    gradient would lose it without a word, so it is refused."""
+    if torch.is_grad_enabled():
+        for t in inputs:
+            if t is not None and t.requires_grad:
+                raise RuntimeError(f"{where} is not recorded by autograd and an input requires grad: call it in "
+                                   "a torch.autograd.Function with its backward function, or under torch.no_grad()")
+
+
 def _input_gradient(dx: torch.Tensor | None, need_dx: bool, like: torch.Tensor,
                     shape: tuple) -> torch.Tensor | None:
     if need_dx:
@@ -400,7 +410,11 @@ def fp8_block_linear_act(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor,
     ``bias`` bf16 [N], ``residual`` bf16 [M,N] (``out`` may be the residual:
     added in place), ``act`` an ``ACT_*``. ``z``, when given, receives the
     bf16 pre-activation the backward pass needs. ``workspace``, when given,
-    holds at least ``layer_workspace_size("linear_act", M, N, K)`` bytes."""
+    holds at least ``layer_workspace_size("linear_act", M, N, K)`` bytes.
+
+    Like the other layer operators it is not recorded by autograd: while
+    gradients are enabled, inputs that require one are refused."""
+    _outside_autograd("fp8_block_linear_act", x, bias, residual)
     idx = _device_index(x, "x")
     m, k = _matrix(x, "x")
     n = _matrix(q, "q")[0]
@@ -431,6 +445,7 @@ def fp8_block_linear_act_backward(dy: torch.Tensor, q: torch.Tensor, s: torch.Te
     of dz over rows. With ``need_dx`` false (the first layer that has something
     to train) dx is None and its product does not run. The residual's gradient
     is dy; the weight is a constant."""
+    _outside_autograd("fp8_block_linear_act_backward", dy, z)
     idx = _device_index(dy, "dy")
     m, n = mn = _matrix(dy, "dy")
     k = _matrix(q, "q")[1]
@@ -461,6 +476,7 @@ def fp8_block_glu(x: torch.Tensor, q_gate: torch.Tensor, s_gate: torch.Tensor, q
     act(x Wg^T) * (x Wu^T), rounded once (``fp8_block_mlp_gate_up`` rounds on
     the way). ``g`` and ``u``, given together, receive the two bf16 products,
     which the backward pass needs."""
+    _outside_autograd("fp8_block_glu", x)
     idx = _device_index(x, "x")
     m, k = _matrix(x, "x")
     n = _matrix(q_gate, "q_gate")[0]
@@ -489,6 +505,7 @@ def fp8_block_glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, q
     """Backward pass of ``fp8_block_glu``: bf16 dh [M,N] and the saved g, u ->
     (dx, dg, du) with dg = dh u act'(g), du = dh act(g) and
     dx = dg Wg_hat + du Wu_hat (None, and no product, with ``need_dx`` false)."""
+    _outside_autograd("fp8_block_glu_backward", dh, g, u)
     idx = _device_index(dh, "dh")
     m, n = mn = _matrix(dh, "dh")
     k = _matrix(q_gate, "q_gate")[1]

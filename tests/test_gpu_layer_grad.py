@@ -1,7 +1,10 @@
 """The layer operators' backward passes as a training step uses them: without
-the input gradient."""
+the input gradient, and inside autograd by the README's example."""
 
 from __future__ import annotations
+
+import os
+import re
 
 import pytest
 
@@ -51,3 +54,41 @@ def test_without_the_input_gradient(shape):
         F.fp8_block_linear_act_backward(dy, qg, sg, dx=normal(gen, m, k), need_dx=False)
     with pytest.raises(ValueError):
         F.fp8_block_glu_backward(dy, z, u, qg, sg, qu, su, dx=normal(gen, m, k), need_dx=False)
+
+
+def example(name):
+    """The README's Python block that defines `name`."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    blocks = re.findall(r"```python\n(.*?)```", open(os.path.join(root, "README.md")).read(), flags=re.S)
+    space = {"torch": torch, "F": F}
+    exec(next(b for b in blocks if f"class {name}(" in b), space)
+    return space[name]
+
+
+@pytest.mark.parametrize("m", [1, 40, 130])
+def test_the_example_gives_the_gradient(m):
+    """The autograd example between recorded operations: its gradient is the
+    backward function's, that one the formula's in 64 bits, and the whole step
+    runs twice with gradients that add up."""
+    n, k = 264, 528
+    gen = torch.Generator().manual_seed(m)
+    (qg, sg), (qu, su) = weight(gen, n, k), weight(gen, n, k)
+    x = normal(gen, m, k).requires_grad_(True)
+    scale = normal(gen, n)
+    say("autograd example", m)
+    fn = example("FrozenGlu")
+    h = fn.apply(x, qg, sg, qu, su)
+    (h * scale).sum().backward()
+    first = x.grad.clone()
+    (fn.apply(x, qg, sg, qu, su) * scale).sum().backward()
+    with torch.no_grad():
+        g, u = (torch.empty(m, n, dtype=BF, device="cuda") for _ in range(2))
+        want_h = F.fp8_block_glu(x, qg, sg, qu, su, g=g, u=u)
+        dh = scale.expand(m, n).contiguous()
+        dx, dg, du = F.fp8_block_glu_backward(dh, g, u, qg, sg, qu, su)
+    torch.cuda.synchronize()
+    assert torch.equal(h.detach(), want_h) and torch.equal(first, dx) and torch.equal(x.grad, dx + dx)
+    R.check_glu(x.detach(), qg, sg, qu, su, "silu", want_h, g, u, "example")
+    R.check_glu_backward(dh, g, u, qg, sg, qu, su, "silu", dx, dg, du, "example")
+    with pytest.raises(RuntimeError, match="not recorded by autograd"):
+        F.fp8_block_glu(x, qg, sg, qu, su)
