@@ -86,13 +86,15 @@ KERNEL_SOURCES = {
     "gemm_w8a8_large_kernel": ("gemm_w8a8_large.hip",),
     "stream_read_kernel": ("stream_read.hip",),
     # the layer operators
-    "linear_act_kernel": ("fp8bl_layers.hip", "gemm_layer.hip", "gemm_large_body.h", "fp8bl_act.h"),
-    "glu_kernel": ("fp8bl_layers.hip", "gemm_layer.hip", "gemm_large_body.h", "fp8bl_act.h"),
-    "input_gradient_kernel": ("fp8bl_layers.hip", "gemm_layer.hip", "gemm_large_body.h", "fp8bl_act.h"),
-    "linear_act_skinny_kernel": ("fp8bl_layers.hip", "gemm_layer_skinny.hip", "gemm_skinny_body.h", "fp8bl_act.h"),
-    "glu_skinny_kernel": ("fp8bl_layers.hip", "gemm_layer_skinny.hip", "gemm_skinny_body.h", "fp8bl_act.h"),
-    "input_gradient_skinny_kernel": ("fp8bl_layers.hip", "gemm_layer_skinny.hip", "gemm_skinny_body.h",
-                                     "fp8bl_act.h"),
+    "linear_act_kernel": ("fp8bl_layers.hip", "layer_plan.h", "gemm_layer.hip", "gemm_large_body.h", "fp8bl_act.h"),
+    "glu_kernel": ("fp8bl_layers.hip", "layer_plan.h", "gemm_layer.hip", "gemm_large_body.h", "fp8bl_act.h"),
+    "input_gradient_kernel": ("fp8bl_layers.hip", "layer_plan.h", "gemm_layer.hip", "gemm_large_body.h", "fp8bl_act.h"),
+    "linear_act_skinny_kernel": ("fp8bl_layers.hip", "layer_plan.h", "gemm_layer_skinny.hip", "gemm_skinny_body.h",
+                                 "fp8bl_act.h"),
+    "glu_skinny_kernel": ("fp8bl_layers.hip", "layer_plan.h", "gemm_layer_skinny.hip", "gemm_skinny_body.h",
+                          "fp8bl_act.h"),
+    "input_gradient_skinny_kernel": ("fp8bl_layers.hip", "layer_plan.h", "gemm_layer_skinny.hip",
+                                     "gemm_skinny_body.h", "fp8bl_act.h"),
     "join_kernel": ("layer_join.hip", "fp8bl_act.h"),
     "act_backward_kernel": ("act_backward.hip", "fp8bl_act.h"),
     "glu_backward_kernel": ("act_backward.hip", "fp8bl_act.h"),

@@ -12,30 +12,15 @@
 // first and after its last step, and tiles rarely fill whole rounds of 256 CUs.
 // At tens of rows it is the codes' bytes.
 #include "gemm_large_body.h"
+#include "layer_plan.h"
 
 namespace fp8bl {
 
+using namespace plan;
+
 namespace {
 
-// The tiles built: 32-row blocks of X, ring stages, 64-wide blocks of K per
-// step; one workgroup a CU. (64 rows with 64 of K a step and two workgroups a
-// CU: 64 x 25600 x 5120 47.4 us against 42.0, 64 x 5120 x 25600 45.3 against
-// 38.2, 333 x 4304 x 1168 20.2 against 20.5.)
-enum TileId { k256, k128, k64 };
-template <int ID>
-struct Tile;
-template <>
-struct Tile<k256> {
-  static constexpr int kMB = 8, kStages = 3, kKS = 1;
-};
-template <>
-struct Tile<k128> {
-  static constexpr int kMB = 4, kStages = 4, kKS = 1;
-};
-template <>
-struct Tile<k64> {
-  static constexpr int kMB = 2, kStages = 3, kKS = 2;
-};
+static_assert(kTileK == kBK && kTileCols == kBN, "the plans' tiles are the kernels'");
 
 struct Grid {
   int gk, tiles_m, tiles_n, steps, splits, steps_per_unit;
@@ -90,87 +75,6 @@ void input_gradient_kernel(const uint16_t* __restrict__ x, const uint8_t* __rest
 }
 
 int blocks_of(int64_t v) { return (int)((v + kBlock - 1) / kBlock); }
-
-// Tile and K splits of one of the three products: tiles of `cols` output
-// columns, `products` sums over r, `words` fp32 partials an output (two for
-// the gated pair). The model, in microseconds, was fitted to 3200 measurements
-// of the three products on MI355X (48 to 512 rows, seven weights from 1024 x
-// 1024 to 25600 x 5120, every tile, 1 to 24 splits; rms 6.5%, and the plan it
-// picks is 2% slower than the best measured one on average, 16% at worst): a
-// fixed part, then rounds of units over the chip, a step taking longer the
-// more of the chip runs, then the join. Best of each tile, linear, us:
-//    64 x 5120 x 5120   k64 19.2   k128 22.8   k256 25.2
-//    64 x 5120 x 25600  k64 38.2   k128 45.3   k256 57.3
-//   128 x 25600 x 5120  k64 56.7   k128 58.5   k256 72
-//   512 x 25600 x 5120             k128 156    k256 122
-struct LayerPlan {
-  int tile;                                  // TileId
-  int splits, steps_per_split;
-  double cost;
-};
-struct TileCost {
-  int tile, rows, k_step, stages;
-  double fixed, step_few, step_full, unit;   // step_few: when few CUs run
-};
-template <int ID>
-constexpr TileCost tile_cost(double fixed, double few, double full, double unit) {
-  return TileCost{ID, 32 * Tile<ID>::kMB, kBK * Tile<ID>::kKS, Tile<ID>::kStages, fixed, few, full, unit};
-}
-constexpr TileCost kTileCosts[] = {tile_cost<k256>(9.3, 1.07, 1.20, 0.5), tile_cost<k128>(8.9, 0.77, 0.84, 0.0),
-                                   tile_cost<k64>(8.1, 1.03, 1.27, 0.0)};
-constexpr int kCus = 256;
-constexpr int kMaxSplits = 32;
-
-// Steps of `products` sums over r, each padded to whole steps.
-int64_t steps_of(int64_t r, int products, int k_step) { return (r + k_step - 1) / k_step * products; }
-
-LayerPlan plan_tiles(int64_t m, int64_t n, int cols, int64_t r, int products, int words) {
-  LayerPlan best{k256, 1, 0, 1e300};
-  for (const TileCost& t : kTileCosts) {
-    const int64_t tiles = ((m + t.rows - 1) / t.rows) * ((n + cols - 1) / cols);
-    const int64_t steps = steps_of(r, products, t.k_step);
-    for (int sp = 1; sp <= kMaxSplits; ++sp) {
-      const int64_t per = (steps + sp - 1) / sp;
-      if (sp > 1 && per * t.k_step < 4 * kBK) break;
-      const int64_t units = tiles * sp;
-      const int64_t rest = units % kCus;
-      double cost = t.fixed + (double)(units / kCus) * (per * t.step_full + t.unit);
-      if (rest > 0) cost += per * (t.step_few + (t.step_full - t.step_few) * (double)rest / kCus) + t.unit;
-      if (sp > 1) cost += 1.1 + 1e-6 * (double)(m * n) * (1.3 * sp * words + 1.0);
-      if (cost < best.cost) best = LayerPlan{t.tile, (int)((steps + per - 1) / per), (int)per, cost};
-    }
-  }
-  return best;
-}
-
-// A product as one or two launches over tile columns: where the tiles are a
-// little more than whole rounds of the chip, the whole rounds run unsplit and
-// only the columns left over are split (4096 x 12800 x 5120 backward, 320
-// tiles: 256 unsplit and 64 in four instead of all 320 in four).
-struct Part {
-  int tile0, tiles_n;       // tile columns
-  LayerPlan plan;
-};
-struct ProductPlan {
-  int parts;
-  Part part[2];
-};
-ProductPlan plan_product(int64_t m, int64_t n, int cols, int64_t r, int products, int words) {
-  const int tn = (int)((n + cols - 1) / cols);
-  ProductPlan best{1, {{0, tn, plan_tiles(m, n, cols, r, products, words)}, {}}};
-  const TileCost& t = kTileCosts[k256];
-  static_assert(kTileCosts[k256].tile == k256 && kTileCosts[k64].tile == k64, "the table is in the tiles' order");
-  const int64_t steps = steps_of(r, products, t.k_step);
-  const int64_t tm = (m + t.rows - 1) / t.rows;
-  const int64_t rounds = tm * tn / kCus, head = rounds * kCus / tm;   // head: tile columns
-  if (rounds > 0 && head < tn) {
-    const LayerPlan h{t.tile, 1, (int)steps, t.fixed + (double)rounds * (steps * t.step_full + t.unit)};
-    const LayerPlan rest = plan_tiles(m, n - head * cols, cols, r, products, words);
-    if (h.cost + rest.cost < 0.98 * best.part[0].plan.cost)
-      best = ProductPlan{2, {{0, (int)head, h}, {(int)head, (int)(tn - head), rest}}};
-  }
-  return best;
-}
 
 Grid grid_of(const Part& part, int64_t m, int64_t k) {
   const LayerPlan& p = part.plan;
@@ -227,30 +131,6 @@ hipError_t run_parts(const ProductPlan& p, int64_t m, int64_t k, int cols, size_
 }
 
 }  // namespace
-
-// Which of a product's two kernels runs: the streams of gemm_layer_skinny.hip
-// (up to 32 rows) or the tiles. The streams start and end faster and keep more
-// codes in flight; the tiles read X once a workgroup instead of once a wave.
-// Measured on MI355X, stream against tiles, microseconds:
-//   linear  16 x 25600 x 5120  33.8  38.1    32 x 5120 x 5120   13.3  17.6
-//           32 x 8000 x 8192   20.4  22.5    32 x 25600 x 5120  46.4  39.1
-//   gated    8 x 25600 x 5120  42.4  51.4    16 x 25600 x 5120  47.5  55.5
-//           16 x 5120 x 25600  62.4  51.4    32 x 8192 x 2048   12.4    -
-//           32 x 5120 x 5120   21.9  19.9
-//   input gradient (rows x weight rows x columns)
-//           16 x 12288 x 4096  17.7  21.1    16 x 25600 x 5120  40.5  36
-//           32 x 2048 x 4096   10.6  12.2    32 x 5120 x 5120   18.9  16.7
-// (Pairs of nine to sixteen rows: past 2^27 codes the stream needs workgroups
-// for two a CU, one per 16 columns.)
-enum Product { kLinear, kPair, kInputGradient };
-bool streams(Product p, int64_t m, int64_t n, int64_t codes) {
-  if (m > 32) return false;
-  switch (p) {
-    case kLinear: return m <= 16 || codes <= (1 << 26);
-    case kPair: return m <= 8 || codes <= (m <= 16 ? 1 << 27 : 1 << 25) || (m <= 16 && n >= 8192);
-    default: return codes <= (m <= 16 ? 1 << 26 : 1 << 23);
-  }
-}
 
 size_t linear_act_bytes(int64_t m, int64_t n, int64_t k) {
   if (streams(kLinear, m, n, n * k)) return linear_act_skinny_bytes(m, n, k);

@@ -3,38 +3,15 @@
 // are bound by the codes, each read once; with a small weight by the launch
 // and the latency of a wave's few loads.
 #include "gemm_skinny_body.h"
+#include "layer_plan.h"
 
 namespace fp8bl {
 
+using namespace plan;
+
 namespace {
 
-// How X is brought in (gemm_skinny_body.h), the K of a super-step, the ring's
-// slots and the workgroups a CU holds. X goes through LDS, but for up to four
-// rows of a gated pair or a small grid, where it is too little to matter.
-// Half-width super-steps keep such a workgroup at 64 KB, two to a CU, where the
-// grid has them, and leave 32 rows of X room for three slots. Microseconds, X
-// in registers / through LDS in steps of 256 K / of 128 K, two to a CU:
-//   linear   1 x 12288 x 4096  13.6    -   12.3    1 x 5120 x 25600  30.0    -   28.5
-//           16 x 12288 x 4096  17.3  17.5  15.1   16 x 25600 x 5120  37.5  37.9  33.8
-//           16 x 5120 x 5120   12.4  10.7  11.5   16 x 8000 x 8192   18.6  17.3  17.6
-//            1 x 5120 x 5120    9.1   9.2    -     8 x 5120 x 5120   11.1  10.2  10.9
-//   gated    1 x 25600 x 5120  36.8    -   38.4   16 x 12288 x 4096  22.1  23.1  19.2
-//            8 x 25600 x 5120  43.1  53.1  42.4   16 x 2560 x 5120   11.0   9.4   9.6
-// and of 17 to 32 rows, registers / LDS: linear 32 x 5120 x 5120 16.8 / 13.3,
-// 32 x 4096 x 8192 22.2 / 17.1, gated 32 x 2560 x 5120 15.6 / 11.9,
-// 32 x 8192 x 2048 14.4 / 12.4. (Four slots of 128 K: 12.3 at 16 x 5120 x 5120.)
-template <int MT_, bool LDS_, int KW_, int D_, int RESIDENT_>
-struct Path {
-  static constexpr int MT = MT_, KW = KW_, D = D_, kResident = RESIDENT_;
-  static constexpr bool kLds = LDS_;
-};
-template <typename F>
-void with_path(int64_t m, int64_t workgroups, bool gated, F&& f) {
-  if (m > 16) return f(Path<2, true, 128, 3, 1>{});
-  const bool many = workgroups > 256;          // CUs get two
-  if (m <= 4 && (gated || !many)) return f(Path<1, false, kSuper, kRing, 2>{});
-  return many ? f(Path<1, true, 128, 2, 2>{}) : f(Path<1, true, kSuper, kRing, 1>{});
-}
+static_assert(kStreamK == kSuper && kStreamWaves == kWaves, "the plans' streams are the kernels'");
 
 // y = act(x W^T + bias) + residual on the sums that meet in LDS.
 // (1 x 8000 x 8192 12.6 us, 5.2 TB/s of codes, partly from the last-level
@@ -81,8 +58,6 @@ void glu_skinny_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict
 //
 // v_mfma_f32_16x16x32_bf16: lane l holds row (l % 16) of the left operand and
 // column (l % 16) of the right one at k = 8 (l / 16) .. +8.
-constexpr int kStripCols = 256;
-constexpr int kStepRows = 32;
 constexpr int kStripTiles = kStripCols / 16;
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) i32x2* lds_i32x2_ptr_t;
@@ -222,51 +197,6 @@ void input_gradient_skinny_kernel(const uint16_t* __restrict__ a, const uint8_t*
   }
 }
 
-constexpr int64_t kPassRows = 32;
-
-// Splits of the reduction: about two workgroups a CU (64 KB of LDS each), at
-// least one super-step a wave.
-struct GradientPlan {
-  int strips, steps1, steps, splits, steps_per_split;
-};
-GradientPlan plan_gradient_skinny(int64_t n, int64_t k, int products) {
-  GradientPlan p;
-  p.strips = (int)((k + kStripCols - 1) / kStripCols);
-  p.steps1 = (int)((n + kStepRows - 1) / kStepRows);
-  p.steps = p.steps1 * products;
-  int splits = (512 + p.strips - 1) / p.strips;
-  const int most = (p.steps + kWaves - 1) / kWaves;
-  if (splits > most) splits = most;
-  p.steps_per_split = (p.steps + splits - 1) / splits;
-  p.splits = (p.steps + p.steps_per_split - 1) / p.steps_per_split;
-  return p;
-}
-
-// K splits of the two forward forms, by the workgroups (32 weight rows each)
-// and a wave's super-steps. A split costs its join, about 3 us, so it has to
-// save iterations: 16 x 5120 x 5120 (160 workgroups, 5 super-steps a wave)
-// runs 12.2 us unsplit and 14.2 in two, 1 x 2048 x 2048 5.0 and 5.9; but
-// 1 x 1024 x 8192 (32 workgroups, 8 super-steps) 10.8 unsplit and 7.1 in four,
-// and 16 x 5120 x 25600 (25 super-steps, 160 workgroups on 256 CUs) 42.7
-// unsplit and 37.9 in four.
-struct LayerPlan {
-  int splits, ss_per_split;
-};
-LayerPlan plan_layer(int64_t groups, int64_t k) {
-  const int nss = (int)((k + kSuper - 1) / kSuper);
-  const int iters = (nss + kWaves - 1) / kWaves;
-  int splits = 1;
-  if (groups < 128 && iters >= 4) {
-    while (groups * splits < 128 && splits * 2 <= iters) splits *= 2;
-  } else if (groups < 256 && iters >= 16) {
-    splits = 4;
-  }
-  LayerPlan p;
-  p.ss_per_split = (nss + splits - 1) / splits;
-  p.splits = (nss + p.ss_per_split - 1) / p.ss_per_split;
-  return p;
-}
-
 }  // namespace
 
 size_t linear_act_skinny_bytes(int64_t m, int64_t n, int64_t k) {
@@ -277,7 +207,7 @@ size_t linear_act_skinny_bytes(int64_t m, int64_t n, int64_t k) {
 hipError_t launch_linear_act_skinny(const uint16_t* x, const uint8_t* q, const float* s, uint16_t* y,
                                     const LayerEpilogue& ep, int64_t m, int64_t n, int64_t k, void* ws,
                                     size_t ws_bytes, hipStream_t stream) {
-  const LayerPlan p = plan_layer((n + 31) / 32, k);
+  const StreamPlan p = plan_layer((n + 31) / 32, k);
   if (p.splits > 1 && (ws == nullptr || ws_bytes < linear_act_skinny_bytes(m, n, k))) return hipErrorInvalidValue;
   float* const part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
   const dim3 grid((uint32_t)((n + 31) / 32), (uint32_t)p.splits), block(kWaves * 64);
@@ -300,7 +230,7 @@ size_t glu_skinny_bytes(int64_t m, int64_t n, int64_t k) {
 hipError_t launch_glu_skinny(const uint16_t* x, const uint8_t* qg, const float* sg, const uint8_t* qu,
                              const float* su, uint16_t* h, const LayerEpilogue& ep, int64_t m, int64_t n,
                              int64_t k, void* ws, size_t ws_bytes, hipStream_t stream) {
-  const LayerPlan p = plan_layer((n + 15) / 16, k);
+  const StreamPlan p = plan_layer((n + 15) / 16, k);
   if (p.splits > 1 && (ws == nullptr || ws_bytes < glu_skinny_bytes(m, n, k))) return hipErrorInvalidValue;
   float* const part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
   const dim3 grid((uint32_t)((n + 15) / 16), (uint32_t)p.splits), block(kWaves * 64);
