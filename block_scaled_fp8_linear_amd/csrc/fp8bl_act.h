@@ -1,8 +1,9 @@
 // Activations of the layer operators and their derivatives, in fp32 (the
 // formulas are in fp8bl_layers.h). Exponentials and quotients run on the
 // hardware exp2 and reciprocal: a sigmoid is off by a relative
-// (2 |v| + 4) 2^-23 at most, far below the half step of the bf16 results
-// (2^-9) and of the same size as the fp32 sums' own rounding.
+// (2 |v| + 4) 2^-23 at most (the product in the exponent is off by |v| times
+// its roundings), far below the half step of the bf16 results (2^-8) and of
+// the same size as the fp32 sums' own rounding.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -31,10 +32,12 @@ constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 // The normal distribution's tail Phi(-a), a >= 0, with e = e^(-a^2/2):
 // Phi(-a) e^(a^2/2) is smooth and slowly varying, here a polynomial of degree
 // 7 in 1 / (1 + 0.35 a), fitted by reweighted least squares to the smallest
-// largest relative error on 0 <= a <= 14.5 (beyond, e is 0): 3.2e-7, 5.6e-7
-// evaluated in fp32. About 14 instructions with no branch; the library's erfcf
-// took 150 us of 894 us in the epilogue of 8192 x 12288 x 4096. It keeps its
-// relative precision where Phi is small, as (1 + erf) / 2 would not.
+// largest relative error on 0 <= a <= 14.5 (beyond, e is 0): 3.6e-7 with these
+// coefficients, 6.0e-7 evaluated in fp32. e's exponent is rounded to fp32, which
+// adds a^2 2^-24 to the tail's relative error (2.2e-6 in all at a = 6, 8e-6 at
+// a = 13): still far inside the half step where Phi is small, as (1 + erf) / 2
+// would not be. About 14 instructions with no branch; the library's erfcf took
+// 150 us of 894 us in the epilogue of 8192 x 12288 x 4096.
 __device__ __forceinline__ float normal_tail(float a, float& e) {
   e = __builtin_amdgcn_exp2f(a * a * (-0.5f * kLog2E));
   const float s = __builtin_amdgcn_rcpf(__builtin_fmaf(0.35f, a, 1.0f));
