@@ -29,7 +29,7 @@ void linear_act_skinny_kernel(const uint16_t* __restrict__ x, const uint8_t* __r
 
 // h = act(x Wg^T) (x Wu^T): of a workgroup's two 16-row tiles one is gate rows
 // and the other the up rows of the same 16 columns, so a lane ends with both
-// sums of its outputs. (1 x 25600 x 5120 43 us, 6.1 TB/s of codes.)
+// sums of its outputs. (1 x 25600 x 5120 43 - 47 us, 5.6 - 6.1 TB/s of codes.)
 template <typename P>
 __global__ __launch_bounds__(kWaves * 64, P::kResident)
 void glu_skinny_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ qg,

@@ -18,12 +18,13 @@ constexpr int kStepRows = 32;      // and its weight rows a super-step
 // Which of a product's two kernels runs: the streams of gemm_layer_skinny.hip
 // (up to 32 rows) or the tiles. The streams start and end faster and keep more
 // codes in flight; the tiles read X once a workgroup instead of once a wave.
-// Measured on MI355X, stream against tiles, microseconds:
+// Measured on MI355X, stream against tiles, microseconds (graph replays that
+// walk several weights, here and below):
 //   linear  16 x 25600 x 5120  33.8  38.1    32 x 5120 x 5120   13.3  17.6
 //           32 x 8000 x 8192   20.4  22.5    32 x 25600 x 5120  46.4  39.1
-//   gated    8 x 25600 x 5120  42.4  51.4    16 x 25600 x 5120  47.5  55.5
-//           16 x 5120 x 25600  62.4  51.4    32 x 8192 x 2048   12.4    -
-//           32 x 5120 x 5120   21.9  19.9
+//   gated    8 x 25600 x 5120  49.9  63.1    16 x 25600 x 5120  56.0  66.9
+//           16 x 5120 x 25600  71.6  60.2    32 x 8192 x 2048   14.3  16.9
+//           32 x 5120 x 5120   23.8  20.6
 //   input gradient (rows x weight rows x columns)
 //           16 x 12288 x 4096  17.7  21.1    16 x 25600 x 5120  40.5  36
 //           32 x 2048 x 4096   10.6  12.2    32 x 5120 x 5120   18.9  16.7
@@ -68,7 +69,10 @@ struct Tile<k64> {
 // 1024 to 25600 x 5120, every tile, 1 to 24 splits; rms 6.5%, and the plan it
 // picks is 2% slower than the best measured one on average, 16% at worst): a
 // fixed part, then rounds of units over the chip, a step taking longer the
-// more of the chip runs, then the join. Best of each tile, linear, us:
+// more of the chip runs, then the join. (The pair was fitted with one array as
+// both of its weights. With two, at 36 sizes of 40 to 512 rows, the plan is 1%
+// slower than the best of three tiles and eight splits, 11% at worst.) Best of
+// each tile, linear, us:
 //    64 x 5120 x 5120   k64 19.2   k128 22.8   k256 25.2
 //    64 x 5120 x 25600  k64 38.2   k128 45.3   k256 57.3
 //   128 x 25600 x 5120  k64 56.7   k128 58.5   k256 72
@@ -154,11 +158,11 @@ inline ProductPlan plan_product(int64_t m, int64_t n, int cols, int64_t r, int p
 //           16 x 12288 x 4096  17.3  17.5  15.1   16 x 25600 x 5120  37.5  37.9  33.8
 //           16 x 5120 x 5120   12.4  10.7  11.5   16 x 8000 x 8192   18.6  17.3  17.6
 //            1 x 5120 x 5120    9.1   9.2    -     8 x 5120 x 5120   11.1  10.2  10.9
-//   gated    1 x 25600 x 5120  36.8    -   38.4   16 x 12288 x 4096  22.1  23.1  19.2
-//            8 x 25600 x 5120  43.1  53.1  42.4   16 x 2560 x 5120   11.0   9.4   9.6
+//   gated    1 x 25600 x 5120  46.9  54.5  48.2   16 x 12288 x 4096  25.8  26.8  22.5
+//            8 x 25600 x 5120  49.5  59.7  50.1   16 x 2560 x 5120   12.1  10.7  11.4
 // and of 17 to 32 rows, registers / LDS: linear 32 x 5120 x 5120 16.8 / 13.3,
-// 32 x 4096 x 8192 22.2 / 17.1, gated 32 x 2560 x 5120 15.6 / 11.9,
-// 32 x 8192 x 2048 14.4 / 12.4. (Four slots of 128 K: 12.3 at 16 x 5120 x 5120.)
+// 32 x 4096 x 8192 22.2 / 17.1, gated 32 x 2560 x 5120 15.8 / 13.1,
+// 32 x 8192 x 2048 16.8 / 14.3. (Four slots of 128 K: 12.3 at 16 x 5120 x 5120.)
 template <int MT_, bool LDS_, int KW_, int D_, int RESIDENT_>
 struct Path {
   static constexpr int MT = MT_, KW = KW_, D = D_, kResident = RESIDENT_;
