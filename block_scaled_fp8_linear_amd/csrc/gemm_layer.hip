@@ -29,7 +29,7 @@ struct Grid {
 // y = act(x W^T + bias) + residual, and z = x W^T + bias where it is saved:
 // bias, activation and residual on the fp32 sums in the epilogue, so that z is
 // written once and nothing is read back. (8192 x 12288 x 4096 with bias, tanh
-// GELU and z saved 672 - 715 us from one card to the next, 1.15 - 1.23 PFLOP/s;
+// GELU and z saved 672 - 730 us from one card to the next, 1.13 - 1.23 PFLOP/s;
 // y alone, plain, 630. 512 x 5120 x 25600 with residual 129 us, 1.04 PFLOP/s;
 // 512 x 5120 x 5120 41 us, of which the join of its splits is 7.)
 template <bool SPLIT, int ACT, int ID>
