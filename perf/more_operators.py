@@ -407,7 +407,7 @@ def _e4m3_table():
 def _nearest_e4m3(x):
     """x to the nearest multiple of its binade's step, ties to even, at most 448."""
     _, e = torch.frexp(x)
-    step = torch.ldexp(torch.ones_like(x), (e - 4).clamp_min(-9))
+    step = (((e - 4).clamp_min(-9).long() + 1023) << 52).view(torch.float64)     # 2^(e - 4), from its bits
     return (torch.round(x / step) * step).clamp(-448, 448)
 
 
