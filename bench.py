@@ -86,19 +86,29 @@ KERNEL_SOURCES = {
     "gemm_w8a8_large_kernel": ("gemm_w8a8_large.hip",),
     "stream_read_kernel": ("stream_read.hip",),
     # the layer operators
-    "linear_act_kernel": ("fp8bl_layers.hip", "layer_plan.h", "gemm_layer.hip", "gemm_large_body.h", "fp8bl_act.h"),
-    "glu_kernel": ("fp8bl_layers.hip", "layer_plan.h", "gemm_layer.hip", "gemm_large_body.h", "fp8bl_act.h"),
-    "input_gradient_kernel": ("fp8bl_layers.hip", "layer_plan.h", "gemm_layer.hip", "gemm_large_body.h", "fp8bl_act.h"),
-    "linear_act_skinny_kernel": ("fp8bl_layers.hip", "layer_plan.h", "gemm_layer_skinny.hip", "gemm_skinny_body.h",
+    "linear_act_kernel": ("fp8bl_layers.hip", "fp8bl_arrays.h", "layer_plan.h", "gemm_layer.hip", "gemm_large_body.h", "fp8bl_act.h"),
+    "glu_kernel": ("fp8bl_layers.hip", "fp8bl_arrays.h", "layer_plan.h", "gemm_layer.hip", "gemm_large_body.h", "fp8bl_act.h"),
+    "input_gradient_kernel": ("fp8bl_layers.hip", "fp8bl_arrays.h", "layer_plan.h", "gemm_layer.hip", "gemm_large_body.h", "fp8bl_act.h"),
+    "linear_act_skinny_kernel": ("fp8bl_layers.hip", "fp8bl_arrays.h", "layer_plan.h", "gemm_layer_skinny.hip", "gemm_skinny_body.h",
                                  "fp8bl_act.h"),
-    "glu_skinny_kernel": ("fp8bl_layers.hip", "layer_plan.h", "gemm_layer_skinny.hip", "gemm_skinny_body.h",
+    "glu_skinny_kernel": ("fp8bl_layers.hip", "fp8bl_arrays.h", "layer_plan.h", "gemm_layer_skinny.hip", "gemm_skinny_body.h",
                           "fp8bl_act.h"),
-    "input_gradient_skinny_kernel": ("fp8bl_layers.hip", "layer_plan.h", "gemm_layer_skinny.hip",
+    "input_gradient_skinny_kernel": ("fp8bl_layers.hip", "fp8bl_arrays.h", "layer_plan.h", "gemm_layer_skinny.hip",
                                      "gemm_skinny_body.h", "fp8bl_act.h"),
     "join_kernel": ("layer_join.hip", "fp8bl_act.h"),
     "act_backward_kernel": ("act_backward.hip", "fp8bl_act.h"),
     "glu_backward_kernel": ("act_backward.hip", "fp8bl_act.h"),
     "column_sum_kernel": ("act_backward.hip", "fp8bl_act.h"),
+    # the 8-bit integer linear
+    "int8_quantize_kernel": ("fp8bl_int8.hip", "fp8bl_ops.h", "int8_quantize.hip"),
+    "gemm_int8_kernel": ("fp8bl_int8.hip", "fp8bl_ops.h", "gemm_int8.hip"),
+    # from the QKV projection to its cache
+    "rope_kernel": ("fp8bl_qkv.hip", "fp8bl_ops.h", "qk_norm_rope.hip", "qkv_device.h"),
+    "store_kernel": ("fp8bl_qkv.hip", "fp8bl_ops.h", "qk_norm_rope.hip", "qkv_device.h"),
+    "rope_store_kernel": ("fp8bl_qkv.hip", "fp8bl_ops.h", "qk_norm_rope.hip", "qkv_device.h"),
+    "back_kernel": ("fp8bl_qkv.hip", "fp8bl_ops.h", "qk_norm_rope_backward.hip", "qkv_device.h"),
+    "back_sum_kernel": ("qk_norm_rope_backward.hip", "qkv_device.h"),
+    "load_kernel": ("fp8bl_qkv.hip", "fp8bl_ops.h", "kv_load.hip", "qkv_device.h"),
 }
 SHARED_SOURCES = ("fp8bl_api.hip", "fp8bl_checks.h", "fp8bl_device.h", "fp8bl_internal.h")
 

@@ -10,11 +10,14 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 _PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG_DIR, "libfp8bl.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG_DIR), "include", "fp8bl.h")
 LAYERS_HEADER_PATH = os.path.join(os.path.dirname(_PKG_DIR), "include", "fp8bl_layers.h")
+INT8_HEADER_PATH = os.path.join(os.path.dirname(_PKG_DIR), "include", "fp8bl_int8.h")
+QKV_HEADER_PATH = os.path.join(os.path.dirname(_PKG_DIR), "include", "fp8bl_qkv.h")
 
 FP8BL_OK = 0
 FP8BL_INVALID_ARG = 1
@@ -98,6 +101,24 @@ def load() -> ctypes.CDLL:
         call = getattr(lib, f"fp8_block_{op}")
         call.restype = c_int
         call.argtypes = [vp] * pointers + tail
+    for name in ("int8_row_quantize", "int8_row_quantize_bf16"):
+        call = getattr(lib, name)
+        call.restype = c_int
+        call.argtypes = [vp, vp, vp, i64, i64, vp]
+    for name, pointers in (("int8_linear", 6), ("int8_linear_bf16", 5)):
+        size, call = getattr(lib, name + "_workspace_size"), getattr(lib, name)
+        size.restype = sz
+        size.argtypes = [i64, i64, i64]
+        call.restype = c_int
+        call.argtypes = [vp] * pointers + [i64, i64, i64, vp, sz, vp]
+    for name in ("fp8_qk_norm_rope", "fp8_kv_store", "fp8_kv_load", "fp8_qk_norm_rope_store"):
+        call = getattr(lib, name)
+        call.restype = c_int
+        call.argtypes = [ctypes.c_char_p, vp]
+    lib.fp8_qk_norm_rope_backward_workspace_size.restype = sz
+    lib.fp8_qk_norm_rope_backward_workspace_size.argtypes = [i64, i64, i64, i64]
+    lib.fp8_qk_norm_rope_backward.restype = c_int
+    lib.fp8_qk_norm_rope_backward.argtypes = [ctypes.c_char_p, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -106,7 +127,7 @@ def header_functions(path: str | None = None) -> list[str]:
     """Names of the functions a header declares (include/fp8bl.h by default)."""
     text = open(path or HEADER_PATH).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return re.findall(r"^\s*(?:const\s+)?\w+\*?\s+\*?(fp8_\w+)\s*\(", text, flags=re.M)
+    return re.findall(r"^\s*(?:const\s+)?\w+\*?\s+\*?((?:fp8|int8)_\w+)\s*\(", text, flags=re.M)
 
 
 def status_string(status: int) -> str:
@@ -233,3 +254,77 @@ def glu_backward_raw(dh: int, g: int, u: int, qg: int, sg: int, qu: int, su: int
                      stream: int = 0) -> int:
     return load().fp8_block_glu_backward(dh, g, u, qg, sg, qu, su, dg, du, dx, m, n, k, act, ws,
                                          ws_bytes, stream)
+
+
+# 8-bit integer linear (include/fp8bl_int8.h).
+
+def int8_row_quantize_raw(x: int, q: int, s: int, m: int, k: int, bf16: bool, stream: int = 0) -> int:
+    lib = load()
+    return (lib.int8_row_quantize_bf16 if bf16 else lib.int8_row_quantize)(x, q, s, m, k, stream)
+
+
+def int8_linear_raw(xq: int, xs: int, wq: int, ws: int, bias: int, y: int, m: int, n: int, k: int,
+                    work: int, work_bytes: int, stream: int = 0) -> int:
+    return load().int8_linear(xq, xs, wq, ws, bias, y, m, n, k, work, work_bytes, stream)
+
+
+def int8_linear_bf16_raw(x: int, wq: int, ws: int, bias: int, y: int, m: int, n: int, k: int,
+                         work: int, work_bytes: int, stream: int = 0) -> int:
+    return load().int8_linear_bf16(x, wq, ws, bias, y, m, n, k, work, work_bytes, stream)
+
+
+def int8_workspace_size(m: int, n: int, k: int, from_bf16: bool = True) -> int:
+    """Workspace bytes of int8_linear_bf16, or of int8_linear."""
+    lib = load()
+    size = lib.int8_linear_bf16_workspace_size if from_bf16 else lib.int8_linear_workspace_size
+    return int(size(int(m), int(n), int(k)))
+
+
+# From the QKV projection to its cache (include/fp8bl_qkv.h).
+
+MAX_AXES = 8
+MAX_PAIRS = 128
+
+# struct fp8bl_qkv: its members in order, every one of eight bytes but the axes
+_HEADS = ("q", "k", "v", "q_out", "k_out", "v_out", "dq", "dk")
+_QKV_FIELDS = (("tokens", "q_heads", "k_heads", "head_dim")
+               + tuple(f"{h}_{part}" for h in _HEADS for part in ("data", "token_stride", "head_stride"))
+               + ("q_weight", "k_weight", "dq_weight", "dk_weight", "positions", "inv_freq",
+                  "axes", "pairs", "interleaved", "eps",
+                  "slots", "k_cache", "v_cache", "k_scale", "v_scale", "cache_rows"))
+_QKV_STRUCT = struct.Struct(f"={_QKV_FIELDS.index('eps')}qd{len(_QKV_FIELDS) - _QKV_FIELDS.index('eps') - 1}q"
+                            f"{MAX_PAIRS}s")
+qkv_pack = _QKV_STRUCT.pack
+
+
+def qkv_struct(axis: bytes = b"", **members) -> bytes:
+    """struct fp8bl_qkv with the named members set and zeros elsewhere."""
+    unknown = set(members) - set(_QKV_FIELDS)
+    if unknown:
+        raise ValueError(f"no such members: {sorted(unknown)}")
+    return qkv_pack(*(members.get(f, 0) for f in _QKV_FIELDS), axis)
+
+
+def qk_norm_rope_raw(args: bytes, stream: int = 0) -> int:
+    return load().fp8_qk_norm_rope(args, stream)
+
+
+def qk_norm_rope_backward_raw(args: bytes, work: int, work_bytes: int, stream: int = 0) -> int:
+    return load().fp8_qk_norm_rope_backward(args, work, work_bytes, stream)
+
+
+def qk_norm_rope_backward_workspace_size(tokens: int, q_heads: int, k_heads: int, head_dim: int) -> int:
+    return int(load().fp8_qk_norm_rope_backward_workspace_size(int(tokens), int(q_heads), int(k_heads),
+                                                               int(head_dim)))
+
+
+def kv_store_raw(args: bytes, stream: int = 0) -> int:
+    return load().fp8_kv_store(args, stream)
+
+
+def kv_load_raw(args: bytes, stream: int = 0) -> int:
+    return load().fp8_kv_load(args, stream)
+
+
+def qk_norm_rope_store_raw(args: bytes, stream: int = 0) -> int:
+    return load().fp8_qk_norm_rope_store(args, stream)

@@ -153,7 +153,7 @@ hipError_t launch_glu_backward(const uint16_t* dh, const uint16_t* g, const uint
                                hipStream_t stream);
 hipError_t launch_fill_zero(void* p, size_t bytes, hipStream_t stream);
 
-// Checks shared by the two ABI files.
+// Checks shared by the ABI files.
 int gate_current_device();
 
 constexpr size_t kWorkspaceAlign = 256;

@@ -1,0 +1,172 @@
+// What the kernels between the QKV projection and its cache share: the lanes
+// of a head, sums over them, and the angles of a token.
+//
+// A head of D elements lies in L lanes, the power of two from D / 8 on: lane c
+// of them holds elements 8 c .. 8 c + 7 (none from D / 8 on), so a wave reads
+// 64 / L heads with one 16-byte load a lane.
+#pragma once
+
+#include "fp8bl_device.h"
+#include "fp8bl_qkv.h"
+
+namespace fp8bl {
+
+namespace {
+
+constexpr int kQkvWaves = 4;
+constexpr int kQkvThreads = kQkvWaves * 64;
+constexpr int64_t kMaxBlocks = (int64_t)1 << 22;   // workgroups of a launch
+
+struct HeadView {
+  uint16_t* p;
+  int64_t ts, hs;
+  int heads;
+};
+
+inline HeadView head_view(const fp8bl_heads& h, int64_t heads) {
+  return HeadView{h.data, h.token_stride, h.head_stride, (int)heads};
+}
+
+struct TurnArgs {
+  const uint16_t* wq;
+  const uint16_t* wk;
+  const int32_t* positions;
+  const float* inv_freq;
+  int tokens, dim, pairs;
+  float eps;
+  uint8_t axis[FP8BL_MAX_PAIRS];
+};
+
+inline TurnArgs turn_args(const fp8bl_qkv& a) {
+  TurnArgs t{a.q_weight, a.k_weight, a.positions, a.inv_freq, (int)a.tokens, (int)a.head_dim, (int)a.pairs,
+             (float)a.eps, {}};
+  for (int i = 0; i < (int)a.pairs; ++i) t.axis[i] = a.axis[i];
+  return t;
+}
+
+inline int head_lanes(int64_t dim) {
+  int l = 2;
+  while (8 * l < dim) l *= 2;
+  return l;
+}
+
+// Calls f.template run<L>() with the L of a head dimension.
+template <typename F>
+hipError_t with_lanes(int64_t dim, F&& f) {
+  switch (head_lanes(dim)) {
+    case 2: return f.template run<2>();
+    case 4: return f.template run<4>();
+    case 8: return f.template run<8>();
+    case 16: return f.template run<16>();
+    default: return f.template run<32>();
+  }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E, kHalfMirror = 0x141, kRowRor8 = 0x128;
+
+// Sum (maximum) over the L lanes of a head, the same bits in each of them.
+template <int L, typename Op>
+__device__ __forceinline__ float head_reduce(float v, Op op) {
+  v = op(v, dpp<kQuadXor1>(v));
+  if constexpr (L >= 4) v = op(v, dpp<kQuadXor2>(v));
+  if constexpr (L >= 8) v = op(v, dpp<kHalfMirror>(v));
+  if constexpr (L >= 16) v = op(v, dpp<kRowRor8>(v));
+  if constexpr (L >= 32) v = op(v, __shfl_xor(v, 16, 64));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float head_sum(float v) {
+  return head_reduce<L>(v, [](float a, float b) { return a + b; });
+}
+template <int L>
+__device__ __forceinline__ float head_max(float v) {
+  return head_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+__device__ __forceinline__ void unpack8(u32x4 a, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(a[i] << 16);
+    v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
+  return u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+}
+
+// cos and sin of pair p of a token. The angle position * inv_freq reaches
+// 2^31 radians: it is taken in fp64 as a number of turns, whose fraction
+// then fits fp32.
+__device__ __forceinline__ float2 turn_of(const TurnArgs& t, int axis, int p, int token) {
+  const double turns = (double)t.positions[(size_t)axis * t.tokens + token] *
+                       ((double)t.inv_freq[p] * 0.15915494309189533577);
+  const float f = (float)(turns - rint(turns));
+  float2 cs;
+  sincospif(2.0f * f, &cs.y, &cs.x);
+  return cs;
+}
+
+// Where the lane's chunk c of a head stands: in the first or second members of
+// the half layout's pairs, among the interleaved pairs, or behind them.
+struct Chunk {
+  int partner;    // lane with the other members (half layout), or the lane itself
+  int pair;       // pair of the chunk's first element
+  float sign;     // of the sine: -1 first members, 1 second, 0 not turned
+};
+template <bool INTER>
+__device__ __forceinline__ Chunk chunk_of(int lane, int c, int pairs) {
+  const int e = 8 * c;
+  if constexpr (INTER) return Chunk{lane, e / 2, e < 2 * pairs ? 1.0f : 0.0f};
+  if (e < pairs) return Chunk{lane + pairs / 8, e, -1.0f};
+  if (e < 2 * pairs) return Chunk{lane - pairs / 8, e - pairs, 1.0f};
+  return Chunk{lane, 0, 0.0f};
+}
+
+// What the lane's elements are multiplied with in a turn, from the token's
+// table of cosines and sines: out_i = x_i c_i + (other member)_i s_i.
+template <bool INTER>
+__device__ __forceinline__ void turn_factors(const float2* table, const Chunk& ch, float (&c)[8], float (&s)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (ch.sign == 0.0f) {
+      c[i] = 1.0f;
+      s[i] = 0.0f;
+    } else if constexpr (INTER) {
+      const float2 t = table[ch.pair + i / 2];
+      c[i] = t.x;
+      s[i] = i & 1 ? t.y : -t.y;
+    } else {
+      const float2 t = table[ch.pair + i];
+      c[i] = t.x;
+      s[i] = ch.sign * t.y;
+    }
+  }
+}
+
+// The other members of the lane's elements.
+template <bool INTER>
+__device__ __forceinline__ u32x4 other_members(u32x4 x, int partner) {
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if constexpr (INTER)
+      o[i] = (x[i] << 16) | (x[i] >> 16);
+    else
+      o[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(partner << 2, (int)x[i]);
+  return o;
+}
+
+// LDS written by a wave for itself: its writes are done before its reads.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+}  // namespace
+
+}  // namespace fp8bl
