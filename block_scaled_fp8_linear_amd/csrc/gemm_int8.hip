@@ -1,11 +1,30 @@
 // 8-bit integer GEMM:
 //   Y[m,n] = bf16( float(sum_k xq[m,k] wq[n,k]) * (xs[m] * ws[n]) + bias[n] )
-// with the sum exact in int32 (v_mfma_i32_16x16x64_i8).
+// with the sum exact in int32, so that neither tiles nor K splits change a bit
+// of the result.
 //
-// v_mfma_i32_16x16x64_i8: lane l supplies 16 consecutive-k codes of row
-// l % 16 of its block at k chunk l / 16, for A and B alike. The weight is the A
-// operand and X the B operand, so a lane's four sums are rows 4 (l / 16) .. +3
-// of the weight block, four consecutive output columns of X row l % 16.
+// A workgroup of four waves, 2 x 2, each with a wave tile of 32 WM x 32 WN
+// outputs in blocks of v_mfma_i32_32x32x32_i8. One step is 128 of K, four slices
+// of 32: a wave reads WM + WN operands of a slice from LDS while the WM WN
+// products of the one before it run. (With 4 x 4 blocks a wave, the LDS delivers
+// 128 KB and takes in 64 KB a step of 2048 matrix cycles: three quarters of
+// what it can do. Narrower wave tiles would be bound by it.)
+//
+// Stages of (TM + TN) x 128 bytes are filled by loads that write LDS themselves,
+// S steps ahead. The last operands of a stage are read during the step's third
+// slice, so one barrier a step, before the fourth, tells both that the next
+// stage has landed and that this one can be refilled.
+//
+// LDS rows are 128 bytes with the 16-byte chunks permuted by
+// (row & 7) ^ ((row >> 3) & 1): 16 consecutive rows of one chunk lie in 16
+// different bank groups.
+//
+// v_mfma_i32_32x32x32_i8: lane l supplies 16 codes of row l % 32 at K half
+// l / 32, A (the weight) and B (X) alike; it holds the sums of X row l % 32 and
+// weight rows 8 g + 4 (l / 32) + i, g and i from 0 to 3.
+//
+// Rows past M or N and K past the end read as zero: buffer descriptors that
+// cover the valid rows, and offsets out of range for chunks behind K.
 #include "fp8bl_device.h"
 #include "fp8bl_ops.h"
 
@@ -14,65 +33,398 @@ namespace fp8bl {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
+constexpr int kBK = 128;
 constexpr int kThreads = 256;
+constexpr uint32_t kOob = 0x80000000u;
 
-// 64 x 64 outputs a workgroup, 64 rows of X by 16 columns a wave, operands
-// straight from memory.
-__global__ __launch_bounds__(kThreads)
-void gemm_int8_kernel(const int8_t* __restrict__ xq, const float* __restrict__ xs, const int8_t* __restrict__ wq,
-                      const float* __restrict__ ws, const uint16_t* __restrict__ bias, uint16_t* __restrict__ y,
-                      int M, int N, int K, int tiles_n) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * 64;
-  const int n0 = (int)(blockIdx.x % tiles_n) * 64 + 16 * wave;
-  const int r = lane & 15, g = lane >> 4;
-  i32x4 acc[4] = {};
-  for (int k0 = 0; k0 < K; k0 += 64) {
-    const int c = k0 + 16 * g;
-    i32x4 a = {}, b[4] = {};
-    if (c < K) {
-      if (n0 + r < N) a = *reinterpret_cast<const i32x4*>(wq + (size_t)(n0 + r) * K + c);
+constexpr int vm_wait(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
+constexpr int kLgkmWait0 = 0xC07F;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, __builtin_amdgcn_readfirstlane((int)bytes),
+                                           0x00020000);
+}
+
+struct GemmArgs {
+  const int8_t* xq;
+  const float* xs;
+  const int8_t* wq;
+  const float* ws;
+  const uint16_t* bias;
+  uint16_t* y;
+  int32_t* part;
+  int M, N, K;
+  int tiles_m, tiles_n, splits, steps_per_unit, steps;
+};
+
+template <int WM, int WN, int S>
+struct Tile {
+  static constexpr int kTM = 64 * WM, kTN = 64 * WN;
+  static constexpr int kStage = (kTM + kTN) * kBK;
+  static constexpr int kXLoads = kTM / 32, kWLoads = kTN / 32;    // of 8 rows, for each wave and step
+  static constexpr int kLoads = kXLoads + kWLoads;
+  static_assert(S * kStage + (2 * kTN + kTM) * 4 <= 160 * 1024, "the stages and the epilogue's vectors fit the LDS");
+  static_assert((S - 1) * kLoads <= 63, "outstanding loads fit the counter");
+};
+
+template <int WM, int WN, int S, bool SPLIT>
+__global__ __launch_bounds__(kThreads, 1)
+void gemm_int8_kernel(GemmArgs g) {
+  using T = Tile<WM, WN, S>;
+  constexpr int kTM = T::kTM, kTN = T::kTN, kStage = T::kStage;
+  // The stages and the epilogue's vectors in one array: with several, the
+  // compiler tells their accesses apart and waits for every load into LDS
+  // before the next read of it.
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S * kStage + (2 * kTN + kTM) * 4];
+  float* const ep_ws = reinterpret_cast<float*>(&lds[S * kStage]);
+  float* const ep_bias = ep_ws + kTN;
+  float* const ep_xs = ep_bias + kTN;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  const int M = g.M, N = g.N, K = g.K;
+
+  // ---- Units (tile, K split), dealt to the persistent workgroups round-robin;
+  // each XCD gets a contiguous run, walked in groups of 8 M-tiles.
+  const int ntiles = g.tiles_m * g.tiles_n;
+  const int units = ntiles * g.splits;
+  const int my_units = (units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  struct Unit {
+    int m0, n0, step0, nsteps, split;
+  };
+  auto unit_of = [&](int i) -> Unit {
+    Unit U{0, 0, 0, 0, 0};              // past the last unit: nothing to load
+    if (i >= my_units) return U;
+    const int u = (int)blockIdx.x + i * (int)gridDim.x;
+    const int r = (units & 7) == 0 ? (u & 7) * (units >> 3) + (u >> 3) : u;
+    U.split = r / ntiles;
+    const int id = r - U.split * ntiles;
+    constexpr int GM = 8;
+    const int group = id / (GM * g.tiles_n);
+    const int first_m = group * GM;
+    const int gsize = min(g.tiles_m - first_m, GM);
+    const int in_group = id - group * GM * g.tiles_n;
+    U.m0 = (first_m + in_group % gsize) * kTM;
+    U.n0 = (in_group / gsize) * kTN;
+    U.step0 = U.split * g.steps_per_unit;
+    U.nsteps = min(g.steps_per_unit, g.steps - U.step0);
+    return U;
+  };
+
+  // ---- Loads. Load j of wave w fills 8 rows from (TM / 4) w + 8 j on: lane l
+  // lands on row l / 8 of them at physical chunk l % 8 and fetches the logical
+  // chunk that lies there.
+  const int c_even = (lane & 7) ^ (lane >> 3);
+  uint32_t xvo[T::kXLoads], wvo[T::kWLoads];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (m0 + 16 * i + r < M) b[i] = *reinterpret_cast<const i32x4*>(xq + (size_t)(m0 + 16 * i + r) * K + c);
+  for (int j = 0; j < T::kXLoads; ++j)
+    xvo[j] = (uint32_t)(((kTM / 4) * wave + 8 * j + (lane >> 3)) * K + (c_even ^ (j & 1)) * 16);
+#pragma unroll
+  for (int j = 0; j < T::kWLoads; ++j)
+    wvo[j] = (uint32_t)(((kTN / 4) * wave + 8 * j + (lane >> 3)) * K + (c_even ^ (j & 1)) * 16);
+  Unit LU;
+  __amdgpu_buffer_rsrc_t xrs, wrs;
+  auto set_load_unit = [&](const Unit& U) {
+    LU = U;
+    xrs = make_rsrc(g.xq + (size_t)U.m0 * K, (uint32_t)(U.nsteps > 0 ? min(M - U.m0, kTM) * K : 0));
+    wrs = make_rsrc(g.wq + (size_t)U.n0 * K, (uint32_t)(U.nsteps > 0 ? min(N - U.n0, kTN) * K : 0));
+  };
+  // load i (of kLoads) of step `kt` of the load unit into the stage at `sb`
+  auto issue = [&](int sb, int kt, int i) {
+    const int kbase = (LU.step0 + kt) * kBK;
+    const int klim = kt < LU.nsteps ? K - kbase : 0;
+    const bool of_x = i < T::kXLoads;
+    const int j = of_x ? i : i - T::kXLoads;
+    const bool in = (c_even ^ (j & 1)) * 16 < klim;
+    const uint32_t vo = of_x ? xvo[of_x ? j : 0] : wvo[of_x ? 0 : j];
+    const int row = of_x ? (kTM / 4) * wave + 8 * j : kTM + (kTN / 4) * wave + 8 * j;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(of_x ? xrs : wrs, (lds_ptr_t)&lds[sb + row * kBK], 16, in ? vo : kOob,
+                                             (uint32_t)kbase, 0, 0);
+  };
+
+  // ---- Operands of slice s of a stage.
+  const int r32 = lane & 31, half = lane >> 5;
+  const int swz = (r32 & 7) ^ ((r32 >> 3) & 1);
+  const int xrow = (32 * WM * wm + r32) * kBK, wrow = (kTM + 32 * WN * wn + r32) * kBK;
+  auto read_x = [&](int sb, int s, int b) -> i32x4 {
+    return *reinterpret_cast<const i32x4*>(&lds[sb + xrow + 32 * b * kBK + (((2 * s + half) ^ swz) << 4)]);
+  };
+  auto read_w = [&](int sb, int s, int b) -> i32x4 {
+    return *reinterpret_cast<const i32x4*>(&lds[sb + wrow + 32 * b * kBK + (((2 * s + half) ^ swz) << 4)]);
+  };
+
+  auto wg_barrier = [] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  // Prologue: the first S steps; wait for the first of them.
+  set_load_unit(unit_of(0));
+  int lci = 0, lkt = 0;                // the next step to load: of unit lci
+  auto next_load = [&] {
+    if (++lkt == g.steps_per_unit) {
+      lkt = 0;
+      set_load_unit(unit_of(++lci));
+    }
+  };
+#pragma unroll
+  for (int a = 0; a < S; ++a) {
+#pragma unroll
+    for (int i = 0; i < T::kLoads; ++i) issue(a * kStage, lkt, i);
+    next_load();
+  }
+  __builtin_amdgcn_s_waitcnt(vm_wait((S - 1) * T::kLoads));
+  wg_barrier();
+
+  i32x4 xf[2][WM], wf[2][WN];
+#pragma unroll
+  for (int b = 0; b < WM; ++b) xf[0][b] = read_x(0, 0, b);
+#pragma unroll
+  for (int b = 0; b < WN; ++b) wf[0][b] = read_w(0, 0, b);
+
+  i32x16 acc[WN][WM];
+#pragma unroll
+  for (int n = 0; n < WN; ++n)
+#pragma unroll
+    for (int m = 0; m < WM; ++m) acc[n][m] = i32x16{};
+
+  int stage = 0;
+  for (int ci = 0; ci < my_units; ++ci) {
+    const Unit CU = unit_of(ci);
+    for (int kt = 0; kt < g.steps_per_unit; ++kt) {
+      const int sb = stage * kStage;
+      const int nstage = stage + 1 == S ? 0 : stage + 1;
+      const int sbn = nstage * kStage;
+      const bool last = kt == g.steps_per_unit - 1;
+      // the epilogue's vectors, one element a thread: on their way during the
+      // unit's last step
+      uint32_t e_ws = 0, e_xs = 0, e_bias = 0;
+      if (!SPLIT && last) {
+        e_ws = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(g.ws + CU.n0, (uint32_t)min(N - CU.n0, kTN) * 4), tid * 4, 0, 0);
+        e_xs = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(g.xs + CU.m0, (uint32_t)min(M - CU.m0, kTM) * 4), tid * 4, 0, 0);
+        if (g.bias)
+          e_bias = __builtin_amdgcn_raw_buffer_load_b16(make_rsrc(g.bias + CU.n0, (uint32_t)min(N - CU.n0, kTN) * 2), tid * 2, 0, 0);
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (s == 3) {
+          // this wave's reads of the stage have returned and its loads of the
+          // next stage have landed; behind the barrier so have all waves'
+          __builtin_amdgcn_s_waitcnt(kLgkmWait0);
+          __builtin_amdgcn_s_waitcnt(vm_wait((S - 2) * T::kLoads));
+          if (kt == 0 || last) __builtin_amdgcn_s_waitcnt(vm_wait(0));      // the last epilogue's stores among them
+          if (!SPLIT && last) {
+            asm volatile("" : "+v"(e_bias));     // not looked at before the wait above
+            if (tid < kTN) ep_ws[tid] = __uint_as_float(e_ws), ep_bias[tid] = __uint_as_float(e_bias << 16);
+            if (tid < kTM) ep_xs[tid] = __uint_as_float(e_xs);
+            __builtin_amdgcn_s_waitcnt(kLgkmWait0);
+          }
+          wg_barrier();
+        }
+        const int cur = s & 1, nxt = cur ^ 1;
+        const int rb = s == 3 ? sbn : sb;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int b = 0; b < WN; ++b) wf[nxt][b] = read_w(rb, (s + 1) & 3, b);
+#pragma unroll
+        for (int b = 0; b < WM; ++b) xf[nxt][b] = read_x(rb, (s + 1) & 3, b);
+        if (s == 3) {
+#pragma unroll
+          for (int i = 0; i < T::kLoads; ++i) issue(sb, lkt, i);
+        }
+#pragma unroll
+        for (int n = 0; n < WN; ++n)
+#pragma unroll
+          for (int m = 0; m < WM; ++m)
+            acc[n][m] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[cur][n], xf[cur][m], acc[n][m], 0, 0, 0);
+        // reads behind the first products, in the last slice loads behind the others
+        constexpr int kProducts = WM * WN, kReads = WM + WN, kEvery = kReads > kProducts / 2 ? 2 * kReads / kProducts : 1;
+        constexpr int kFirst = kReads / kEvery, kRest = kProducts > kFirst ? kProducts - kFirst : 1;
+#pragma unroll
+        for (int i = 0; i < kProducts; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                     // MFMA
+          if (i < kFirst) __builtin_amdgcn_sched_group_barrier(0x100, kEvery, 0);                // DS read
+          if (s == 3 && i >= kFirst)
+            __builtin_amdgcn_sched_group_barrier(0x020, (T::kLoads + kRest - 1) / kRest, 0);     // VMEM
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      next_load();
+      stage = nstage;
+    }
+
+    // ---- Epilogue of unit ci.
+    int le;
+    asm volatile("" : "=v"(le) : "0"(lane));     // keeps the addresses below out of the loop's registers
+    const int er = le & 31, eh = le >> 5;
+    const int row0 = 32 * WM * wm + er;          // in the tile
+    const int rows = M - CU.m0;
+    const int col0 = 32 * WN * wn;
+    if constexpr (SPLIT) {
+      int32_t* const p = g.part + (size_t)CU.split * partial_slab(M, N);
+#pragma unroll
+      for (int m = 0; m < WM; ++m) {
+        const int row = row0 + 32 * m;
+#pragma unroll
+        for (int n = 0; n < WN; ++n)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int col = CU.n0 + col0 + 32 * n + 8 * q + 4 * eh;
+            const i32x4 v = {acc[n][m][4 * q], acc[n][m][4 * q + 1], acc[n][m][4 * q + 2], acc[n][m][4 * q + 3]};
+            int32_t* const to = p + ((size_t)CU.m0 + row) * N + col;
+            if (row < rows && col + 4 <= N)
+              __builtin_memcpy(to, &v, 16);
+            else if (row < rows)
+              for (int i = 0; i < 4; ++i)
+                if (col + i < N) to[i] = v[i];
+          }
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < WN; ++n)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {            // column groups 2 p and 2 p + 1
+          __builtin_amdgcn_sched_barrier(0);     // a few sums at a time in registers
+          float w[2][4], b[2][4];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int at = col0 + 32 * n + 16 * p + 8 * q + 4 * eh;
+            const f32x4 wv = *reinterpret_cast<const f32x4*>(&ep_ws[at]);
+            const f32x4 bv = *reinterpret_cast<const f32x4*>(&ep_bias[at]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[q][i] = wv[i], b[q][i] = bv[i];
+          }
+#pragma unroll
+          for (int m = 0; m < WM; ++m) {
+            const float x = ep_xs[row0 + 32 * m];
+            uint32_t d[2][2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              float v[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                v[i] = (float)acc[n][m][4 * (2 * p + q) + i] * (x * w[q][i]);
+                if (g.bias) v[i] += b[q][i];
+              }
+              d[q][0] = pack_bf16x2(v[0], v[1]);
+              d[q][1] = pack_bf16x2(v[2], v[3]);
+            }
+            // halves of the wave trade groups: each lane then has 8 columns in a row
+            u32x4 out;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const auto t = __builtin_amdgcn_permlane32_swap(d[0][i], d[1][i], false, false);
+              out[i] = t[0];
+              out[2 + i] = t[1];
+            }
+            const int row = row0 + 32 * m;
+            const int col = CU.n0 + col0 + 32 * n + 16 * p + 8 * eh;
+            uint16_t* const to = g.y + ((size_t)CU.m0 + row) * N + col;
+            if (row < rows && col + 8 <= N)
+              __builtin_memcpy(to, &out, 16);
+            else if (row < rows)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (col + i < N) to[i] = (uint16_t)(out[i >> 1] >> (16 * (i & 1)));
+          }
+        }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b[i], acc[i], 0, 0, 0);
-  }
+    for (int n = 0; n < WN; ++n)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t row = m0 + 16 * i + r;
-    if (row >= M) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int col = n0 + 4 * g + j;
-      if (col >= N) continue;
-      float v = (float)acc[i][j] * (xs[row] * ws[col]);
-      if (bias) v += bf16_f32(bias[col]);
-      y[(size_t)row * N + col] = f32_bf16(v);
-    }
+      for (int m = 0; m < WM; ++m) acc[n][m] = i32x16{};
+    if constexpr (!SPLIT) wg_barrier();          // the vectors have been read
   }
+  __builtin_amdgcn_s_waitcnt(vm_wait(0));        // loads behind the last step still target the LDS
+}
+
+// Sum of the K splits' partials with the epilogue, four columns a thread.
+__global__ __launch_bounds__(256)
+void join_int8_kernel(GemmArgs g) {
+  const int64_t groups = (g.N + 3) / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = i / groups;
+  const int col = (int)(i - row * groups) * 4;
+  if (row >= g.M) return;
+  const size_t slab = partial_slab(g.M, g.N), at = (size_t)row * g.N + col;
+  const float x = g.xs[row];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (col + j >= g.N) break;
+    int t = 0;
+    for (int s = 0; s < g.splits; ++s) t += g.part[s * slab + at + j];
+    float v = (float)t * (x * g.ws[col + j]);
+    if (g.bias) v += bf16_f32(g.bias[col + j]);
+    g.y[at + j] = f32_bf16(v);
+  }
+}
+
+struct Plan {
+  int tile;        // 0: 256 x 256, 1: 128 x 128, 2: 64 x 64
+  int splits, steps_per_unit;
+};
+constexpr int kTileEdge[3] = {256, 128, 64};
+
+#ifndef INT8_PLAN
+Plan plan_int8(int64_t m, int64_t n, int64_t k) {
+  const int steps = (int)((k + kBK - 1) / kBK);
+  Plan p{0, 1, steps};
+  const int64_t t256 = ((m + 255) / 256) * ((n + 255) / 256), t128 = ((m + 127) / 128) * ((n + 127) / 128);
+  p.tile = t256 >= 192 ? 0 : t128 >= 192 ? 1 : 2;
+  return p;
+}
+#else
+Plan plan_int8(int64_t m, int64_t n, int64_t k) {
+  const int steps = (int)((k + kBK - 1) / kBK);
+  Plan p{atoi(getenv("I8_TILE")), atoi(getenv("I8_SPLITS")), 0};
+  p.steps_per_unit = (steps + p.splits - 1) / p.splits;
+  p.splits = (steps + p.steps_per_unit - 1) / p.steps_per_unit;
+  return p;
+}
+#endif
+
+template <int WM, int WN, int S>
+hipError_t launch_tiles(GemmArgs g, hipStream_t stream) {
+  constexpr int tm = Tile<WM, WN, S>::kTM, tn = Tile<WM, WN, S>::kTN;
+  g.tiles_m = (g.M + tm - 1) / tm;
+  g.tiles_n = (g.N + tn - 1) / tn;
+  const int64_t units = (int64_t)g.tiles_m * g.tiles_n * g.splits;
+  const int64_t most = (int64_t)device_cus() * (160 * 1024 / (S * Tile<WM, WN, S>::kStage + (2 * tn + tm) * 4));
+  const dim3 grid((uint32_t)(units < most ? units : most));
+  if (g.splits == 1)
+    hipLaunchKernelGGL((gemm_int8_kernel<WM, WN, S, false>), grid, dim3(kThreads), 0, stream, g);
+  else
+    hipLaunchKernelGGL((gemm_int8_kernel<WM, WN, S, true>), grid, dim3(kThreads), 0, stream, g);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || g.splits == 1) return e;
+  const int64_t threads = (int64_t)g.M * ((g.N + 3) / 4);
+  hipLaunchKernelGGL(join_int8_kernel, dim3((uint32_t)((threads + 255) / 256)), dim3(256), 0, stream, g);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-size_t int8_gemm_bytes(int64_t, int64_t, int64_t) { return 0; }
+size_t int8_gemm_bytes(int64_t m, int64_t n, int64_t k) {
+  const Plan p = plan_int8(m, n, k);
+  return p.splits <= 1 ? 0 : round_up((size_t)p.splits * partial_slab(m, n) * sizeof(int32_t), kWorkspaceAlign);
+}
 
 hipError_t launch_int8_gemm(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws,
-                            const uint16_t* bias, uint16_t* y, int64_t m, int64_t n, int64_t k, void*,
+                            const uint16_t* bias, uint16_t* y, int64_t m, int64_t n, int64_t k, void* workspace,
                             hipStream_t stream) {
-  const int64_t tiles_n = (n + 63) / 64;
-  const int64_t rows = 64 * (((int64_t)1 << 23) / tiles_n);   // a launch has fewer than 2^32 threads
-  for (int64_t r0 = 0; r0 < m; r0 += rows) {
-    const int64_t mr = m - r0 < rows ? m - r0 : rows;
-    hipLaunchKernelGGL(gemm_int8_kernel, dim3((uint32_t)((mr + 63) / 64 * tiles_n)), dim3(kThreads), 0, stream,
-                       xq + (size_t)r0 * k, xs + r0, wq, ws, bias, y + (size_t)r0 * n, (int)mr, (int)n, (int)k,
-                       (int)tiles_n);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  const Plan p = plan_int8(m, n, k);
+  GemmArgs g{xq, xs, wq, ws, bias, y, static_cast<int32_t*>(workspace), (int)m, (int)n, (int)k, 0, 0, p.splits,
+             p.steps_per_unit, (int)((k + kBK - 1) / kBK)};
+  switch (p.tile) {
+    case 0: return launch_tiles<4, 4, 2>(g, stream);
+    case 1: return launch_tiles<2, 2, 4>(g, stream);
+    default: return launch_tiles<1, 1, 4>(g, stream);
   }
-  return hipSuccess;
 }
 
 }  // namespace fp8bl
