@@ -16,6 +16,14 @@ size_t int8_gemm_bytes(int64_t m, int64_t n, int64_t k);
 hipError_t launch_int8_gemm(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws,
                             const uint16_t* bias, uint16_t* y, int64_t m, int64_t n, int64_t k, void* workspace,
                             hipStream_t stream);
+// At up to kInt8SkinnyRows rows; and from a bf16 x of few rows, quantized on the
+// way (int8_skinny_quantizes).
+constexpr int64_t kInt8SkinnyRows = 32;
+hipError_t launch_int8_skinny(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws,
+                              const uint16_t* bias, uint16_t* y, int64_t m, int64_t n, int64_t k, hipStream_t stream);
+bool int8_skinny_quantizes(int64_t m, int64_t n, int64_t k);
+hipError_t launch_int8_skinny_bf16(const uint16_t* x, const int8_t* wq, const float* ws, const uint16_t* bias,
+                                   uint16_t* y, int64_t m, int64_t n, int64_t k, hipStream_t stream);
 
 // ---- From the QKV projection to its cache.
 hipError_t launch_qk_norm_rope(const fp8bl_qkv& a, hipStream_t stream);

@@ -36,7 +36,6 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
-constexpr int kBK = 128;
 constexpr int kThreads = 256;
 constexpr uint32_t kOob = 0x80000000u;
 
@@ -60,21 +59,22 @@ struct GemmArgs {
   int tiles_m, tiles_n, splits, steps_per_unit, steps;
 };
 
-template <int WM, int WN, int S>
+template <int WM, int WN, int BK, int S>
 struct Tile {
   static constexpr int kTM = 64 * WM, kTN = 64 * WN;
-  static constexpr int kStage = (kTM + kTN) * kBK;
-  static constexpr int kXLoads = kTM / 32, kWLoads = kTN / 32;    // of 8 rows, for each wave and step
+  static constexpr int kStage = (kTM + kTN) * BK;
+  static constexpr int kRows = 1024 / BK;                         // of a load
+  static constexpr int kXLoads = kTM / 4 / kRows, kWLoads = kTN / 4 / kRows;    // for each wave and step
   static constexpr int kLoads = kXLoads + kWLoads;
   static_assert(S * kStage + (2 * kTN + kTM) * 4 <= 160 * 1024, "the stages and the epilogue's vectors fit the LDS");
   static_assert((S - 1) * kLoads <= 63, "outstanding loads fit the counter");
 };
 
-template <int WM, int WN, int S, bool SPLIT>
+template <int WM, int WN, int BK, int S, bool SPLIT>
 __global__ __launch_bounds__(kThreads, 1)
 void gemm_int8_kernel(GemmArgs g) {
-  using T = Tile<WM, WN, S>;
-  constexpr int kTM = T::kTM, kTN = T::kTN, kStage = T::kStage;
+  using T = Tile<WM, WN, BK, S>;
+  constexpr int kTM = T::kTM, kTN = T::kTN, kStage = T::kStage, kSlices = BK / 32;
   // The stages and the epilogue's vectors in one array: with several, the
   // compiler tells their accesses apart and waits for every load into LDS
   // before the next read of it.
@@ -89,7 +89,7 @@ void gemm_int8_kernel(GemmArgs g) {
   const int M = g.M, N = g.N, K = g.K;
 
   // ---- Units (tile, K split), dealt to the persistent workgroups round-robin;
-  // each XCD gets a contiguous run, walked in groups of 8 M-tiles.
+  // each XCD gets a contiguous run, walked in groups of 4 M-tiles.
   const int ntiles = g.tiles_m * g.tiles_n;
   const int units = ntiles * g.splits;
   const int my_units = (units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
@@ -103,7 +103,7 @@ void gemm_int8_kernel(GemmArgs g) {
     const int r = (units & 7) == 0 ? (u & 7) * (units >> 3) + (u >> 3) : u;
     U.split = r / ntiles;
     const int id = r - U.split * ntiles;
-    constexpr int GM = 8;
+    constexpr int GM = 4;
     const int group = id / (GM * g.tiles_n);
     const int first_m = group * GM;
     const int gsize = min(g.tiles_m - first_m, GM);
@@ -115,17 +115,21 @@ void gemm_int8_kernel(GemmArgs g) {
     return U;
   };
 
-  // ---- Loads. Load j of wave w fills 8 rows from (TM / 4) w + 8 j on: lane l
-  // lands on row l / 8 of them at physical chunk l % 8 and fetches the logical
-  // chunk that lies there.
-  const int c_even = (lane & 7) ^ (lane >> 3);
+  // ---- Loads. Load j of wave w fills kRows rows from (TM / 4) w + kRows j on:
+  // lane l lands on row l / kChunks of them at physical chunk l % kChunks and
+  // fetches the logical chunk that lies there.
+  constexpr int kChunks = BK / 16;
+  const int lrow = lane / kChunks;
+  auto logical = [&](int j) {
+    return BK == 128 ? (lane & 7) ^ (lane >> 3) ^ (j & 1) : (lane & 3) ^ (lane >> 4);
+  };
   uint32_t xvo[T::kXLoads], wvo[T::kWLoads];
 #pragma unroll
   for (int j = 0; j < T::kXLoads; ++j)
-    xvo[j] = (uint32_t)(((kTM / 4) * wave + 8 * j + (lane >> 3)) * K + (c_even ^ (j & 1)) * 16);
+    xvo[j] = (uint32_t)(((kTM / 4) * wave + T::kRows * j + lrow) * K + logical(j) * 16);
 #pragma unroll
   for (int j = 0; j < T::kWLoads; ++j)
-    wvo[j] = (uint32_t)(((kTN / 4) * wave + 8 * j + (lane >> 3)) * K + (c_even ^ (j & 1)) * 16);
+    wvo[j] = (uint32_t)(((kTN / 4) * wave + T::kRows * j + lrow) * K + logical(j) * 16);
   Unit LU;
   __amdgpu_buffer_rsrc_t xrs, wrs;
   auto set_load_unit = [&](const Unit& U) {
@@ -135,26 +139,26 @@ void gemm_int8_kernel(GemmArgs g) {
   };
   // load i (of kLoads) of step `kt` of the load unit into the stage at `sb`
   auto issue = [&](int sb, int kt, int i) {
-    const int kbase = (LU.step0 + kt) * kBK;
+    const int kbase = (LU.step0 + kt) * BK;
     const int klim = kt < LU.nsteps ? K - kbase : 0;
     const bool of_x = i < T::kXLoads;
     const int j = of_x ? i : i - T::kXLoads;
-    const bool in = (c_even ^ (j & 1)) * 16 < klim;
+    const bool in = logical(j) * 16 < klim;
     const uint32_t vo = of_x ? xvo[of_x ? j : 0] : wvo[of_x ? 0 : j];
-    const int row = of_x ? (kTM / 4) * wave + 8 * j : kTM + (kTN / 4) * wave + 8 * j;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(of_x ? xrs : wrs, (lds_ptr_t)&lds[sb + row * kBK], 16, in ? vo : kOob,
+    const int row = of_x ? (kTM / 4) * wave + T::kRows * j : kTM + (kTN / 4) * wave + T::kRows * j;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(of_x ? xrs : wrs, (lds_ptr_t)&lds[sb + row * BK], 16, in ? vo : kOob,
                                              (uint32_t)kbase, 0, 0);
   };
 
   // ---- Operands of slice s of a stage.
   const int r32 = lane & 31, half = lane >> 5;
-  const int swz = (r32 & 7) ^ ((r32 >> 3) & 1);
-  const int xrow = (32 * WM * wm + r32) * kBK, wrow = (kTM + 32 * WN * wn + r32) * kBK;
+  const int swz = BK == 128 ? (r32 & 7) ^ ((r32 >> 3) & 1) : (r32 >> 2) & 3;
+  const int xrow = (32 * WM * wm + r32) * BK, wrow = (kTM + 32 * WN * wn + r32) * BK;
   auto read_x = [&](int sb, int s, int b) -> i32x4 {
-    return *reinterpret_cast<const i32x4*>(&lds[sb + xrow + 32 * b * kBK + (((2 * s + half) ^ swz) << 4)]);
+    return *reinterpret_cast<const i32x4*>(&lds[sb + xrow + 32 * b * BK + (((2 * s + half) ^ swz) << 4)]);
   };
   auto read_w = [&](int sb, int s, int b) -> i32x4 {
-    return *reinterpret_cast<const i32x4*>(&lds[sb + wrow + 32 * b * kBK + (((2 * s + half) ^ swz) << 4)]);
+    return *reinterpret_cast<const i32x4*>(&lds[sb + wrow + 32 * b * BK + (((2 * s + half) ^ swz) << 4)]);
   };
 
   auto wg_barrier = [] {
@@ -211,8 +215,8 @@ void gemm_int8_kernel(GemmArgs g) {
           e_bias = __builtin_amdgcn_raw_buffer_load_b16(make_rsrc(g.bias + CU.n0, (uint32_t)min(N - CU.n0, kTN) * 2), tid * 2, 0, 0);
       }
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if (s == 3) {
+      for (int s = 0; s < kSlices; ++s) {
+        if (s == kSlices - 1) {
           // this wave's reads of the stage have returned and its loads of the
           // next stage have landed; behind the barrier so have all waves'
           __builtin_amdgcn_s_waitcnt(kLgkmWait0);
@@ -227,13 +231,13 @@ void gemm_int8_kernel(GemmArgs g) {
           wg_barrier();
         }
         const int cur = s & 1, nxt = cur ^ 1;
-        const int rb = s == 3 ? sbn : sb;
+        const int rb = s == kSlices - 1 ? sbn : sb;
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int b = 0; b < WN; ++b) wf[nxt][b] = read_w(rb, (s + 1) & 3, b);
+        for (int b = 0; b < WN; ++b) wf[nxt][b] = read_w(rb, (s + 1) % kSlices, b);
 #pragma unroll
-        for (int b = 0; b < WM; ++b) xf[nxt][b] = read_x(rb, (s + 1) & 3, b);
-        if (s == 3) {
+        for (int b = 0; b < WM; ++b) xf[nxt][b] = read_x(rb, (s + 1) % kSlices, b);
+        if (s == kSlices - 1) {
 #pragma unroll
           for (int i = 0; i < T::kLoads; ++i) issue(sb, lkt, i);
         }
@@ -249,7 +253,7 @@ void gemm_int8_kernel(GemmArgs g) {
         for (int i = 0; i < kProducts; ++i) {
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                     // MFMA
           if (i < kFirst) __builtin_amdgcn_sched_group_barrier(0x100, kEvery, 0);                // DS read
-          if (s == 3 && i >= kFirst)
+          if (s == kSlices - 1 && i >= kFirst)
             __builtin_amdgcn_sched_group_barrier(0x020, (T::kLoads + kRest - 1) / kRest, 0);     // VMEM
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -366,40 +370,33 @@ void join_int8_kernel(GemmArgs g) {
 
 struct Plan {
   int tile;        // 0: 256 x 256, 1: 128 x 128, 2: 64 x 64
-  int splits, steps_per_unit;
+  int splits;
 };
-constexpr int kTileEdge[3] = {256, 128, 64};
 
 #ifndef INT8_PLAN
 Plan plan_int8(int64_t m, int64_t n, int64_t k) {
-  const int steps = (int)((k + kBK - 1) / kBK);
-  Plan p{0, 1, steps};
   const int64_t t256 = ((m + 255) / 256) * ((n + 255) / 256), t128 = ((m + 127) / 128) * ((n + 127) / 128);
-  p.tile = t256 >= 192 ? 0 : t128 >= 192 ? 1 : 2;
-  return p;
+  return Plan{t256 >= 192 ? 0 : t128 >= 192 ? 1 : 2, 1};
 }
 #else
-Plan plan_int8(int64_t m, int64_t n, int64_t k) {
-  const int steps = (int)((k + kBK - 1) / kBK);
-  Plan p{atoi(getenv("I8_TILE")), atoi(getenv("I8_SPLITS")), 0};
-  p.steps_per_unit = (steps + p.splits - 1) / p.splits;
-  p.splits = (steps + p.steps_per_unit - 1) / p.steps_per_unit;
-  return p;
-}
+Plan plan_int8(int64_t m, int64_t n, int64_t k) { return Plan{atoi(getenv("I8_TILE")), atoi(getenv("I8_SPLITS"))}; }
 #endif
 
-template <int WM, int WN, int S>
+template <int WM, int WN, int BK, int S>
 hipError_t launch_tiles(GemmArgs g, hipStream_t stream) {
-  constexpr int tm = Tile<WM, WN, S>::kTM, tn = Tile<WM, WN, S>::kTN;
+  constexpr int tm = Tile<WM, WN, BK, S>::kTM, tn = Tile<WM, WN, BK, S>::kTN;
+  g.steps = (g.K + BK - 1) / BK;
+  g.steps_per_unit = (g.steps + g.splits - 1) / g.splits;
+  g.splits = (g.steps + g.steps_per_unit - 1) / g.steps_per_unit;
   g.tiles_m = (g.M + tm - 1) / tm;
   g.tiles_n = (g.N + tn - 1) / tn;
   const int64_t units = (int64_t)g.tiles_m * g.tiles_n * g.splits;
-  const int64_t most = (int64_t)device_cus() * (160 * 1024 / (S * Tile<WM, WN, S>::kStage + (2 * tn + tm) * 4));
+  const int64_t most = (int64_t)device_cus() * (160 * 1024 / (S * Tile<WM, WN, BK, S>::kStage + (2 * tn + tm) * 4));
   const dim3 grid((uint32_t)(units < most ? units : most));
   if (g.splits == 1)
-    hipLaunchKernelGGL((gemm_int8_kernel<WM, WN, S, false>), grid, dim3(kThreads), 0, stream, g);
+    hipLaunchKernelGGL((gemm_int8_kernel<WM, WN, BK, S, false>), grid, dim3(kThreads), 0, stream, g);
   else
-    hipLaunchKernelGGL((gemm_int8_kernel<WM, WN, S, true>), grid, dim3(kThreads), 0, stream, g);
+    hipLaunchKernelGGL((gemm_int8_kernel<WM, WN, BK, S, true>), grid, dim3(kThreads), 0, stream, g);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || g.splits == 1) return e;
   const int64_t threads = (int64_t)g.M * ((g.N + 3) / 4);
@@ -410,6 +407,7 @@ hipError_t launch_tiles(GemmArgs g, hipStream_t stream) {
 }  // namespace
 
 size_t int8_gemm_bytes(int64_t m, int64_t n, int64_t k) {
+  if (m <= kInt8SkinnyRows) return 0;
   const Plan p = plan_int8(m, n, k);
   return p.splits <= 1 ? 0 : round_up((size_t)p.splits * partial_slab(m, n) * sizeof(int32_t), kWorkspaceAlign);
 }
@@ -417,13 +415,23 @@ size_t int8_gemm_bytes(int64_t m, int64_t n, int64_t k) {
 hipError_t launch_int8_gemm(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws,
                             const uint16_t* bias, uint16_t* y, int64_t m, int64_t n, int64_t k, void* workspace,
                             hipStream_t stream) {
+  if (m <= kInt8SkinnyRows) return launch_int8_skinny(xq, xs, wq, ws, bias, y, m, n, k, stream);
   const Plan p = plan_int8(m, n, k);
-  GemmArgs g{xq, xs, wq, ws, bias, y, static_cast<int32_t*>(workspace), (int)m, (int)n, (int)k, 0, 0, p.splits,
-             p.steps_per_unit, (int)((k + kBK - 1) / kBK)};
+  const GemmArgs g{xq, xs, wq, ws, bias, y, static_cast<int32_t*>(workspace), (int)m, (int)n, (int)k, 0, 0, p.splits,
+                   0, 0};
   switch (p.tile) {
-    case 0: return launch_tiles<4, 4, 2>(g, stream);
-    case 1: return launch_tiles<2, 2, 4>(g, stream);
-    default: return launch_tiles<1, 1, 4>(g, stream);
+    case 0: return launch_tiles<4, 4, 128, 2>(g, stream);
+    case 1: return launch_tiles<2, 2, 128, 4>(g, stream);
+#ifdef INT8_PLAN
+    case 3: return launch_tiles<4, 4, 64, 4>(g, stream);
+    case 4: return launch_tiles<2, 4, 128, 3>(g, stream);
+    case 5: return launch_tiles<2, 4, 64, 6>(g, stream);
+    case 6: return launch_tiles<2, 2, 128, 2>(g, stream);
+    case 7: return launch_tiles<1, 2, 128, 4>(g, stream);
+    case 8: return launch_tiles<1, 1, 128, 8>(g, stream);
+    case 9: return launch_tiles<4, 2, 128, 3>(g, stream);
+#endif
+    default: return launch_tiles<1, 1, 128, 4>(g, stream);
   }
 }
 
