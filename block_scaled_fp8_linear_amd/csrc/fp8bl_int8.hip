@@ -108,8 +108,8 @@ FP8BL_EXPORT int int8_linear_bf16(const uint16_t* x, const int8_t* wq, const flo
   if (st != FP8BL_OK) return st;
   st = gate_current_device();
   if (st != FP8BL_OK) return st;
-  if (fp8bl::int8_skinny_quantizes(m, n, k))
-    return hip_status(fp8bl::launch_int8_skinny_bf16(x, wq, w_scale, bias, y, m, n, k, stream));
+  if (fp8bl::int8_skinny_quantizes(m, k))
+    return hip_status(fp8bl::launch_int8_skinny_bf16(x, wq, w_scale, bias, y, n, k, stream));
   uint8_t* const w = static_cast<uint8_t*>(workspace);
   int8_t* const xq = reinterpret_cast<int8_t*>(w);
   float* const xs = reinterpret_cast<float*>(w + codes_bytes(m, k));

@@ -36,6 +36,8 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
+constexpr int kBK = 128;             // K of a step
+constexpr int kSlices = kBK / 32;
 constexpr int kThreads = 256;
 constexpr uint32_t kOob = 0x80000000u;
 
@@ -59,22 +61,22 @@ struct GemmArgs {
   int tiles_m, tiles_n, splits, steps_per_unit, steps;
 };
 
-template <int WM, int WN, int BK, int S>
+template <int WM, int WN, int S>
 struct Tile {
   static constexpr int kTM = 64 * WM, kTN = 64 * WN;
-  static constexpr int kStage = (kTM + kTN) * BK;
-  static constexpr int kRows = 1024 / BK;                         // of a load
+  static constexpr int kStage = (kTM + kTN) * kBK;
+  static constexpr int kRows = 1024 / kBK;                        // of a load
   static constexpr int kXLoads = kTM / 4 / kRows, kWLoads = kTN / 4 / kRows;    // for each wave and step
   static constexpr int kLoads = kXLoads + kWLoads;
   static_assert(S * kStage + (2 * kTN + kTM) * 4 <= 160 * 1024, "the stages and the epilogue's vectors fit the LDS");
   static_assert((S - 1) * kLoads <= 63, "outstanding loads fit the counter");
 };
 
-template <int WM, int WN, int BK, int S, bool SPLIT>
+template <int WM, int WN, int S, bool SPLIT>
 __global__ __launch_bounds__(kThreads, 1)
 void gemm_int8_kernel(GemmArgs g) {
-  using T = Tile<WM, WN, BK, S>;
-  constexpr int kTM = T::kTM, kTN = T::kTN, kStage = T::kStage, kSlices = BK / 32;
+  using T = Tile<WM, WN, S>;
+  constexpr int kTM = T::kTM, kTN = T::kTN, kStage = T::kStage;
   // The stages and the epilogue's vectors in one array: with several, the
   // compiler tells their accesses apart and waits for every load into LDS
   // before the next read of it.
@@ -118,11 +120,9 @@ void gemm_int8_kernel(GemmArgs g) {
   // ---- Loads. Load j of wave w fills kRows rows from (TM / 4) w + kRows j on:
   // lane l lands on row l / kChunks of them at physical chunk l % kChunks and
   // fetches the logical chunk that lies there.
-  constexpr int kChunks = BK / 16;
+  constexpr int kChunks = kBK / 16;
   const int lrow = lane / kChunks;
-  auto logical = [&](int j) {
-    return BK == 128 ? (lane & 7) ^ (lane >> 3) ^ (j & 1) : (lane & 3) ^ (lane >> 4);
-  };
+  auto logical = [&](int j) { return (lane & 7) ^ (lane >> 3) ^ (j & 1); };
   uint32_t xvo[T::kXLoads], wvo[T::kWLoads];
 #pragma unroll
   for (int j = 0; j < T::kXLoads; ++j)
@@ -139,26 +139,26 @@ void gemm_int8_kernel(GemmArgs g) {
   };
   // load i (of kLoads) of step `kt` of the load unit into the stage at `sb`
   auto issue = [&](int sb, int kt, int i) {
-    const int kbase = (LU.step0 + kt) * BK;
+    const int kbase = (LU.step0 + kt) * kBK;
     const int klim = kt < LU.nsteps ? K - kbase : 0;
     const bool of_x = i < T::kXLoads;
     const int j = of_x ? i : i - T::kXLoads;
     const bool in = logical(j) * 16 < klim;
     const uint32_t vo = of_x ? xvo[of_x ? j : 0] : wvo[of_x ? 0 : j];
     const int row = of_x ? (kTM / 4) * wave + T::kRows * j : kTM + (kTN / 4) * wave + T::kRows * j;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(of_x ? xrs : wrs, (lds_ptr_t)&lds[sb + row * BK], 16, in ? vo : kOob,
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(of_x ? xrs : wrs, (lds_ptr_t)&lds[sb + row * kBK], 16, in ? vo : kOob,
                                              (uint32_t)kbase, 0, 0);
   };
 
   // ---- Operands of slice s of a stage.
   const int r32 = lane & 31, half = lane >> 5;
-  const int swz = BK == 128 ? (r32 & 7) ^ ((r32 >> 3) & 1) : (r32 >> 2) & 3;
-  const int xrow = (32 * WM * wm + r32) * BK, wrow = (kTM + 32 * WN * wn + r32) * BK;
+  const int swz = (r32 & 7) ^ ((r32 >> 3) & 1);
+  const int xrow = (32 * WM * wm + r32) * kBK, wrow = (kTM + 32 * WN * wn + r32) * kBK;
   auto read_x = [&](int sb, int s, int b) -> i32x4 {
-    return *reinterpret_cast<const i32x4*>(&lds[sb + xrow + 32 * b * BK + (((2 * s + half) ^ swz) << 4)]);
+    return *reinterpret_cast<const i32x4*>(&lds[sb + xrow + 32 * b * kBK + (((2 * s + half) ^ swz) << 4)]);
   };
   auto read_w = [&](int sb, int s, int b) -> i32x4 {
-    return *reinterpret_cast<const i32x4*>(&lds[sb + wrow + 32 * b * BK + (((2 * s + half) ^ swz) << 4)]);
+    return *reinterpret_cast<const i32x4*>(&lds[sb + wrow + 32 * b * kBK + (((2 * s + half) ^ swz) << 4)]);
   };
 
   auto wg_barrier = [] {
@@ -347,24 +347,42 @@ void gemm_int8_kernel(GemmArgs g) {
   __builtin_amdgcn_s_waitcnt(vm_wait(0));        // loads behind the last step still target the LDS
 }
 
-// Sum of the K splits' partials with the epilogue, four columns a thread.
+// Sum of the K splits' partials with the epilogue, four columns a thread. Rows
+// of partials start at any multiple of four bytes.
 __global__ __launch_bounds__(256)
-void join_int8_kernel(GemmArgs g) {
-  const int64_t groups = (g.N + 3) / 4;
+void join_int8_kernel(const int32_t* __restrict__ part, const float* __restrict__ xs, const float* __restrict__ ws,
+                      const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int splits, int M, int N) {
+  const int64_t groups = (N + 3) / 4;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t row = i / groups;
   const int col = (int)(i - row * groups) * 4;
-  if (row >= g.M) return;
-  const size_t slab = partial_slab(g.M, g.N), at = (size_t)row * g.N + col;
-  const float x = g.xs[row];
+  if (row >= M) return;
+  const size_t slab = partial_slab(M, N), at = (size_t)row * N + col;
+  const float x = xs[row];
+  if (col + 4 <= N) {
+    i32x4 t = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      i32x4 p;
+      __builtin_memcpy(&p, part + s * slab + at, 16);
+      t += p;
+    }
+    float v[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (col + j >= g.N) break;
+    for (int j = 0; j < 4; ++j) {
+      v[j] = (float)t[j] * (x * ws[col + j]);
+      if (bias) v[j] += bf16_f32(bias[col + j]);
+    }
+    const u32x2 out = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    __builtin_memcpy(y + at, &out, 8);
+    return;
+  }
+  for (int j = 0; col + j < N; ++j) {
     int t = 0;
-    for (int s = 0; s < g.splits; ++s) t += g.part[s * slab + at + j];
-    float v = (float)t * (x * g.ws[col + j]);
-    if (g.bias) v += bf16_f32(g.bias[col + j]);
-    g.y[at + j] = f32_bf16(v);
+    for (int s = 0; s < splits; ++s) t += part[s * slab + at + j];
+    float v = (float)t * (x * ws[col + j]);
+    if (bias) v += bf16_f32(bias[col + j]);
+    y[at + j] = f32_bf16(v);
   }
 }
 
@@ -373,41 +391,77 @@ struct Plan {
   int splits;
 };
 
-#ifndef INT8_PLAN
+// Tile edge and split count by a time estimate in microseconds, fitted to 21
+// shapes from 48 x 8000 x 8192 to 2000 x 256 x 25600 measured with every choice
+// (the choices' times are 0.7% above the best ones' on average): a step of 128 of
+// K on a compute unit, a unit's start and epilogue, and the join of splits. Units
+// of 64 run two to a compute unit. 512 x 5120 x 5120 takes 25.3 us in tiles of
+// 128, 31.5 of 64 and 65.5 of 256; 333 x 4300 x 1168 11.4, 9.2 and 25.8; 8192 x
+// 8192 x 8192 623, 907 and 486; 64 x 1000 x 25600 57.6 in tiles of 64 and 13.4
+// with eight splits.
 Plan plan_int8(int64_t m, int64_t n, int64_t k) {
-  const int64_t t256 = ((m + 255) / 256) * ((n + 255) / 256), t128 = ((m + 127) / 128) * ((n + 127) / 128);
-  return Plan{t256 >= 192 ? 0 : t128 >= 192 ? 1 : 2, 1};
+  constexpr int kEdge[3] = {256, 128, 64};
+  constexpr double kStepUs[3] = {1.84, 0.61, 0.33}, kUnitUs[3] = {7.0, 1.6, 1.1};
+  constexpr double kJoinUs = 2.2, kJoinElemUs = 2.1e-6;
+  const int64_t steps = (k + 127) / 128;
+  Plan best{0, 1};
+  double least = 1e300;
+  for (int t = 0; t < 3; ++t) {
+    const int64_t tiles = ((m + kEdge[t] - 1) / kEdge[t]) * ((n + kEdge[t] - 1) / kEdge[t]);
+    for (const int splits : {1, 2, 3, 4, 6, 8}) {
+      const int64_t each = (steps + splits - 1) / splits;
+      if (splits > 1 && each < 4) break;
+      const int64_t units = tiles * splits;
+      double us;
+      if (t == 2) {
+        const int64_t rest = units % 512;
+        us = (double)(2 * (units / 512) + (rest == 0 ? 0 : rest <= 256 ? 1 : 2)) * each * kStepUs[t] +
+             (double)((units + 511) / 512) * kUnitUs[t];
+      } else {
+        us = (double)((units + 255) / 256) * (each * kStepUs[t] + kUnitUs[t]);
+      }
+      if (splits > 1) us += kJoinUs + kJoinElemUs * splits * (double)m * (double)n;
+      if (us < least) {
+        least = us;
+        best = Plan{t, splits};
+      }
+    }
+  }
+  return best;
 }
-#else
-Plan plan_int8(int64_t m, int64_t n, int64_t k) { return Plan{atoi(getenv("I8_TILE")), atoi(getenv("I8_SPLITS"))}; }
-#endif
 
-template <int WM, int WN, int BK, int S>
+template <int WM, int WN, int S>
 hipError_t launch_tiles(GemmArgs g, hipStream_t stream) {
-  constexpr int tm = Tile<WM, WN, BK, S>::kTM, tn = Tile<WM, WN, BK, S>::kTN;
-  g.steps = (g.K + BK - 1) / BK;
+  constexpr int tm = Tile<WM, WN, S>::kTM, tn = Tile<WM, WN, S>::kTN;
+  g.steps = (g.K + kBK - 1) / kBK;
   g.steps_per_unit = (g.steps + g.splits - 1) / g.splits;
   g.splits = (g.steps + g.steps_per_unit - 1) / g.steps_per_unit;
   g.tiles_m = (g.M + tm - 1) / tm;
   g.tiles_n = (g.N + tn - 1) / tn;
   const int64_t units = (int64_t)g.tiles_m * g.tiles_n * g.splits;
-  const int64_t most = (int64_t)device_cus() * (160 * 1024 / (S * Tile<WM, WN, BK, S>::kStage + (2 * tn + tm) * 4));
+  const int64_t most = (int64_t)device_cus() * (160 * 1024 / (S * Tile<WM, WN, S>::kStage + (2 * tn + tm) * 4));
   const dim3 grid((uint32_t)(units < most ? units : most));
   if (g.splits == 1)
-    hipLaunchKernelGGL((gemm_int8_kernel<WM, WN, BK, S, false>), grid, dim3(kThreads), 0, stream, g);
+    hipLaunchKernelGGL((gemm_int8_kernel<WM, WN, S, false>), grid, dim3(kThreads), 0, stream, g);
   else
-    hipLaunchKernelGGL((gemm_int8_kernel<WM, WN, BK, S, true>), grid, dim3(kThreads), 0, stream, g);
+    hipLaunchKernelGGL((gemm_int8_kernel<WM, WN, S, true>), grid, dim3(kThreads), 0, stream, g);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || g.splits == 1) return e;
-  const int64_t threads = (int64_t)g.M * ((g.N + 3) / 4);
-  hipLaunchKernelGGL(join_int8_kernel, dim3((uint32_t)((threads + 255) / 256)), dim3(256), 0, stream, g);
-  return hipGetLastError();
+  return launch_int8_join(g.part, g.xs, g.ws, g.bias, g.y, g.splits, g.M, g.N, stream);
 }
 
 }  // namespace
 
+hipError_t launch_int8_join(const int32_t* part, const float* xs, const float* ws, const uint16_t* bias, uint16_t* y,
+                            int splits, int64_t m, int64_t n, hipStream_t stream) {
+  const int64_t threads = m * ((n + 3) / 4);
+  hipLaunchKernelGGL(join_int8_kernel, dim3((uint32_t)((threads + 255) / 256)), dim3(256), 0, stream, part, xs, ws,
+                     bias, y, splits, (int)m, (int)n);
+  return hipGetLastError();
+}
+
 size_t int8_gemm_bytes(int64_t m, int64_t n, int64_t k) {
-  if (m <= kInt8SkinnyRows) return 0;
+  if (m <= kInt8SkinnyRows) return int8_skinny_bytes(m, n, k);
   const Plan p = plan_int8(m, n, k);
   return p.splits <= 1 ? 0 : round_up((size_t)p.splits * partial_slab(m, n) * sizeof(int32_t), kWorkspaceAlign);
 }
@@ -415,23 +469,14 @@ size_t int8_gemm_bytes(int64_t m, int64_t n, int64_t k) {
 hipError_t launch_int8_gemm(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws,
                             const uint16_t* bias, uint16_t* y, int64_t m, int64_t n, int64_t k, void* workspace,
                             hipStream_t stream) {
-  if (m <= kInt8SkinnyRows) return launch_int8_skinny(xq, xs, wq, ws, bias, y, m, n, k, stream);
+  if (m <= kInt8SkinnyRows) return launch_int8_skinny(xq, xs, wq, ws, bias, y, m, n, k, workspace, stream);
   const Plan p = plan_int8(m, n, k);
   const GemmArgs g{xq, xs, wq, ws, bias, y, static_cast<int32_t*>(workspace), (int)m, (int)n, (int)k, 0, 0, p.splits,
                    0, 0};
   switch (p.tile) {
-    case 0: return launch_tiles<4, 4, 128, 2>(g, stream);
-    case 1: return launch_tiles<2, 2, 128, 4>(g, stream);
-#ifdef INT8_PLAN
-    case 3: return launch_tiles<4, 4, 64, 4>(g, stream);
-    case 4: return launch_tiles<2, 4, 128, 3>(g, stream);
-    case 5: return launch_tiles<2, 4, 64, 6>(g, stream);
-    case 6: return launch_tiles<2, 2, 128, 2>(g, stream);
-    case 7: return launch_tiles<1, 2, 128, 4>(g, stream);
-    case 8: return launch_tiles<1, 1, 128, 8>(g, stream);
-    case 9: return launch_tiles<4, 2, 128, 3>(g, stream);
-#endif
-    default: return launch_tiles<1, 1, 128, 4>(g, stream);
+    case 0: return launch_tiles<4, 4, 2>(g, stream);
+    case 1: return launch_tiles<2, 2, 4>(g, stream);
+    default: return launch_tiles<1, 1, 4>(g, stream);
   }
 }
 

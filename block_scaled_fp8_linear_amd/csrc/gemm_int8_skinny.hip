@@ -30,6 +30,7 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 constexpr int kKW = 256;                  // K of a super-step
 constexpr int kSlabLoads = kKW / 64;      // loads of a 16-row slab of it
 constexpr int kSlab = 16 * kKW;
+constexpr int kSlots = 2;                 // of a wave: one super-step on its way behind the one computed
 constexpr unsigned kXcds = 8;
 constexpr uint32_t kOob = 0x80000000u;
 constexpr int kNonTemporal = 2;           // the weight is read once
@@ -52,21 +53,21 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, ui
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, 0x00020000);
 }
 
-// The row that a workgroup quantizes for itself: 8 chunks of 8 a thread at most,
-// which stay in registers between the maximum and the codes. In LDS the row is
-// whole super-steps long, zero behind K; 16 more zeros stand for the operand's
-// rows that are not there.
-constexpr int kFusedChunks = 8;
-constexpr int kFusedElems = kFusedChunks * 256 * 8, kFusedCodes = kFusedElems + 16;
+// The row that a workgroup quantizes for itself stays in registers between the
+// maximum and the codes. In LDS it is whole super-steps long, zero behind K; 16
+// more zeros stand for the operand's rows that are not there.
+constexpr int kFusedElems = 16384, kFusedCodes = kFusedElems + 16;
 
-template <int MT, int NT, int WAVES, int D, bool FUSED>
+template <int MT, int NT, int WAVES, bool FUSED>
 __global__ __launch_bounds__(WAVES * 64)
 void gemm_int8_skinny_kernel(SkinnyArgs a) {
   constexpr int kSlot = (NT + (FUSED ? 0 : MT)) * kSlab;
   constexpr int kLoads = kSlot / 1024;
-  constexpr int kRing = WAVES * D * kSlot;
-  static_assert((D - 1) * kLoads <= 63, "outstanding loads fit the counter");
-  static_assert(!FUSED || (MT == 1 && WAVES == 4), "one row, 256 threads");
+  constexpr int kRing = WAVES * kSlots * kSlot;
+  static_assert((kSlots - 1) * kLoads <= 63, "outstanding loads fit the counter");
+  static_assert(kRing <= 160 * 1024, "the slots fit the LDS");
+  static_assert(!FUSED || MT == 1, "one row");
+  constexpr int kThreads = WAVES * 64, kChunks = kFusedElems / (kThreads * 8);
   // one array: with several the compiler waits for the loads into LDS at each read
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing + (FUSED ? kFusedCodes + 128 : 0)];
   uint8_t* const codes = &lds[kRing];
@@ -78,7 +79,7 @@ void gemm_int8_skinny_kernel(SkinnyArgs a) {
   const int n0 = blockIdx.x * 16 * NT;
   const int nss = (K + kKW - 1) / kKW;
   const int ss0 = blockIdx.y * a.ss_per_split, ss1 = min(ss0 + a.ss_per_split, nss);
-  uint8_t* const ring = &lds[wave * D * kSlot];
+  uint8_t* const ring = &lds[wave * kSlots * kSlot];
 
   const __amdgpu_buffer_rsrc_t wrs = make_rsrc(a.wq + (size_t)n0 * K, (uint32_t)(min(N - n0, 16 * NT) * K));
   const __amdgpu_buffer_rsrc_t xrs = make_rsrc(a.x, (uint32_t)(FUSED ? 0 : M * K));
@@ -160,17 +161,17 @@ void gemm_int8_skinny_kernel(SkinnyArgs a) {
   if constexpr (FUSED) {
     // x ahead of the codes, which come from further away: loads return in order
     const uint16_t* const x = static_cast<const uint16_t*>(a.x);
-    u32x4 raw[kFusedChunks];
+    u32x4 raw[kChunks];
 #pragma unroll
-    for (int i = 0; i < kFusedChunks; ++i) {
-      const int c = (tid + 256 * i) * 8;
+    for (int i = 0; i < kChunks; ++i) {
+      const int c = (tid + kThreads * i) * 8;
       raw[i] = c < K ? *reinterpret_cast<const u32x4*>(x + c) : u32x4{0, 0, 0, 0};
     }
 #pragma unroll
-    for (int p = 0; p < D; ++p) issue(ss_of(wave + p * WAVES), p);
+    for (int p = 0; p < kSlots; ++p) issue(ss_of(wave + p * WAVES), p);
     uint32_t top = 0;                       // of magnitudes, which order like integers
 #pragma unroll
-    for (int i = 0; i < kFusedChunks; ++i)
+    for (int i = 0; i < kChunks; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) top = max(top, max((raw[i][j] << 16) & 0x7FFFFFFFu, raw[i][j] & 0x7FFF0000u));
     float amax = __uint_as_float(top);
@@ -184,9 +185,9 @@ void gemm_int8_skinny_kernel(SkinnyArgs a) {
     const RowScale rs = int8_scale(amax);
     if (tid == 0) scales[0] = rs.s;
 #pragma unroll
-    for (int i = 0; i < kFusedChunks; ++i) {
-      if (2048 * i >= xend) break;
-      const int c = (tid + 256 * i) * 8;    // zeros behind K, to the end of the last super-step
+    for (int i = 0; i < kChunks; ++i) {
+      if (8 * kThreads * i >= xend) break;
+      const int c = (tid + kThreads * i) * 8;    // zeros behind K, to the end of the last super-step
       float v[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -200,24 +201,24 @@ void gemm_int8_skinny_kernel(SkinnyArgs a) {
     lds_barrier();
   } else {
 #pragma unroll
-    for (int p = 0; p < D; ++p) issue(ss_of(wave + p * WAVES), p);
+    for (int p = 0; p < kSlots; ++p) issue(ss_of(wave + p * WAVES), p);
   }
-  for (int i = 0; i < iters; i += D) {
+  for (int i = 0; i < iters; i += kSlots) {
 #pragma unroll
-    for (int u = 0; u < D; ++u) {
+    for (int u = 0; u < kSlots; ++u) {
       if (i + u >= iters) break;
-      __builtin_amdgcn_s_waitcnt(vm_wait((D - 1) * kLoads));
+      __builtin_amdgcn_s_waitcnt(vm_wait((kSlots - 1) * kLoads));
       compute(ss_of(wave + (i + u) * WAVES), u, acc);
       // the slot's reads have returned: the loads write LDS on their own
       __builtin_amdgcn_s_waitcnt(kLgkmWait0);
-      issue(ss_of(wave + (i + u + D) * WAVES), u);
+      issue(ss_of(wave + (i + u + kSlots) * WAVES), u);
     }
   }
   __builtin_amdgcn_s_waitcnt(vm_wait(0));
   __syncthreads();
 
   i32x4* const red = reinterpret_cast<i32x4*>(lds);          // [WAVES][MT * NT][64]
-  static_assert(MT * NT * 1024 <= D * kSlot, "the waves' sums fit the ring");
+  static_assert(MT * NT * 1024 <= kSlots * kSlot, "the waves' sums fit the ring");
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -245,30 +246,76 @@ void gemm_int8_skinny_kernel(SkinnyArgs a) {
   }
 }
 
-template <int MT, int NT, int WAVES, int D, bool FUSED>
-hipError_t launch(SkinnyArgs a, int splits, hipStream_t stream) {
-  hipLaunchKernelGGL((gemm_int8_skinny_kernel<MT, NT, WAVES, D, FUSED>), dim3((uint32_t)((a.N + 16 * NT - 1) / (16 * NT)), splits),
-                     dim3(WAVES * 64), 0, stream, a);
+// Rows and waves of a workgroup, and K splits.
+struct Plan {
+  int nt, waves, splits, ss_per_split;
+};
+
+// 32 rows of the weight by four waves; 16 by eight (four where X has up to 32
+// rows, for the LDS) while that leaves no compute unit a second workgroup:
+// 1 x 4000 x 8192 takes 7.8 us so and 10.1 with 32 rows, 1 x 5120 x 5120 10.0 and
+// 7.7. K is split over workgroups where a wave would have eight super-steps or
+// more, down to three, as far as there are units left for it: the join costs 2.5
+// us, 16 x 300 x 25600 takes 17.0 us whole and 7.9 in eight, 16 x 1000 x 1024 4.1
+// and 6.0 in four. Not for one row of bf16, whose quantizer would need a launch
+// of its own: 1 x 300 x 16384 takes 9.2 us whole and 12.2 in eight.
+Plan plan_skinny8(int64_t m, int64_t n, int64_t k) {
+  const int nss = (int)((k + kKW - 1) / kKW);
+  Plan p{2, 4, 1, nss};
+  const int64_t groups = (n + 15) / 16;
+  if (groups > 256) return p;
+  p.nt = 1;
+  p.waves = m > 16 ? 4 : 8;
+  if (nss < 8 * p.waves || (m == 1 && k <= kFusedElems)) return p;
+  int splits = 1;
+  while (groups * splits * 2 <= 256 && nss >= 3 * p.waves * splits) splits *= 2;
+  p.ss_per_split = (nss + splits - 1) / splits;
+  p.splits = (nss + p.ss_per_split - 1) / p.ss_per_split;
+  return p;
+}
+
+template <int MT, int NT, int WAVES, bool FUSED>
+hipError_t launch(const SkinnyArgs& a, const Plan& p, hipStream_t stream) {
+  hipLaunchKernelGGL((gemm_int8_skinny_kernel<MT, NT, WAVES, FUSED>),
+                     dim3((uint32_t)((a.N + 16 * NT - 1) / (16 * NT)), (uint32_t)p.splits), dim3(WAVES * 64), 0, stream,
+                     a);
   return hipGetLastError();
+}
+
+SkinnyArgs args_of(const void* x, const float* xs, const int8_t* wq, const float* ws, const uint16_t* bias,
+                   uint16_t* y, int64_t m, int64_t n, int64_t k, void* workspace, const Plan& p) {
+  return SkinnyArgs{x, xs, wq, ws, bias, y, static_cast<int32_t*>(workspace), (int)m, (int)n, (int)k, p.ss_per_split};
 }
 
 }  // namespace
 
-bool int8_skinny_quantizes(int64_t m, int64_t n, int64_t k) {
-  (void)n;
+size_t int8_skinny_bytes(int64_t m, int64_t n, int64_t k) {
+  const Plan p = plan_skinny8(m, n, k);
+  return p.splits > 1 ? round_up((size_t)p.splits * partial_slab(m, n) * sizeof(int32_t), kWorkspaceAlign) : 0;
+}
+
+// One row of up to 16384, which the threads' registers hold.
+bool int8_skinny_quantizes(int64_t m, int64_t k) {
   return m == 1 && k <= kFusedElems;
 }
 
 hipError_t launch_int8_skinny(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws,
-                              const uint16_t* bias, uint16_t* y, int64_t m, int64_t n, int64_t k, hipStream_t stream) {
-  const SkinnyArgs a{xq, xs, wq, ws, bias, y, nullptr, (int)m, (int)n, (int)k, (int)((k + kKW - 1) / kKW)};
-  return m <= 16 ? launch<1, 2, 4, 2, false>(a, 1, stream) : launch<2, 2, 4, 2, false>(a, 1, stream);
+                              const uint16_t* bias, uint16_t* y, int64_t m, int64_t n, int64_t k, void* workspace,
+                              hipStream_t stream) {
+  const Plan p = plan_skinny8(m, n, k);
+  const SkinnyArgs a = args_of(xq, xs, wq, ws, bias, y, m, n, k, workspace, p);
+  const hipError_t e = m > 16         ? p.nt == 2 ? launch<2, 2, 4, false>(a, p, stream) : launch<2, 1, 4, false>(a, p, stream)
+                       : p.nt == 2    ? launch<1, 2, 4, false>(a, p, stream)
+                                      : launch<1, 1, 8, false>(a, p, stream);
+  if (e != hipSuccess || p.splits == 1) return e;
+  return launch_int8_join(a.part, xs, ws, bias, y, p.splits, m, n, stream);
 }
 
 hipError_t launch_int8_skinny_bf16(const uint16_t* x, const int8_t* wq, const float* ws, const uint16_t* bias,
-                                   uint16_t* y, int64_t m, int64_t n, int64_t k, hipStream_t stream) {
-  const SkinnyArgs a{x, nullptr, wq, ws, bias, y, nullptr, (int)m, (int)n, (int)k, (int)((k + kKW - 1) / kKW)};
-  return launch<1, 2, 4, 4, true>(a, 1, stream);
+                                   uint16_t* y, int64_t n, int64_t k, hipStream_t stream) {
+  const Plan p = plan_skinny8(1, n, k);
+  const SkinnyArgs a = args_of(x, nullptr, wq, ws, bias, y, 1, n, k, nullptr, p);
+  return p.nt == 2 ? launch<1, 2, 4, true>(a, p, stream) : launch<1, 1, 8, true>(a, p, stream);
 }
 
 }  // namespace fp8bl

@@ -1,4 +1,4 @@
-// Quantization of one row to 8-bit integers by a workgroup:
+// Quantization of a row to 8-bit integers:
 //   S = fl32(max |x| / 127), 1 where that is 0;
 //   code = the integer nearest to fl32(x / S), ties to even, within +-127.
 #pragma once
@@ -63,35 +63,6 @@ __device__ __forceinline__ RowScale int8_scale(float amax) {
   float s = __fdiv_rn(amax, 127.0f);
   if (s == 0.0f) s = 1.0f;
   return RowScale{s, __fdiv_rn(1.0f, s), s < 0x1p-100f};
-}
-
-// One row by a workgroup of THREADS: the maximum in a first pass, the codes in a
-// second, which finds the row in the cache. Returns the scale, in every thread.
-// `wave_max` holds one float a wave.
-template <int THREADS, typename T>
-__device__ __forceinline__ float int8_quantize_row(const T* __restrict__ x, int8_t* q, int K, float* wave_max) {
-  float amax = 0.0f;
-  for (int c = threadIdx.x * 8; c < K; c += THREADS * 8) {
-    float v[8];
-    load8(x + c, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-  }
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 64));
-  __syncthreads();           // the last row's maxima have been read
-  if ((threadIdx.x & 63) == 0) wave_max[threadIdx.x >> 6] = amax;
-  __syncthreads();
-  amax = wave_max[0];
-#pragma unroll
-  for (int w = 1; w < THREADS / 64; ++w) amax = fmaxf(amax, wave_max[w]);
-  const RowScale r = int8_scale(amax);
-  for (int c = threadIdx.x * 8; c < K; c += THREADS * 8) {
-    float v[8];
-    load8(x + c, v);
-    *reinterpret_cast<u32x2*>(q + c) = codes8(v, r);
-  }
-  return r.s;
 }
 
 }  // namespace
