@@ -19,7 +19,7 @@ struct LoadArgs {
 template <int L>
 __global__ __launch_bounds__(kQkvThreads)
 void load_kernel(LoadArgs g) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = 8 * (lane % L), heads = g.out[0].heads;
   for (int64_t token = (int64_t)blockIdx.x * kQkvWaves + wave; token < g.tokens;
        token += (int64_t)gridDim.x * kQkvWaves) {

@@ -26,6 +26,25 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(top(c), top(d), lo, true);
 }
 
+// fl32(x / s) for the codes. With y = fl32(1 / s), q0 = fl32(x y) and the residual
+// r = x - q0 s (exact), fma(r, y, q0) is the quotient but for the last bit's
+// rounding where it lies within 2^-23 of a bit's half; subnormal scales and their
+// like, whose residuals are not exact, take the IEEE division.
+__device__ __forceinline__ void quotients(float (&x)[8], float s) {
+  if (s >= 0x1p-64f) {
+    const float y = __fdiv_rn(1.0f, s);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float q0 = __fmul_rn(x[e], y);
+      const float r = __builtin_fmaf(-q0, s, x[e]);
+      x[e] = __builtin_copysignf(__builtin_fmaf(r, y, q0), x[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = __fdiv_rn(x[e], s);
+  }
+}
+
 struct RopeArgs {
   HeadView q, k, v, qo, ko;
   TurnArgs t;
@@ -60,19 +79,30 @@ __device__ __forceinline__ void rope_heads(const HeadView& in, const HeadView& o
   const uint16_t* const src = in.p + token * in.ts + col;
   uint16_t* const dst = out.p + token * out.ts + col;
   const float inv_dim = 1.0f / (float)dim;
-  for (int h = first + lane / L; h - lane / L < last; h += 64 / L) {
-    const bool live = mine && h < last;
-    const u32x4 raw = live ? *reinterpret_cast<const u32x4*>(src + h * in.hs) : u32x4{0, 0, 0, 0};
-    float x[8], o[8];
-    unpack8(raw, x);
-    unpack8(other_members<INTER>(raw, ch.partner), o);
-    float sq = 0.0f;
+  // kAhead steps' loads on their way at a time
+  constexpr int kAhead = 4, G = 64 / L;
+  for (int h0 = first; h0 < last; h0 += kAhead * G) {
+    u32x4 raw[kAhead];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sq = __builtin_fmaf(x[i], x[i], sq);
-    const float r = rsqrtf(head_sum<L>(sq) * inv_dim + eps);
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = h0 + i * G + lane / L;
+      raw[i] = mine && h < last ? *reinterpret_cast<const u32x4*>(src + h * in.hs) : u32x4{0, 0, 0, 0};
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = r * __builtin_fmaf(x[i], a[i], o[i] * b[i]);
-    if (live) *reinterpret_cast<u32x4*>(dst + h * out.hs) = pack8(x);
+    for (int i = 0; i < kAhead; ++i) {
+      if (h0 + i * G >= last) break;
+      const int h = h0 + i * G + lane / L;
+      float x[8], o[8];
+      unpack8(raw[i], x);
+      unpack8(other_members<INTER>(raw[i], ch.partner), o);
+      float sq = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sq = __builtin_fmaf(x[e], x[e], sq);
+      const float r = rsqrtf(head_sum<L>(sq) * inv_dim + eps);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = r * __builtin_fmaf(x[e], a[e], o[e] * b[e]);
+      if (mine && h < last) *reinterpret_cast<u32x4*>(dst + h * out.hs) = pack8(x);
+    }
   }
 }
 
@@ -100,8 +130,8 @@ __device__ __forceinline__ void rope_unit(const RopeArgs& g, int k_heads, int un
 // for few tokens.)
 template <int L, bool INTER>
 __device__ __forceinline__ void rope_waves(const RopeArgs& g, int k_heads, int block, int blocks, float2* table) {
-  const int units = g.t.tokens * g.parts;
-  for (int64_t u = (int64_t)block * kQkvWaves + (threadIdx.x >> 6); u < units; u += (int64_t)blocks * kQkvWaves)
+  const int units = g.t.tokens * g.parts, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int64_t u = (int64_t)block * kQkvWaves + wave; u < units; u += (int64_t)blocks * kQkvWaves)
     rope_unit<L, INTER>(g, k_heads, (int)u, threadIdx.x & 63, table);
 }
 
@@ -114,88 +144,147 @@ void rope_kernel(RopeArgs g) {
 
 constexpr int kMaxRun = 16;
 
-// Bit r: a token behind i0 + r has its slot.
-template <int R>
-__device__ __forceinline__ uint32_t later_ones(const int32_t* slots, int i0, int tokens, const int* run_slots) {
-  int mine[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) mine[r] = run_slots[r];
-  uint32_t found = 0;
-  for (int j = i0 + 1 + (int)threadIdx.x; j < tokens; j += kQkvThreads) {
-    const int v = slots[j];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (v == mine[r] && j > i0 + r) found |= 1u << r;
+// Bit r, in every lane: one of the slots that this wave looks at, behind token
+// i0 + r, is that token's. The workgroup's threads look at four slots each a
+// load, four loads on their way at a time; slots outside the run's own range, as
+// nearly all are, need no more than that comparison. Lane r of a wave holds the
+// slot of token i0 + r.
+__device__ __forceinline__ uint32_t later_ones(const int32_t* __restrict__ slots, int i0, int run, int run_slots,
+                                               int tokens) {
+  int lo = 0x7FFFFFFF, hi = -1;
+  for (int r = 0; r < run; ++r) {
+    const int s = __builtin_amdgcn_readlane(run_slots, r);
+    lo = s >= 0 ? min(lo, s) : lo;
+    hi = max(hi, s);
   }
-  return found;
+  if (hi < 0) return 0;                      // padding alone
+  const uint32_t span = (uint32_t)(hi - lo);
+  bool again = false;                        // in the run itself: lane r looks at those behind its own
+  for (int r = 1; r < run; ++r)
+    again |= run_slots == __builtin_amdgcn_readlane(run_slots, r) && (int)(threadIdx.x & 63) < r;
+  uint32_t found = 0;
+  constexpr int kThreads = kQkvThreads, kLoads = 4, kRound = kLoads * 4 * kThreads;
+  for (int j0 = i0 + run; j0 < tokens; j0 += kRound) {
+    int v[kLoads][4];
+    const int first = j0 + 4 * (int)threadIdx.x;
+#pragma unroll
+    for (int f = 0; f < kLoads; ++f) {
+      const int j = first + f * 4 * kThreads;
+      if (j + 4 <= tokens)
+        __builtin_memcpy(v[f], slots + j, 16);
+      else
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[f][e] = j + e < tokens ? slots[j + e] : -1;
+    }
+    bool near = false;
+#pragma unroll
+    for (int f = 0; f < kLoads; ++f)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) near |= (uint32_t)v[f][e] - (uint32_t)lo <= span;
+    if (near)
+      for (int r = 0; r < run; ++r) {
+        const int s = __builtin_amdgcn_readlane(run_slots, r);
+#pragma unroll
+        for (int f = 0; f < kLoads; ++f)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (s >= 0 && v[f][e] == s) found |= 1u << r;
+      }
+  }
+  if (__any(found != 0)) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) found |= __shfl_xor(found, off, 64);
+  }
+  return found | (uint32_t)__ballot(again);
 }
 
 // The run's keys (normed and turned where FUSED) and values into the cache.
 template <int L, bool INTER, bool FUSED>
 __device__ __forceinline__ void store_run(const RopeArgs& g, const CacheArgs& k, int run_index) {
-  __shared__ int run_slots[kMaxRun];
-  __shared__ uint32_t dead;
+  __shared__ uint32_t found[kQkvWaves];
   __shared__ float2 tables[FUSED ? kMaxRun : 1][FUSED ? FP8BL_MAX_PAIRS : 1];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  constexpr int G = 64 / L, kBatch = 4;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i0 = run_index * k.run, run = min(k.run, g.t.tokens - i0);
-  if (tid < kMaxRun) run_slots[tid] = tid < run ? k.slots[i0 + tid] : -1;
-  if (tid == 0) dead = 0;
-  __syncthreads();
-  const uint32_t found = k.run == 1   ? later_ones<1>(k.slots, i0, g.t.tokens, run_slots)
-                         : k.run == 4 ? later_ones<4>(k.slots, i0, g.t.tokens, run_slots)
-                                      : later_ones<kMaxRun>(k.slots, i0, g.t.tokens, run_slots);
-  if (found) atomicOr(&dead, found);
+  const int dim = g.t.dim, heads = g.k.heads;
+  const int col = 8 * (lane % L);
+  const bool mine = col < dim;
+  const int steps = (heads + G - 1) / G;     // of a token's keys, and of its values
+  const int items = run * 2 * steps;
+  struct Item {
+    int r, of_v, h;
+  };
+  auto item = [&](int u) { return Item{u / (2 * steps), u / steps % 2, u % steps * G + lane / L}; };
+  u32x4 raw[kBatch];
+  auto load = [&](int u0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int u = u0 + i * kQkvWaves;
+      const Item t = item(u < items ? u : 0);
+      const HeadView& in = t.of_v ? g.v : g.k;
+      raw[i] = mine && u < items && t.h < heads
+                   ? *reinterpret_cast<const u32x4*>(in.p + (i0 + t.r) * in.ts + t.h * in.hs + col)
+                   : u32x4{0, 0, 0, 0};
+    }
+  };
+  // lane r: the slot of token i0 + r
+  const int run_slots = lane < run ? k.slots[i0 + lane] : -1;
+  load(wave);              // on their way while the slots are compared
+
+  const uint32_t mine_found = later_ones(k.slots, i0, run, run_slots, g.t.tokens);
+  if (lane == 0) found[wave] = mine_found;
   if constexpr (FUSED)
     for (int p = tid; p < run * g.t.pairs; p += kQkvThreads)
       tables[p / g.t.pairs][p % g.t.pairs] = turn_of(g.t, g.t.axis[p % g.t.pairs], p % g.t.pairs, i0 + p / g.t.pairs);
   __syncthreads();
+  uint32_t dead = found[0];
+#pragma unroll
+  for (int w = 1; w < kQkvWaves; ++w) dead |= found[w];
+  dead = __builtin_amdgcn_readfirstlane(dead);
 
-  constexpr int G = 64 / L;
-  const int dim = g.t.dim, heads = g.k.heads;
-  const int col = 8 * (lane % L);
-  const bool mine = col < dim;
   const Chunk ch = chunk_of<INTER>(lane, lane % L, FUSED ? g.t.pairs : 8);
   float w[8], wo[8];
   if constexpr (FUSED) {
-    const u32x4 raw = mine ? *reinterpret_cast<const u32x4*>(g.t.wk + col) : u32x4{0, 0, 0, 0};
-    unpack8(raw, w);
-    unpack8(other_members<INTER>(raw, ch.partner), wo);
+    const u32x4 wr = mine ? *reinterpret_cast<const u32x4*>(g.t.wk + col) : u32x4{0, 0, 0, 0};
+    unpack8(wr, w);
+    unpack8(other_members<INTER>(wr, ch.partner), wo);
   }
   const float inv_dim = 1.0f / (float)dim;
-  const int steps = (heads + G - 1) / G;     // of a token's keys, and of its values
-  for (int u = wave; u < run * 2 * steps; u += kQkvWaves) {
-    const int r = u / (2 * steps), of_v = u / steps % 2, h = u % steps * G + lane / L;
-    const int slot = run_slots[r];
-    if (slot < 0 || slot >= k.rows || (dead >> r & 1)) continue;
-    const HeadView& in = of_v ? g.v : g.k;
-    const bool live = mine && h < heads;
-    const u32x4 raw = live ? *reinterpret_cast<const u32x4*>(in.p + (i0 + r) * in.ts + h * in.hs + col)
-                           : u32x4{0, 0, 0, 0};
-    float x[8];
-    unpack8(raw, x);
-    if (FUSED && !of_v) {
-      float o[8], c[8], s[8], sq = 0.0f;
-      unpack8(other_members<INTER>(raw, ch.partner), o);
-      turn_factors<INTER>(tables[r], ch, c, s);
+  for (int u0 = wave; u0 < items; u0 += kBatch * kQkvWaves) {
+    if (u0 != wave) load(u0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sq = __builtin_fmaf(x[i], x[i], sq);
-      const float n = rsqrtf(head_sum<L>(sq) * inv_dim + g.t.eps);
+    for (int i = 0; i < kBatch; ++i) {
+      const int u = u0 + i * kQkvWaves;
+      if (u >= items) break;
+      const Item t = item(u);
+      const int slot = __builtin_amdgcn_readlane(run_slots, t.r);
+      if (slot < 0 || slot >= k.rows || (dead >> t.r & 1)) continue;
+      float x[8];
+      unpack8(raw[i], x);
+      if (FUSED && !t.of_v) {
+        float o[8], c[8], s[8], sq = 0.0f;
+        unpack8(other_members<INTER>(raw[i], ch.partner), o);
+        turn_factors<INTER>(tables[t.r], ch, c, s);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = n * __builtin_fmaf(x[i], w[i] * c[i], o[i] * (wo[i] * s[i]));
-    }
-    float amax = 0.0f;
+        for (int e = 0; e < 8; ++e) sq = __builtin_fmaf(x[e], x[e], sq);
+        const float n = rsqrtf(head_sum<L>(sq) * inv_dim + g.t.eps);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
-    amax = head_max<L>(amax);
-    float sc = __fdiv_rn(amax, 448.0f);
-    if (sc == 0.0f) sc = 1.0f;
+        for (int e = 0; e < 8; ++e) x[e] = n * __builtin_fmaf(x[e], w[e] * c[e], o[e] * (wo[e] * s[e]));
+      }
+      float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], sc);
-    if (live) {
-      const size_t row = (size_t)slot * heads + h;
-      const u32x2 codes = {e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7])};
-      *reinterpret_cast<u32x2*>((of_v ? k.vc : k.kc) + row * dim + col) = codes;
-      if (col == 0) (of_v ? k.vs : k.ks)[row] = sc;
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+      amax = head_max<L>(amax);
+      float sc = __fdiv_rn(amax, 448.0f);
+      if (sc == 0.0f) sc = 1.0f;
+      quotients(x, sc);
+      if (mine && t.h < heads) {
+        const size_t row = (size_t)slot * heads + t.h;
+        const u32x2 codes = {e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7])};
+        *reinterpret_cast<u32x2*>((t.of_v ? k.vc : k.kc) + row * dim + col) = codes;
+        if (col == 0) (t.of_v ? k.vs : k.ks)[row] = sc;
+      }
     }
   }
 }
@@ -228,7 +317,11 @@ int parts_of(int64_t tokens, int64_t steps) {
 
 int steps_of(int64_t heads, int lanes) { return (int)((heads + 64 / lanes - 1) / (64 / lanes)); }
 
-int run_of(int64_t tokens) { return tokens <= 2048 ? 1 : tokens <= 8192 ? 4 : kMaxRun; }
+// Tokens to a workgroup that stores: one where tokens are few; four, whose keys
+// and values then take one batch of loads a wave at eight heads of 128 (8192
+// tokens 17.3 us, eight 22.8, one 26.5); sixteen where the comparison of the
+// slots, which grows with the square of the tokens over the run, would weigh.
+int run_of(int64_t tokens) { return tokens <= 1024 ? 1 : tokens <= 16384 ? 4 : kMaxRun; }
 
 RopeArgs rope_args(const fp8bl_qkv& a) {
   return RopeArgs{head_view(a.q, a.q_heads), head_view(a.k, a.k_heads), head_view(a.v, a.k_heads),
@@ -273,8 +366,8 @@ struct Store {
     g.t.tokens = (int)a.tokens;
     g.t.dim = (int)a.head_dim;
     const CacheArgs k = cache_args(a);
-    const uint32_t runs = (uint32_t)((a.tokens + k.run - 1) / k.run);
-    hipLaunchKernelGGL((store_kernel<L>), dim3(runs), dim3(kQkvThreads), 0, stream, g, k);
+    hipLaunchKernelGGL((store_kernel<L>), dim3((uint32_t)((a.tokens + k.run - 1) / k.run)), dim3(kQkvThreads), 0,
+                       stream, g, k);
     return hipGetLastError();
   }
 };

@@ -33,31 +33,43 @@ __device__ __forceinline__ void back_heads(const BackArgs& g, int which, const u
   const uint16_t* const yp = yv.p + token * yv.ts + col;
   uint16_t* const op = ov.p + token * ov.ts + col;
   const float inv_dim = 1.0f / (float)dim;
-  for (int h = first + lane / L; h - lane / L < last; h += 64 / L) {
-    const bool live = mine && h < last;
-    const u32x4 zero = {0, 0, 0, 0};
-    const u32x4 xr = live ? *reinterpret_cast<const u32x4*>(xp + h * xv.hs) : zero;
-    const u32x4 yr = live ? *reinterpret_cast<const u32x4*>(yp + h * yv.hs) : zero;
-    float x[8], y[8], o[8], sq = 0.0f, ux = 0.0f;
-    unpack8(xr, x);
-    unpack8(yr, y);
-    unpack8(other_members<INTER>(yr, ch.partner), o);
+  // kAhead steps' loads on their way at a time
+  constexpr int kAhead = 1, G = 64 / L;
+  for (int h0 = first; h0 < last; h0 += kAhead * G) {
+    u32x4 xr[kAhead], yr[kAhead];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      y[i] = __builtin_fmaf(y[i], c[i], -(o[i] * s[i]));        // dn
-      sq = __builtin_fmaf(x[i], x[i], sq);
-      ux = __builtin_fmaf(y[i] * w[i], x[i], ux);
+    for (int j = 0; j < kAhead; ++j) {
+      const int h = h0 + j * G + lane / L;
+      const bool live = mine && h < last;
+      xr[j] = live ? *reinterpret_cast<const u32x4*>(xp + h * xv.hs) : u32x4{0, 0, 0, 0};
+      yr[j] = live ? *reinterpret_cast<const u32x4*>(yp + h * yv.hs) : u32x4{0, 0, 0, 0};
     }
-    const float r = rsqrtf(head_sum<L>(sq) * inv_dim + g.t.eps);
-    const float along = head_sum<L>(ux) * inv_dim * r * r;
-    // a head that is not there leaves zeros in the sums, whatever r is
-    const float rl = live ? r : 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      dw[i] = __builtin_fmaf(y[i] * rl, x[i], dw[i]);
-      o[i] = r * __builtin_fmaf(-x[i], along, y[i] * w[i]);
+    for (int j = 0; j < kAhead; ++j) {
+      if (h0 + j * G >= last) break;
+      const int h = h0 + j * G + lane / L;
+      const bool live = mine && h < last;
+      float x[8], y[8], o[8], sq = 0.0f, ux = 0.0f;
+      unpack8(xr[j], x);
+      unpack8(yr[j], y);
+      unpack8(other_members<INTER>(yr[j], ch.partner), o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        y[i] = __builtin_fmaf(y[i], c[i], -(o[i] * s[i]));        // dn
+        sq = __builtin_fmaf(x[i], x[i], sq);
+        ux = __builtin_fmaf(y[i] * w[i], x[i], ux);
+      }
+      const float r = rsqrtf(head_sum<L>(sq) * inv_dim + g.t.eps);
+      const float along = head_sum<L>(ux) * inv_dim * r * r;
+      // a head that is not there leaves zeros in the sums, whatever r is
+      const float rl = live ? r : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        dw[i] = __builtin_fmaf(y[i] * rl, x[i], dw[i]);
+        o[i] = r * __builtin_fmaf(-x[i], along, y[i] * w[i]);
+      }
+      if (live) *reinterpret_cast<u32x4*>(op + h * ov.hs) = pack8(o);
     }
-    if (live) *reinterpret_cast<u32x4*>(op + h * ov.hs) = pack8(o);
   }
 }
 
@@ -66,7 +78,7 @@ __global__ __launch_bounds__(kQkvThreads)
 void back_kernel(BackArgs g) {
   __shared__ float2 tables[kQkvWaves][FP8BL_MAX_PAIRS];
   __shared__ float sums[kQkvWaves][2][8 * L];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Chunk ch = chunk_of<INTER>(lane, lane % L, g.t.pairs);
   float dwq[8] = {}, dwk[8] = {};
   constexpr int G = 64 / L;

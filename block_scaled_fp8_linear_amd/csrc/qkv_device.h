@@ -98,16 +98,21 @@ __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
   return u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
 }
 
-// cos and sin of pair p of a token. The angle position * inv_freq reaches
-// 2^31 radians: it is taken in fp64 as a number of turns, whose fraction
-// then fits fp32.
+// cos and sin of pair p of a token. The angle position * inv_freq reaches 2^31
+// radians: it is taken in fp64 as a number of turns. What is left of it behind
+// whole quarter turns, at most pi / 4, goes through the two power series to
+// a^11 and a^10 (off by 2e-10), so that both come out rounded once to fp32.
 __device__ __forceinline__ float2 turn_of(const TurnArgs& t, int axis, int p, int token) {
   const double turns = (double)t.positions[(size_t)axis * t.tokens + token] *
                        ((double)t.inv_freq[p] * 0.15915494309189533577);
-  const float f = (float)(turns - rint(turns));
-  float2 cs;
-  sincospif(2.0f * f, &cs.y, &cs.x);
-  return cs;
+  const double quarters = rint(4.0 * turns);
+  const double a = (turns - 0.25 * quarters) * 6.28318530717958647693, z = a * a;
+  const double s = a * fma(z, fma(z, fma(z, fma(z, fma(z, -1.0 / 39916800, 1.0 / 362880), -1.0 / 5040), 1.0 / 120),
+                               -1.0 / 6), 1.0);
+  const double c = fma(z, fma(z, fma(z, fma(z, fma(z, -1.0 / 3628800, 1.0 / 40320), -1.0 / 720), 1.0 / 24), -0.5), 1.0);
+  const int q = (int)(int64_t)quarters & 3;
+  const float fs = (float)(q & 1 ? c : s), fc = (float)(q & 1 ? s : c);
+  return float2{q == 1 || q == 2 ? -fc : fc, q >= 2 ? -fs : fs};
 }
 
 // Where the lane's chunk c of a head stands: in the first or second members of
