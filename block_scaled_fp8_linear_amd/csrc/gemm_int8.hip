@@ -69,7 +69,8 @@ struct Tile {
   static constexpr int kXLoads = kTM / 4 / kRows, kWLoads = kTN / 4 / kRows;    // for each wave and step
   static constexpr int kLoads = kXLoads + kWLoads;
   static_assert(S * kStage + (2 * kTN + kTM) * 4 <= 160 * 1024, "the stages and the epilogue's vectors fit the LDS");
-  static_assert((S - 1) * kLoads <= 63, "outstanding loads fit the counter");
+  static constexpr int kStores = 2 * WM * WN;                     // of a wave's sums as bf16 (the splits' own are twice as many)
+  static_assert((S - 2) * kLoads + kStores <= 63 && (S - 1) * kLoads <= 63, "outstanding loads fit the counter");
 };
 
 template <int WM, int WN, int S, bool SPLIT>
@@ -198,6 +199,7 @@ void gemm_int8_kernel(GemmArgs g) {
     for (int m = 0; m < WM; ++m) acc[n][m] = i32x16{};
 
   int stage = 0;
+  bool stored = true;                  // the last unit's tile was whole (before the first unit: nothing to wait for)
   for (int ci = 0; ci < my_units; ++ci) {
     const Unit CU = unit_of(ci);
     for (int kt = 0; kt < g.steps_per_unit; ++kt) {
@@ -220,8 +222,13 @@ void gemm_int8_kernel(GemmArgs g) {
           // this wave's reads of the stage have returned and its loads of the
           // next stage have landed; behind the barrier so have all waves'
           __builtin_amdgcn_s_waitcnt(kLgkmWait0);
-          __builtin_amdgcn_s_waitcnt(vm_wait((S - 2) * T::kLoads));
-          if (kt == 0 || last) __builtin_amdgcn_s_waitcnt(vm_wait(0));      // the last epilogue's stores among them
+          // (a whole tile's stores, one for each 16 bytes, are behind the loads
+          // waited for in the next unit's first step and may take until its second)
+          if (kt == 0 && stored)
+            __builtin_amdgcn_s_waitcnt(vm_wait((S - 2) * T::kLoads + T::kStores));
+          else
+            __builtin_amdgcn_s_waitcnt(vm_wait((S - 2) * T::kLoads));
+          if (last || (kt == 0 && !stored)) __builtin_amdgcn_s_waitcnt(vm_wait(0));
           if (!SPLIT && last) {
             asm volatile("" : "+v"(e_bias));     // not looked at before the wait above
             if (tid < kTN) ep_ws[tid] = __uint_as_float(e_ws), ep_bias[tid] = __uint_as_float(e_bias << 16);
@@ -263,6 +270,26 @@ void gemm_int8_kernel(GemmArgs g) {
     }
 
     // ---- Epilogue of unit ci.
+    // With 16 blocks the sums stay in accumulation registers and are read out one
+    // at a time: left to itself the compiler copies all of them at once and
+    // spills what the loop keeps (8192 x 12288 x 4096 392 us, 381 so). It knows
+    // nothing of the wait between the last products and these reads, so that is
+    // here, for every block.
+    constexpr bool kReadOut = WM * WN >= 16;
+    if constexpr (kReadOut) {
+#pragma unroll
+      for (int n = 0; n < WN; ++n)
+#pragma unroll
+        for (int m = 0; m < WM; ++m) asm volatile("s_nop 15\n\ts_nop 15" : "+a"(acc[n][m]));
+    }
+    auto sum = [&](int n, int m, int i) {
+      int v;
+      if constexpr (kReadOut)
+        asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(acc[n][m][i]));
+      else
+        v = acc[n][m][i];
+      return v;
+    };
     int le;
     asm volatile("" : "=v"(le) : "0"(lane));     // keeps the addresses below out of the loop's registers
     const int er = le & 31, eh = le >> 5;
@@ -279,7 +306,7 @@ void gemm_int8_kernel(GemmArgs g) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int col = CU.n0 + col0 + 32 * n + 8 * q + 4 * eh;
-            const i32x4 v = {acc[n][m][4 * q], acc[n][m][4 * q + 1], acc[n][m][4 * q + 2], acc[n][m][4 * q + 3]};
+            const i32x4 v = {sum(n, m, 4 * q), sum(n, m, 4 * q + 1), sum(n, m, 4 * q + 2), sum(n, m, 4 * q + 3)};
             int32_t* const to = p + ((size_t)CU.m0 + row) * N + col;
             if (row < rows && col + 4 <= N)
               __builtin_memcpy(to, &v, 16);
@@ -293,7 +320,6 @@ void gemm_int8_kernel(GemmArgs g) {
       for (int n = 0; n < WN; ++n)
 #pragma unroll
         for (int p = 0; p < 2; ++p) {            // column groups 2 p and 2 p + 1
-          __builtin_amdgcn_sched_barrier(0);     // a few sums at a time in registers
           float w[2][4], b[2][4];
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
@@ -305,6 +331,7 @@ void gemm_int8_kernel(GemmArgs g) {
           }
 #pragma unroll
           for (int m = 0; m < WM; ++m) {
+            __builtin_amdgcn_sched_barrier(0);   // a few sums at a time in registers
             const float x = ep_xs[row0 + 32 * m];
             uint32_t d[2][2];
 #pragma unroll
@@ -312,7 +339,7 @@ void gemm_int8_kernel(GemmArgs g) {
               float v[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                v[i] = (float)acc[n][m][4 * (2 * p + q) + i] * (x * w[q][i]);
+                v[i] = (float)sum(n, m, 4 * (2 * p + q) + i) * (x * w[q][i]);
                 if (g.bias) v[i] += b[q][i];
               }
               d[q][0] = pack_bf16x2(v[0], v[1]);
@@ -342,6 +369,7 @@ void gemm_int8_kernel(GemmArgs g) {
     for (int n = 0; n < WN; ++n)
 #pragma unroll
       for (int m = 0; m < WM; ++m) acc[n][m] = i32x16{};
+    stored = CU.m0 + kTM <= M && CU.n0 + kTN <= N;
     if constexpr (!SPLIT) wg_barrier();          // the vectors have been read
   }
   __builtin_amdgcn_s_waitcnt(vm_wait(0));        // loads behind the last step still target the LDS
@@ -401,7 +429,7 @@ struct Plan {
 // with eight splits.
 Plan plan_int8(int64_t m, int64_t n, int64_t k) {
   constexpr int kEdge[3] = {256, 128, 64};
-  constexpr double kStepUs[3] = {1.84, 0.61, 0.33}, kUnitUs[3] = {7.0, 1.6, 1.1};
+  constexpr double kStepUs[3] = {1.8, 0.61, 0.33}, kUnitUs[3] = {5.0, 2.2, 1.1};
   constexpr double kJoinUs = 2.2, kJoinElemUs = 2.1e-6;
   const int64_t steps = (k + 127) / 128;
   Plan best{0, 1};

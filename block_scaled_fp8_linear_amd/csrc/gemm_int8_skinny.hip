@@ -3,10 +3,10 @@
 // walked, split and joined does not change a bit of the result.
 //
 // A workgroup owns 16 NT weight rows and one K range (normally all of K), cut
-// into super-steps of 256 that go round-robin to its waves. Codes are loaded 4
-// rows x 256 bytes an instruction, straight into the wave's LDS slots (16-byte
-// chunks permuted by the row, so that the operands' reads, one chunk of 16
-// rows, lie in 16 different bank groups), and X likewise. A wave reads only
+// into super-steps of KW that go round-robin to its waves. Codes are loaded 4
+// rows x 256 bytes (8 x 128) an instruction, straight into the wave's LDS slots
+// (16-byte chunks permuted by the row, so that the operands' reads, one chunk of
+// 16 rows, lie in 16 different bank groups), and X likewise. A wave reads only
 // what it loaded: no barrier until the waves' sums meet.
 //
 // FUSED: one row of bf16: every workgroup quantizes it for itself, into LDS,
@@ -27,9 +27,6 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
-constexpr int kKW = 256;                  // K of a super-step
-constexpr int kSlabLoads = kKW / 64;      // loads of a 16-row slab of it
-constexpr int kSlab = 16 * kKW;
 constexpr int kSlots = 2;                 // of a wave: one super-step on its way behind the one computed
 constexpr unsigned kXcds = 8;
 constexpr uint32_t kOob = 0x80000000u;
@@ -46,7 +43,7 @@ struct SkinnyArgs {
   const uint16_t* bias;
   uint16_t* y;
   int32_t* part;
-  int M, N, K, ss_per_split;
+  int M, N, K, k_split;
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
@@ -58,9 +55,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, ui
 // more zeros stand for the operand's rows that are not there.
 constexpr int kFusedElems = 16384, kFusedCodes = kFusedElems + 16;
 
-template <int MT, int NT, int WAVES, bool FUSED>
+template <int MT, int NT, int WAVES, int KW, bool FUSED>
 __global__ __launch_bounds__(WAVES * 64)
 void gemm_int8_skinny_kernel(SkinnyArgs a) {
+  constexpr int kSlab = 16 * KW;                 // 16 rows of a super-step
+  constexpr int kSlabLoads = KW / 64;            // loads of it
+  constexpr int kSlabRows = 1024 / KW, kChunksRow = KW / 16;      // rows of a load, 16-byte chunks of a row
   constexpr int kSlot = (NT + (FUSED ? 0 : MT)) * kSlab;
   constexpr int kLoads = kSlot / 1024;
   constexpr int kRing = WAVES * kSlots * kSlot;
@@ -77,21 +77,22 @@ void gemm_int8_skinny_kernel(SkinnyArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int M = a.M, N = a.N, K = a.K;
   const int n0 = blockIdx.x * 16 * NT;
-  const int nss = (K + kKW - 1) / kKW;
-  const int ss0 = blockIdx.y * a.ss_per_split, ss1 = min(ss0 + a.ss_per_split, nss);
+  const int nss = (K + KW - 1) / KW;
+  const int each = a.k_split / KW, ss0 = blockIdx.y * each, ss1 = min(ss0 + each, nss);
   uint8_t* const ring = &lds[wave * kSlots * kSlot];
 
   const __amdgpu_buffer_rsrc_t wrs = make_rsrc(a.wq + (size_t)n0 * K, (uint32_t)(min(N - n0, 16 * NT) * K));
   const __amdgpu_buffer_rsrc_t xrs = make_rsrc(a.x, (uint32_t)(FUSED ? 0 : M * K));
 
-  // Load r of a slab brings rows 4 r .. 4 r + 3: lane l lands at byte 16 l of
-  // its 1 KB and fetches the chunk (l & 15) ^ row.
-  uint32_t off[kSlabLoads];
+  // Load r of a slab brings kSlabRows rows from kSlabRows r on: lane l lands at
+  // byte 16 l of its 1 KB, at chunk l % kChunksRow of its row, and fetches that
+  // chunk ^ key(row): 16 rows of one chunk lie in 16 different chunks of 256 bytes.
+  auto key = [](int row) { return KW == 256 ? row : (row >> 1) & 7; };
+  auto chunk = [&](int r) { return (lane % kChunksRow) ^ key(kSlabRows * r + lane / kChunksRow); };
+  uint32_t off[4];        // (the first kSlabLoads: a lambda that captures an array sized by a template
+                          // parameter leaves the host stub undefined)
 #pragma unroll
-  for (int r = 0; r < kSlabLoads; ++r) {
-    const int row = 4 * r + (lane >> 4);
-    off[r] = (uint32_t)(row * K + ((lane & 15) ^ row) * 16);
-  }
+  for (int r = 0; r < kSlabLoads; ++r) off[r] = (uint32_t)((kSlabRows * r + lane / kChunksRow) * K + chunk(r) * 16);
   const int count = ss1 - ss0;
   // each workgroup starts at a super-step of its own: many K offsets are read at
   // any time, not all rows at one
@@ -102,12 +103,12 @@ void gemm_int8_skinny_kernel(SkinnyArgs a) {
     return ss0 + (r >= count ? r - count : r);
   };
   auto issue = [&](int ss, int slot) {
-    const uint32_t kb = (uint32_t)(ss * kKW);
+    const uint32_t kb = (uint32_t)(ss * KW);
     const int klim = ss < ss1 ? K - (int)kb : 0;
     uint8_t* const base = ring + slot * kSlot;
 #pragma unroll
     for (int r = 0; r < kSlabLoads; ++r) {
-      const bool in = (((lane & 15) ^ (4 * r + (lane >> 4))) * 16) < klim;
+      const bool in = chunk(r) * 16 < klim;
       if constexpr (!FUSED)
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -121,7 +122,7 @@ void gemm_int8_skinny_kernel(SkinnyArgs a) {
     }
   };
   const int r16 = lane & 15, g = lane >> 4;
-  const int xend = nss * kKW;                               // FUSED: bytes of the row of codes
+  const int xend = nss * KW;                               // FUSED: bytes of the row of codes
   i32x4 acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -131,12 +132,12 @@ void gemm_int8_skinny_kernel(SkinnyArgs a) {
     const uint8_t* const base = ring + slot * kSlot;
 #pragma unroll
     for (int h = 0; h < kSlabLoads; ++h) {
-      const int c = g + 4 * h, at = r16 * kKW + ((c ^ r16) << 4);
+      const int c = g + 4 * h, at = r16 * KW + ((c ^ key(r16)) << 4);
       i32x4 xv[MT];
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         if constexpr (FUSED) {
-          xv[i] = *reinterpret_cast<const i32x4*>(codes + (r16 == 0 ? ss * kKW + 16 * c : xend));
+          xv[i] = *reinterpret_cast<const i32x4*>(codes + (r16 == 0 ? ss * KW + 16 * c : xend));
         } else {
           xv[i] = *reinterpret_cast<const i32x4*>(base + (NT + i) * kSlab + at);
         }
@@ -224,59 +225,63 @@ void gemm_int8_skinny_kernel(SkinnyArgs a) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) red[(wave * MT * NT + i * NT + j) * 64 + lane] = acc[i][j];
   __syncthreads();
-  if (wave >= MT * NT) return;
-  i32x4 t = red[wave * 64 + lane];
+  // each wave finishes every WAVES-th block of outputs
+  for (int b = wave; b < MT * NT; b += WAVES) {
+    i32x4 t = red[b * 64 + lane];
 #pragma unroll
-  for (int w = 1; w < WAVES; ++w) t += red[(w * MT * NT + wave) * 64 + lane];
-  const int col = n0 + (wave % NT) * 16 + r16;
-  if (col >= N) return;
-  const float w_scale = a.ws[col];
-  const float bias = a.bias ? bf16_f32(a.bias[col]) : 0.0f;
+    for (int w = 1; w < WAVES; ++w) t += red[(w * MT * NT + b) * 64 + lane];
+    const int col = n0 + (b % NT) * 16 + r16;
+    if (col >= N) continue;
+    const float w_scale = a.ws[col];
+    const float bias = a.bias ? bf16_f32(a.bias[col]) : 0.0f;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int row = (wave / NT) * 16 + 4 * g + r;
-    if (row >= M) continue;
-    if (gridDim.y > 1) {
-      a.part[(size_t)blockIdx.y * partial_slab(M, N) + (size_t)row * N + col] = t[r];
-      continue;
+    for (int r = 0; r < 4; ++r) {
+      const int row = (b / NT) * 16 + 4 * g + r;
+      if (row >= M) continue;
+      if (gridDim.y > 1) {
+        a.part[(size_t)blockIdx.y * partial_slab(M, N) + (size_t)row * N + col] = t[r];
+        continue;
+      }
+      float v = (float)t[r] * ((FUSED ? scales[0] : a.xs[row]) * w_scale);
+      if (a.bias) v += bias;
+      a.y[(size_t)row * N + col] = f32_bf16(v);
     }
-    float v = (float)t[r] * ((FUSED ? scales[0] : a.xs[row]) * w_scale);
-    if (a.bias) v += bias;
-    a.y[(size_t)row * N + col] = f32_bf16(v);
   }
 }
 
-// Rows and waves of a workgroup, and K splits.
+// How a workgroup is cut, by the row tiles of X (m > 16) and whether 16 weight
+// rows a workgroup still leave no compute unit a second one (few).
+//
+// With few columns (n <= 4096): 16 rows by eight waves (four for two row tiles of
+// X): 1 x 4000 x 8192 takes 7.4 us so, 9.9 in 32 rows by four waves; 1 x 1000 x
+// 8192 5.8 and 8.1. Otherwise several workgroups share a compute unit, for which
+// super-steps of 128 or few waves leave the LDS: 16 x 25600 x 5120 takes 26.5 us
+// in 32 rows, four waves and super-steps of 128, 33.0 with super-steps of 256 (one
+// workgroup a compute unit, 800 of them), 31.7 in 16 rows by eight waves; one row
+// in 16 rows by four waves 25600 x 5120 25.8, 8000 x 8192 12.0 (14.5 in 32 rows).
+//
+// K is split over workgroups from 16384 on (8192 with two row tiles), in pieces
+// of 2048 or more, as far as there are compute units for them: the join costs
+// 2.5 us, 16 x 300 x 25600 takes 17.5 us whole and 7.7 in eight, 16 x 2000 x 8192
+// 8.0 and 8.2 in two. Not for a row of bf16 that is quantized on the way: its
+// quantizer would need a launch of its own.
 struct Plan {
-  int nt, waves, splits, ss_per_split;
+  bool few;
+  int splits, k_split;
 };
-
-// 32 rows of the weight by four waves; 16 by eight (four where X has up to 32
-// rows, for the LDS) while that leaves no compute unit a second workgroup:
-// 1 x 4000 x 8192 takes 7.8 us so and 10.1 with 32 rows, 1 x 5120 x 5120 10.0 and
-// 7.7. K is split over workgroups where a wave would have eight super-steps or
-// more, down to three, as far as there are units left for it: the join costs 2.5
-// us, 16 x 300 x 25600 takes 17.0 us whole and 7.9 in eight, 16 x 1000 x 1024 4.1
-// and 6.0 in four. Not for one row of bf16, whose quantizer would need a launch
-// of its own: 1 x 300 x 16384 takes 9.2 us whole and 12.2 in eight.
 Plan plan_skinny8(int64_t m, int64_t n, int64_t k) {
-  const int nss = (int)((k + kKW - 1) / kKW);
-  Plan p{2, 4, 1, nss};
   const int64_t groups = (n + 15) / 16;
-  if (groups > 256) return p;
-  p.nt = 1;
-  p.waves = m > 16 ? 4 : 8;
-  if (nss < 8 * p.waves || (m == 1 && k <= kFusedElems)) return p;
-  int splits = 1;
-  while (groups * splits * 2 <= 256 && nss >= 3 * p.waves * splits) splits *= 2;
-  p.ss_per_split = (nss + splits - 1) / splits;
-  p.splits = (nss + p.ss_per_split - 1) / p.ss_per_split;
+  Plan p{groups <= 256, 1, 0};
+  if (k >= (m > 16 ? 8192 : 16384) && !int8_skinny_quantizes(m, k))
+    while (groups * p.splits * 2 <= 256 && k >= 4096 * (int64_t)p.splits) p.splits *= 2;
+  p.k_split = (int)((k + 256 * p.splits - 1) / (256 * p.splits)) * 256;      // whole super-steps of either size
+  p.splits = (int)((k + p.k_split - 1) / p.k_split);
   return p;
 }
 
-template <int MT, int NT, int WAVES, bool FUSED>
+template <int MT, int NT, int WAVES, int KW, bool FUSED>
 hipError_t launch(const SkinnyArgs& a, const Plan& p, hipStream_t stream) {
-  hipLaunchKernelGGL((gemm_int8_skinny_kernel<MT, NT, WAVES, FUSED>),
+  hipLaunchKernelGGL((gemm_int8_skinny_kernel<MT, NT, WAVES, KW, FUSED>),
                      dim3((uint32_t)((a.N + 16 * NT - 1) / (16 * NT)), (uint32_t)p.splits), dim3(WAVES * 64), 0, stream,
                      a);
   return hipGetLastError();
@@ -284,7 +289,7 @@ hipError_t launch(const SkinnyArgs& a, const Plan& p, hipStream_t stream) {
 
 SkinnyArgs args_of(const void* x, const float* xs, const int8_t* wq, const float* ws, const uint16_t* bias,
                    uint16_t* y, int64_t m, int64_t n, int64_t k, void* workspace, const Plan& p) {
-  return SkinnyArgs{x, xs, wq, ws, bias, y, static_cast<int32_t*>(workspace), (int)m, (int)n, (int)k, p.ss_per_split};
+  return SkinnyArgs{x, xs, wq, ws, bias, y, static_cast<int32_t*>(workspace), (int)m, (int)n, (int)k, p.k_split};
 }
 
 }  // namespace
@@ -304,9 +309,10 @@ hipError_t launch_int8_skinny(const int8_t* xq, const float* xs, const int8_t* w
                               hipStream_t stream) {
   const Plan p = plan_skinny8(m, n, k);
   const SkinnyArgs a = args_of(xq, xs, wq, ws, bias, y, m, n, k, workspace, p);
-  const hipError_t e = m > 16         ? p.nt == 2 ? launch<2, 2, 4, false>(a, p, stream) : launch<2, 1, 4, false>(a, p, stream)
-                       : p.nt == 2    ? launch<1, 2, 4, false>(a, p, stream)
-                                      : launch<1, 1, 8, false>(a, p, stream);
+  const hipError_t e = m > 16 ? p.few ? launch<2, 1, 4, 128, false>(a, p, stream) : launch<2, 2, 2, 256, false>(a, p, stream)
+                       : p.few ? launch<1, 1, 8, 128, false>(a, p, stream)
+                       : m > 1 ? launch<1, 2, 4, 128, false>(a, p, stream)
+                               : launch<1, 1, 4, 256, false>(a, p, stream);
   if (e != hipSuccess || p.splits == 1) return e;
   return launch_int8_join(a.part, xs, ws, bias, y, p.splits, m, n, stream);
 }
@@ -315,7 +321,7 @@ hipError_t launch_int8_skinny_bf16(const uint16_t* x, const int8_t* wq, const fl
                                    uint16_t* y, int64_t n, int64_t k, hipStream_t stream) {
   const Plan p = plan_skinny8(1, n, k);
   const SkinnyArgs a = args_of(x, nullptr, wq, ws, bias, y, 1, n, k, nullptr, p);
-  return p.nt == 2 ? launch<1, 2, 4, true>(a, p, stream) : launch<1, 1, 8, true>(a, p, stream);
+  return p.few ? launch<1, 1, 8, 128, true>(a, p, stream) : launch<1, 1, 4, 256, true>(a, p, stream);
 }
 
 }  // namespace fp8bl

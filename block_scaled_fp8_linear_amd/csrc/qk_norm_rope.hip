@@ -60,70 +60,94 @@ struct CacheArgs {
   int rows, run;    // cache rows; tokens to a workgroup
 };
 
-// The heads [first, last) in steps of 64 / L of one token.
-template <int L, bool INTER>
-__device__ __forceinline__ void rope_heads(const HeadView& in, const HeadView& out, const uint16_t* w, int dim,
-                                           float eps, int token, int first, int last, int lane, const Chunk& ch,
-                                           const float (&c)[8], const float (&s)[8]) {
+// The heads [first, last) of q or k of one token, in steps of 64 / L, kAhead
+// steps' loads on their way at a time.
+constexpr int kAhead = 2;
+
+template <int L>
+struct Heads {
+  const uint16_t* src;
+  uint16_t* dst;
+  const uint16_t* w;
+  int64_t in_hs, out_hs;
+  int first, last, sub;          // sub: the lane's head in a step
+  bool mine;                     // the lane has elements
+  u32x4 raw[kAhead];
+
+  __device__ __forceinline__ void load(int h0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int h = h0 + i * (64 / L) + sub;
+      raw[i] = mine && h < last ? *reinterpret_cast<const u32x4*>(src + h * in_hs) : u32x4{0, 0, 0, 0};
+    }
+  }
+};
+
+template <int L>
+__device__ __forceinline__ Heads<L> heads_of(const HeadView& in, const HeadView& out, const uint16_t* w, int dim,
+                                             int token, int first, int last, int lane) {
   const int col = 8 * (lane % L);
-  const bool mine = col < dim;
+  return Heads<L>{in.p + token * in.ts + col, out.p + token * out.ts + col, w + col, in.hs, out.hs, first, last,
+                  lane / L, col < dim, {}};
+}
+
+// The first loads are on their way already.
+template <int L, bool INTER>
+__device__ __forceinline__ void rope_heads(Heads<L>& g, float inv_dim, float eps, const Chunk& ch, const float (&c)[8],
+                                           const float (&s)[8]) {
   float a[8], b[8];
   {
-    const u32x4 raw = mine ? *reinterpret_cast<const u32x4*>(w + col) : u32x4{0, 0, 0, 0};
+    const u32x4 raw = g.mine ? *reinterpret_cast<const u32x4*>(g.w) : u32x4{0, 0, 0, 0};
     float own[8], other[8];
     unpack8(raw, own);
     unpack8(other_members<INTER>(raw, ch.partner), other);
 #pragma unroll
     for (int i = 0; i < 8; ++i) a[i] = own[i] * c[i], b[i] = other[i] * s[i];
   }
-  const uint16_t* const src = in.p + token * in.ts + col;
-  uint16_t* const dst = out.p + token * out.ts + col;
-  const float inv_dim = 1.0f / (float)dim;
-  // kAhead steps' loads on their way at a time
-  constexpr int kAhead = 4, G = 64 / L;
-  for (int h0 = first; h0 < last; h0 += kAhead * G) {
-    u32x4 raw[kAhead];
+  constexpr int G = 64 / L;
+  for (int h0 = g.first; h0 < g.last; h0 += kAhead * G) {
+    if (h0 != g.first) g.load(h0);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int h = h0 + i * G + lane / L;
-      raw[i] = mine && h < last ? *reinterpret_cast<const u32x4*>(src + h * in.hs) : u32x4{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (h0 + i * G >= last) break;
-      const int h = h0 + i * G + lane / L;
+      if (h0 + i * G >= g.last) break;
+      const int h = h0 + i * G + g.sub;
       float x[8], o[8];
-      unpack8(raw[i], x);
-      unpack8(other_members<INTER>(raw[i], ch.partner), o);
+      unpack8(g.raw[i], x);
+      unpack8(other_members<INTER>(g.raw[i], ch.partner), o);
       float sq = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) sq = __builtin_fmaf(x[e], x[e], sq);
       const float r = rsqrtf(head_sum<L>(sq) * inv_dim + eps);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = r * __builtin_fmaf(x[e], a[e], o[e] * b[e]);
-      if (mine && h < last) *reinterpret_cast<u32x4*>(dst + h * out.hs) = pack8(x);
+      if (g.mine && h < g.last) *reinterpret_cast<u32x4*>(g.dst + h * g.out_hs) = pack8(x);
     }
   }
 }
 
-// One wave's part of a token's heads: steps of 64 / L heads, q's then k's.
+// One wave's part of a token's heads: steps of 64 / L heads, q's then k's. The
+// first heads are loaded ahead of the angles.
 template <int L, bool INTER>
 __device__ __forceinline__ void rope_unit(const RopeArgs& g, int k_heads, int unit, int lane, float2* table) {
   const int token = unit / g.parts, part = unit % g.parts;
+  constexpr int G = 64 / L;
+  const int sq = (g.q.heads + G - 1) / G, sk = (k_heads + G - 1) / G;
+  const int s0 = (sq + sk) * part / g.parts, s1 = (sq + sk) * (part + 1) / g.parts;
+  Heads<L> q = heads_of<L>(g.q, g.qo, g.t.wq, g.t.dim, token, s0 * G, min(min(s1, sq) * G, g.q.heads), lane);
+  Heads<L> k = heads_of<L>(g.k, g.ko, g.t.wk, g.t.dim, token, max(s0 - sq, 0) * G, min((s1 - sq) * G, k_heads), lane);
+  if (s0 < sq) q.load(q.first);
+  if (s0 >= sq) k.load(k.first);
   for (int p = lane; p < g.t.pairs; p += 64) table[p] = turn_of(g.t, g.t.axis[p], p, token);
   wave_sync();
   const Chunk ch = chunk_of<INTER>(lane, lane % L, g.t.pairs);
   float c[8], s[8];
   turn_factors<INTER>(table, ch, c, s);
-  constexpr int G = 64 / L;
-  const int sq = (g.q.heads + G - 1) / G, sk = (k_heads + G - 1) / G;
-  const int s0 = (sq + sk) * part / g.parts, s1 = (sq + sk) * (part + 1) / g.parts;
-  if (s0 < sq)
-    rope_heads<L, INTER>(g.q, g.qo, g.t.wq, g.t.dim, g.t.eps, token, s0 * G, min(min(s1, sq) * G, g.q.heads), lane, ch,
-                         c, s);
-  if (s1 > sq)
-    rope_heads<L, INTER>(g.k, g.ko, g.t.wk, g.t.dim, g.t.eps, token, max(s0 - sq, 0) * G,
-                         min((s1 - sq) * G, k_heads), lane, ch, c, s);
+  const float inv_dim = 1.0f / (float)g.t.dim;
+  if (s0 < sq) rope_heads<L, INTER>(q, inv_dim, g.t.eps, ch, c, s);
+  if (s1 > sq) {
+    if (s0 < sq) k.load(k.first);
+    rope_heads<L, INTER>(k, inv_dim, g.t.eps, ch, c, s);
+  }
 }
 
 // The units of one wave. (tokens * parts is below 2^31: parts is above 1 only
