@@ -38,7 +38,8 @@ index and ``quantization_config``).
 
 The functions here only marshal torch tensors (device memory and the current
 stream) into the C ABI declared in include/ (fp8bl.h, fp8bl_layers.h,
-fp8bl_int8.h, fp8bl_qkv.h); all arithmetic runs in the HIP kernels. There is no CPU fallback: without the built library every
+fp8bl_int8.h, fp8bl_qkv.h), in Python over ctypes or, for the last two headers, in
+the compiled module _tensors; all arithmetic runs in the HIP kernels. There is no CPU fallback: without the built library every
 call raises.
 """
 
@@ -540,289 +541,23 @@ def fp8_block_glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, q
     return dx, dg, du
 
 
-# ---- 8-bit integer linear ----------------------------------------------
+# ---- 8-bit integer linear; from the QKV projection to its cache ---------
 
-_F32, _I8, _U8, _I32 = torch.float32, torch.int8, torch.uint8, torch.int32
-
-
-def _workspace(workspace: torch.Tensor | None, need: int, idx: int) -> tuple:
-    """(address, bytes, tensor) of a call's workspace, on the current device."""
-    if workspace is None:
-        if need == 0:
-            return 0, 0, None
-        workspace = torch.empty(need, dtype=_U8, device="cuda")
-    elif workspace.get_device() != idx or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on cuda:{idx}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+# These functions are compiled (binding/tensors.cpp, which has their
+# documentation): their smallest calls take longer on the host than on the GPU.
+# The first use of one loads the module.
+_COMPILED = ("int8_row_quantize", "int8_linear", "int8_linear_bf16", "fp8_qk_norm_rope", "fp8_qk_norm_rope_backward",
+             "fp8_kv_store", "fp8_kv_load", "fp8_qk_norm_rope_store")
 
 
-def int8_row_quantize(x: torch.Tensor, q: torch.Tensor | None = None,
-                      scale: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
-    """fp32 or bf16 x [M,K] -> (q int8 [M,K], scale fp32 [M]), x ~ q * scale: the
-    tokens of an activation or the output channels of a weight [N,K]."""
-    _outside_autograd("int8_row_quantize", x)
-    idx = _device_index(x, "x")
-    if torch.cuda.current_device() != idx:
-        with torch.cuda.device(idx):
-            return int8_row_quantize(x, q, scale)
-    if x.dtype is not _F32 and x.dtype is not _BF16:
-        raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
-    m, k = _matrix(x, "x")
-    if q is None:
-        q = x.new_empty((m, k), dtype=_I8)
-    if scale is None:
-        scale = x.new_empty((m,), dtype=_F32)
-    status = _lib.int8_row_quantize_raw(_array(x, x.dtype, (m, k), idx, "x"), _array(q, _I8, (m, k), idx, "q"),
-                                        _array(scale, _F32, (m,), idx, "scale"), m, k, x.dtype is _BF16,
-                                        _raw_stream(idx))
-    _check(status, "int8_row_quantize")
-    return q, scale
-
-
-def int8_linear(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
-                bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
-                workspace: torch.Tensor | None = None) -> torch.Tensor:
-    """int8 xq [M,K] with x_scale [M], int8 wq [N,K] with w_scale [N] -> bf16
-    y [M,N] = (xq wq^T) x_scale w_scale + bias, the integer sum exact.
-
-    ``bias`` bf16 [N]. ``workspace``, when given, holds at least
-    ``int8_workspace_size(M, N, K, from_bf16=False)`` bytes; calls that share one
-    must be ordered."""
-    _outside_autograd("int8_linear", x_scale, w_scale, bias)
-    idx = _device_index(xq, "xq")
-    if torch.cuda.current_device() != idx:
-        with torch.cuda.device(idx):
-            return int8_linear(xq, x_scale, wq, w_scale, bias, out, workspace)
-    m, k = _matrix(xq, "xq")
-    n = _matrix(wq, "wq")[0]
-    if out is None:
-        out = xq.new_empty((m, n), dtype=_BF16)
-    pointers = (_array(xq, _I8, (m, k), idx, "xq"), _array(x_scale, _F32, (m,), idx, "x_scale"),
-                _array(wq, _I8, (n, k), idx, "wq"), _array(w_scale, _F32, (n,), idx, "w_scale"),
-                _optional(bias, _BF16, (n,), idx, "bias"), _array(out, _BF16, (m, n), idx, "out"))
-    ws, ws_bytes, workspace = _workspace(workspace, _lib.int8_workspace_size(m, n, k, False), idx)
-    _check(_lib.int8_linear_raw(*pointers, m, n, k, ws, ws_bytes, _raw_stream(idx)), "int8_linear")
-    return out
-
-
-def int8_linear_bf16(x: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
-                     bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
-                     workspace: torch.Tensor | None = None) -> torch.Tensor:
-    """bf16 x [M,K] -> ``int8_row_quantize`` -> ``int8_linear``, the same bits as
-    those two calls. ``workspace``, when given, holds at least
-    ``int8_workspace_size(M, N, K)`` bytes; calls that share one must be ordered."""
-    _outside_autograd("int8_linear_bf16", x, w_scale, bias)
-    idx = _device_index(x, "x")
-    if torch.cuda.current_device() != idx:
-        with torch.cuda.device(idx):
-            return int8_linear_bf16(x, wq, w_scale, bias, out, workspace)
-    m, k = _matrix(x, "x")
-    n = _matrix(wq, "wq")[0]
-    if out is None:
-        out = x.new_empty((m, n))
-    pointers = (_array(x, _BF16, (m, k), idx, "x"), _array(wq, _I8, (n, k), idx, "wq"),
-                _array(w_scale, _F32, (n,), idx, "w_scale"), _optional(bias, _BF16, (n,), idx, "bias"),
-                _array(out, _BF16, (m, n), idx, "out"))
-    ws, ws_bytes, workspace = _workspace(workspace, _lib.int8_workspace_size(m, n, k), idx)
-    _check(_lib.int8_linear_bf16_raw(*pointers, m, n, k, ws, ws_bytes, _raw_stream(idx)), "int8_linear_bf16")
-    return out
-
-
-# ---- from the QKV projection to its cache -------------------------------
-
-_NO_HEADS = (0, 0, 0)
-
-
-def _heads(t: torch.Tensor, shape: tuple, idx: int, name: str) -> tuple:
-    """(address, token stride, head stride) of a bf16 [tokens, heads, dim] view."""
-    if t.dtype is _BF16 and t.get_device() == idx and t.shape == shape:
-        ts, hs, es = t.stride()
-        if es == 1:
-            return t.data_ptr(), ts, hs
-        raise ValueError(f"{name} must have its last axis contiguous")
-    if t.dtype is not _BF16:
-        raise TypeError(f"{name} must be {_BF16}, got {t.dtype}")
-    _device_index(t, name)
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    raise ValueError(f"{name} is on {t.device}, expected cuda:{idx}")
-
-
-def _head_shape(t: torch.Tensor, name: str) -> tuple:
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {list(t.shape)}")
-    return t.shape
-
-
-def _turn(q_weight, k_weight, positions, inv_freq, axes, dim: int, tokens: int, idx: int) -> tuple:
-    """The addresses of norm and rotation, the axes, the pairs, and each pair's axis."""
-    if positions.dim() == 1:
-        positions = positions[None]
-    count, pairs = _matrix(positions, "positions")[0], inv_freq.numel()
-    if axes is None:
-        if count != 1:
-            raise ValueError("axes is needed where positions has several")
-        axis = b""
-    else:
-        axis = bytes(axes)
-        if len(axis) != pairs:
-            raise ValueError(f"axes names {len(axis)} pairs, inv_freq has {pairs}")
-    if pairs > _lib.MAX_PAIRS:
-        raise ValueError(f"at most {_lib.MAX_PAIRS} pairs, got {pairs}")
-    return (_array(q_weight, _BF16, (dim,), idx, "q_weight"), _array(k_weight, _BF16, (dim,), idx, "k_weight"),
-            _array(positions, _I32, (count, tokens), idx, "positions"),
-            _array(inv_freq, _F32, (pairs,), idx, "inv_freq"), count, pairs, axis)
-
-
-def _cache(slots, k_cache, v_cache, k_scale, v_scale, tokens: int, heads: int, dim: int, idx: int) -> tuple:
-    rows = _head_shape(k_cache, "k_cache")[0]
-    whole, scales = (rows, heads, dim), (rows, heads)
-    return (_array(slots, _I32, (tokens,), idx, "slots"), _array(k_cache, _U8, whole, idx, "k_cache"),
-            _array(v_cache, _U8, whole, idx, "v_cache"), _array(k_scale, _F32, scales, idx, "k_scale"),
-            _array(v_scale, _F32, scales, idx, "v_scale"), rows)
-
-
-_NO_CACHE = (0, 0, 0, 0, 0, 0)
-
-
-def fp8_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
-                     positions: torch.Tensor, inv_freq: torch.Tensor, axes=None, eps: float = 1e-6,
-                     interleaved: bool = False, q_out: torch.Tensor | None = None,
-                     k_out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
-    """Norm and rotation of each head of bf16 q [T,Hq,D] and k [T,Hk,D]: x / sqrt(mean(x^2) + eps)
-    * weight, then pair i turned by positions[axes[i], token] * inv_freq[i].
-
-    q and k may be views of the projection's output (last axis contiguous, the
-    other strides multiples of 8); ``q_out`` may be q and ``k_out`` k. Weights
-    bf16 [D]; ``positions`` int32 [axes, T] or [T]; ``inv_freq`` fp32 [P]; ``axes``
-    a sequence of P axis numbers on the host (a tuple or ``bytes``), not needed
-    with one axis. Pair i is elements (i, i + P), or (2 i, 2 i + 1) with
-    ``interleaved``; elements from 2 P on are not turned. D is a multiple of 8
-    up to 256, P one of 8 (4 with ``interleaved``).
-
-    Not recorded by autograd: while gradients are enabled, inputs that require
-    one are refused; ``fp8_qk_norm_rope_backward`` is its backward pass."""
-    _outside_autograd("fp8_qk_norm_rope", q, k, q_weight, k_weight)
-    idx = _device_index(q, "q")
-    if torch.cuda.current_device() != idx:
-        with torch.cuda.device(idx):
-            return fp8_qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, axes, eps, interleaved, q_out, k_out)
-    q_shape = t, hq, d = _head_shape(q, "q")
-    k_shape = (t, _head_shape(k, "k")[1], d)
-    if q_out is None:
-        q_out = q.new_empty(q_shape)
-    if k_out is None:
-        k_out = k.new_empty(k_shape)
-    qw, kw, pos, freq, count, pairs, axis = _turn(q_weight, k_weight, positions, inv_freq, axes, d, t, idx)
-    args = _lib.qkv_pack(t, hq, k_shape[1], d, *_heads(q, q_shape, idx, "q"), *_heads(k, k_shape, idx, "k"),
-                         *_NO_HEADS, *_heads(q_out, q_shape, idx, "q_out"), *_heads(k_out, k_shape, idx, "k_out"),
-                         *_NO_HEADS, *_NO_HEADS, *_NO_HEADS, qw, kw, 0, 0, pos, freq, count, pairs,
-                         1 if interleaved else 0, eps, *_NO_CACHE, axis)
-    _check(_lib.qk_norm_rope_raw(args, _raw_stream(idx)), "fp8_qk_norm_rope")
-    return q_out, k_out
-
-
-def fp8_qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
-                              q_weight: torch.Tensor, k_weight: torch.Tensor, positions: torch.Tensor,
-                              inv_freq: torch.Tensor, axes=None, eps: float = 1e-6, interleaved: bool = False,
-                              q_grad: torch.Tensor | None = None, k_grad: torch.Tensor | None = None,
-                              need_weights: bool = True, workspace: torch.Tensor | None = None) -> tuple:
-    """Backward pass of ``fp8_qk_norm_rope``: the gradients dq, dk of what it
-    returned and its own inputs -> (q_grad, k_grad, q_weight_grad, k_weight_grad),
-    the first two bf16 like q and k (they may be given, as views of one packed
-    gradient, or as dq and dk themselves), the others fp32 [D], None with
-    ``need_weights`` false."""
-    _outside_autograd("fp8_qk_norm_rope_backward", dq, dk, q, k, q_weight, k_weight)
-    idx = _device_index(q, "q")
-    if torch.cuda.current_device() != idx:
-        with torch.cuda.device(idx):
-            return fp8_qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, axes, eps,
-                                             interleaved, q_grad, k_grad, need_weights, workspace)
-    q_shape = t, hq, d = _head_shape(q, "q")
-    k_shape = _, hk, _ = (t, _head_shape(k, "k")[1], d)
-    if q_grad is None:
-        q_grad = q.new_empty(q_shape)
-    if k_grad is None:
-        k_grad = k.new_empty(k_shape)
-    dqw = dkw = None
-    if need_weights:
-        dqw, dkw = (q.new_empty((d,), dtype=_F32) for _ in range(2))
-    qw, kw, pos, freq, count, pairs, axis = _turn(q_weight, k_weight, positions, inv_freq, axes, d, t, idx)
-    args = _lib.qkv_pack(t, hq, hk, d, *_heads(q, q_shape, idx, "q"), *_heads(k, k_shape, idx, "k"), *_NO_HEADS,
-                         *_heads(q_grad, q_shape, idx, "q_grad"), *_heads(k_grad, k_shape, idx, "k_grad"), *_NO_HEADS,
-                         *_heads(dq, q_shape, idx, "dq"), *_heads(dk, k_shape, idx, "dk"), qw, kw,
-                         dqw.data_ptr() if need_weights else 0, dkw.data_ptr() if need_weights else 0, pos, freq,
-                         count, pairs, 1 if interleaved else 0, eps, *_NO_CACHE, axis)
-    ws, ws_bytes, workspace = _workspace(workspace, _lib.qk_norm_rope_backward_workspace_size(t, hq, hk, d), idx)
-    _check(_lib.qk_norm_rope_backward_raw(args, ws, ws_bytes, _raw_stream(idx)), "fp8_qk_norm_rope_backward")
-    return q_grad, k_grad, dqw, dkw
-
-
-def fp8_kv_store(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
-                 v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor) -> None:
-    """bf16 k and v [T,H,D] into rows ``slots`` (int32 [T]) of an E4M3 cache: codes
-    uint8 [rows,H,D] with a scale fp32 [rows,H] for each token and head, S = amax / 448.
-
-    A token whose slot is negative or past the cache is padding and not stored;
-    where tokens share a slot the last one is. Pages are rows too: slot = page *
-    page size + offset, for caches viewed as [rows,H,D]. At most 65536 tokens a call."""
-    _outside_autograd("fp8_kv_store", k, v)
-    idx = _device_index(k, "k")
-    if torch.cuda.current_device() != idx:
-        with torch.cuda.device(idx):
-            return fp8_kv_store(k, v, slots, k_cache, v_cache, k_scale, v_scale)
-    shape = t, h, d = _head_shape(k, "k")
-    args = _lib.qkv_pack(t, 0, h, d, *_NO_HEADS, *_heads(k, shape, idx, "k"), *_heads(v, shape, idx, "v"),
-                         *_NO_HEADS, *_NO_HEADS, *_NO_HEADS, *_NO_HEADS, *_NO_HEADS, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.0,
-                         *_cache(slots, k_cache, v_cache, k_scale, v_scale, t, h, d, idx), b"")
-    _check(_lib.kv_store_raw(args, _raw_stream(idx)), "fp8_kv_store")
-
-
-def fp8_kv_load(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
-                slots: torch.Tensor, k_out: torch.Tensor | None = None,
-                v_out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
-    """Rows ``slots`` (int32 [T]) of the cache -> (k, v) bf16 [T,H,D], zeros for a
-    slot outside the cache. ``k_out`` and ``v_out`` may be views with strides."""
-    idx = _device_index(k_cache, "k_cache")
-    if torch.cuda.current_device() != idx:
-        with torch.cuda.device(idx):
-            return fp8_kv_load(k_cache, v_cache, k_scale, v_scale, slots, k_out, v_out)
-    _, h, d = _head_shape(k_cache, "k_cache")
-    shape = t, _, _ = (slots.numel(), h, d)
-    if k_out is None:
-        k_out = k_cache.new_empty(shape, dtype=_BF16)
-    if v_out is None:
-        v_out = k_cache.new_empty(shape, dtype=_BF16)
-    args = _lib.qkv_pack(t, 0, h, d, *_NO_HEADS, *_NO_HEADS, *_NO_HEADS, *_NO_HEADS,
-                         *_heads(k_out, shape, idx, "k_out"), *_heads(v_out, shape, idx, "v_out"), *_NO_HEADS,
-                         *_NO_HEADS, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.0,
-                         *_cache(slots, k_cache, v_cache, k_scale, v_scale, t, h, d, idx), b"")
-    _check(_lib.kv_load_raw(args, _raw_stream(idx)), "fp8_kv_load")
-    return k_out, v_out
-
-
-def fp8_qk_norm_rope_store(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: torch.Tensor,
-                           k_weight: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
-                           slots: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
-                           k_scale: torch.Tensor, v_scale: torch.Tensor, axes=None, eps: float = 1e-6,
-                           interleaved: bool = False, q_out: torch.Tensor | None = None) -> torch.Tensor:
-    """``fp8_qk_norm_rope`` and ``fp8_kv_store`` in one pass -> q_out: the cache
-    receives v and the normed and turned k, quantized from fp32 (storing a
-    returned k rounds it to bf16 first)."""
-    _outside_autograd("fp8_qk_norm_rope_store", q, k, v, q_weight, k_weight)
-    idx = _device_index(q, "q")
-    if torch.cuda.current_device() != idx:
-        with torch.cuda.device(idx):
-            return fp8_qk_norm_rope_store(q, k, v, q_weight, k_weight, positions, inv_freq, slots, k_cache, v_cache,
-                                          k_scale, v_scale, axes, eps, interleaved, q_out)
-    q_shape = t, hq, d = _head_shape(q, "q")
-    k_shape = _, hk, _ = (t, _head_shape(k, "k")[1], d)
-    if q_out is None:
-        q_out = q.new_empty(q_shape)
-    qw, kw, pos, freq, count, pairs, axis = _turn(q_weight, k_weight, positions, inv_freq, axes, d, t, idx)
-    args = _lib.qkv_pack(t, hq, hk, d, *_heads(q, q_shape, idx, "q"), *_heads(k, k_shape, idx, "k"),
-                         *_heads(v, k_shape, idx, "v"), *_heads(q_out, q_shape, idx, "q_out"), *_NO_HEADS, *_NO_HEADS,
-                         *_NO_HEADS, *_NO_HEADS, qw, kw, 0, 0, pos, freq, count, pairs, 1 if interleaved else 0, eps,
-                         *_cache(slots, k_cache, v_cache, k_scale, v_scale, t, hk, d, idx), axis)
-    _check(_lib.qk_norm_rope_store_raw(args, _raw_stream(idx)), "fp8_qk_norm_rope_store")
-    return q_out
+def __getattr__(name: str):
+    if name not in _COMPILED:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    _lib.load()
+    try:
+        from . import _tensors
+    except ImportError as e:
+        raise ImportError(f"{e}; run `python -m block_scaled_fp8_linear_amd.build`") from e
+    _tensors.configure(Fp8blError, _raw_stream)
+    globals().update({f: getattr(_tensors, f) for f in _COMPILED})
+    return globals()[name]

@@ -1,19 +1,22 @@
-"""Build libfp8bl.so (gfx950 only) in-tree with hipcc.
+"""Build libfp8bl.so (gfx950 only) and the compiled part of the binding in-tree.
 
     python -m block_scaled_fp8_linear_amd.build
 
 Each HIP source is compiled to an object in ``_build/`` (in parallel), then
-linked into ``block_scaled_fp8_linear_amd/libfp8bl.so``. Always rebuilds.
+linked into ``block_scaled_fp8_linear_amd/libfp8bl.so``; binding/tensors.cpp, host
+code over torch's headers, becomes ``_tensors.so`` beside it. Always rebuilds.
 """
 
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -21,6 +24,8 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libfp8bl.so")
+BINDING = os.path.join(PKG_DIR, "binding", "tensors.cpp")
+BINDING_PATH = os.path.join(PKG_DIR, "_tensors.so")
 
 ARCH = "gfx950"
 
@@ -65,20 +70,48 @@ def _compile(src: str, obj: str, verbose: bool) -> None:
         raise RuntimeError(f"hipcc failed for {os.path.basename(src)}:\n{res.stdout}\n{res.stderr}")
 
 
-def build(verbose: bool = False) -> str:
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
-    objs = [os.path.join(BUILD_DIR, os.path.basename(s) + ".o") for s in srcs]
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        list(ex.map(lambda so: _compile(so[0], so[1], verbose), zip(srcs, objs)))
-    tmp = LIB_PATH + ".tmp"
-    cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
+def _run(cmd: list[str], what: str, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+        raise RuntimeError(f"{what} failed:\n{res.stdout}\n{res.stderr}")
+
+
+def _compile_binding(obj: str, verbose: bool) -> None:
+    """binding/tensors.cpp to an object: host code only, with the host compiler."""
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+    includes = [sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
+                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), os.path.join(rocm, "include"), INCLUDE]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__", "-c", BINDING, "-o", obj]
+    for path in includes:
+        cmd += ["-I", path]
+    _run(cmd, "g++ for tensors.cpp", verbose)
+
+
+def _link_binding(obj: str, verbose: bool) -> None:
+    """Against the library beside it and torch, which is loaded by then."""
+    torch_lib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
+    tmp = BINDING_PATH + ".tmp"
+    _run(["g++", "-shared", obj, "-o", tmp, "-L", PKG_DIR, "-l:libfp8bl.so", "-L", torch_lib, "-lc10", "-ltorch_cpu",
+          "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "link of _tensors.so", verbose)
+    os.replace(tmp, BINDING_PATH)
+
+
+def build(verbose: bool = False) -> str:
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
+    objs = [os.path.join(BUILD_DIR, os.path.basename(s) + ".o") for s in srcs]
+    binding = os.path.join(BUILD_DIR, "tensors.cpp.o")
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        host = ex.submit(_compile_binding, binding, verbose)
+        list(ex.map(lambda so: _compile(so[0], so[1], verbose), zip(srcs, objs)))
+        host.result()
+    tmp = LIB_PATH + ".tmp"
+    _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp], "link", verbose)
     os.replace(tmp, LIB_PATH)
+    _link_binding(binding, verbose)
     return LIB_PATH
 
 

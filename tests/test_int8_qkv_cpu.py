@@ -274,3 +274,20 @@ def test_tensor_arguments():
             calls[i]()
         with torch.no_grad(), pytest.raises(TypeError, match="device tensor"):
             calls[i]()
+
+
+def test_compiled_calls_check_their_parameters():
+    i8, f = torch.zeros(2, 32, dtype=torch.int8), torch.zeros(2)
+    for call, text in ((lambda: F.int8_linear(i8, f, i8), "missing argument 'w_scale'"),
+                       (lambda: F.int8_linear(i8, f, i8, f, None, None, None, 1), "at most 7"),
+                       (lambda: F.int8_linear(i8, f, i8, f, scale=f), "unexpected keyword argument 'scale'"),
+                       (lambda: F.int8_linear(i8, f, i8, f, xq=i8), "multiple values"),
+                       (lambda: F.int8_linear(3, f, i8, f), "xq must be a tensor"),
+                       (lambda: F.fp8_kv_store(k=i8, v=i8), "missing argument")):
+        with pytest.raises(TypeError, match=text):
+            call()
+    with pytest.raises(AttributeError):
+        F.no_such_function
+    # keyword names that are not the interned ones
+    with pytest.raises(TypeError, match="device tensor"):
+        F.int8_linear(i8, f, **{"".join(["w", "q"]): i8, "".join(["w_", "scale"]): f})
