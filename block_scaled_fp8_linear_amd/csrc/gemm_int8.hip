@@ -199,7 +199,7 @@ void gemm_int8_kernel(GemmArgs g) {
     for (int m = 0; m < WM; ++m) acc[n][m] = i32x16{};
 
   int stage = 0;
-  bool stored = true;                  // the last unit's tile was whole (before the first unit: nothing to wait for)
+  bool stored = false;                 // the last unit's tile was whole
   for (int ci = 0; ci < my_units; ++ci) {
     const Unit CU = unit_of(ci);
     for (int kt = 0; kt < g.steps_per_unit; ++kt) {
@@ -222,13 +222,18 @@ void gemm_int8_kernel(GemmArgs g) {
           // this wave's reads of the stage have returned and its loads of the
           // next stage have landed; behind the barrier so have all waves'
           __builtin_amdgcn_s_waitcnt(kLgkmWait0);
-          // (a whole tile's stores, one for each 16 bytes, are behind the loads
-          // waited for in the next unit's first step and may take until its second)
-          if (kt == 0 && stored)
-            __builtin_amdgcn_s_waitcnt(vm_wait((S - 2) * T::kLoads + T::kStores));
-          else
+          // (In a unit's first step the last unit's stores are the newest
+          // operations: where all of them were issued, those of a whole tile, they
+          // may take until the second step.)
+          if (kt == 0 && ci > 0) {
+            if (stored)
+              __builtin_amdgcn_s_waitcnt(vm_wait((S - 2) * T::kLoads + T::kStores));
+            else
+              __builtin_amdgcn_s_waitcnt(vm_wait(0));
+          } else {
             __builtin_amdgcn_s_waitcnt(vm_wait((S - 2) * T::kLoads));
-          if (last || (kt == 0 && !stored)) __builtin_amdgcn_s_waitcnt(vm_wait(0));
+          }
+          if (last) __builtin_amdgcn_s_waitcnt(vm_wait(0));      // the epilogue's vectors
           if (!SPLIT && last) {
             asm volatile("" : "+v"(e_bias));     // not looked at before the wait above
             if (tid < kTN) ep_ws[tid] = __uint_as_float(e_ws), ep_bias[tid] = __uint_as_float(e_bias << 16);
