@@ -170,11 +170,25 @@ constexpr int kMaxRun = 16;
 
 // Bit r, in every lane: one of the slots that this wave looks at, behind token
 // i0 + r, is that token's. The workgroup's threads look at four slots each a
-// load, four loads on their way at a time; slots outside the run's own range, as
-// nearly all are, need no more than that comparison. Lane r of a wave holds the
-// slot of token i0 + r.
+// load, four loads on their way at a time (the first ahead of the run's own
+// slots); slots outside the run's own range, as nearly all are, need no more than
+// that comparison. Lane r of a wave holds the slot of token i0 + r.
 __device__ __forceinline__ uint32_t later_ones(const int32_t* __restrict__ slots, int i0, int run, int run_slots,
                                                int tokens) {
+  constexpr int kLoads = 4, kRound = kLoads * 4 * kQkvThreads;
+  int v[kLoads][4];
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int f = 0; f < kLoads; ++f) {
+      const int j = j0 + 4 * ((int)threadIdx.x + f * kQkvThreads);
+      if (j + 4 <= tokens)
+        __builtin_memcpy(v[f], slots + j, 16);
+      else
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[f][e] = j + e < tokens ? slots[j + e] : -1;
+    }
+  };
+  load(i0 + run);
   int lo = 0x7FFFFFFF, hi = -1;
   for (int r = 0; r < run; ++r) {
     const int s = __builtin_amdgcn_readlane(run_slots, r);
@@ -187,19 +201,8 @@ __device__ __forceinline__ uint32_t later_ones(const int32_t* __restrict__ slots
   for (int r = 1; r < run; ++r)
     again |= run_slots == __builtin_amdgcn_readlane(run_slots, r) && (int)(threadIdx.x & 63) < r;
   uint32_t found = 0;
-  constexpr int kThreads = kQkvThreads, kLoads = 4, kRound = kLoads * 4 * kThreads;
   for (int j0 = i0 + run; j0 < tokens; j0 += kRound) {
-    int v[kLoads][4];
-    const int first = j0 + 4 * (int)threadIdx.x;
-#pragma unroll
-    for (int f = 0; f < kLoads; ++f) {
-      const int j = first + f * 4 * kThreads;
-      if (j + 4 <= tokens)
-        __builtin_memcpy(v[f], slots + j, 16);
-      else
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[f][e] = j + e < tokens ? slots[j + e] : -1;
-    }
+    if (j0 != i0 + run) load(j0);
     bool near = false;
 #pragma unroll
     for (int f = 0; f < kLoads; ++f)
@@ -227,7 +230,7 @@ template <int L, bool INTER, bool FUSED>
 __device__ __forceinline__ void store_run(const RopeArgs& g, const CacheArgs& k, int run_index) {
   __shared__ uint32_t found[kQkvWaves];
   __shared__ float2 tables[FUSED ? kMaxRun : 1][FUSED ? FP8BL_MAX_PAIRS : 1];
-  constexpr int G = 64 / L, kBatch = 4;
+  constexpr int G = 64 / L, kBatch = 2;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i0 = run_index * k.run, run = min(k.run, g.t.tokens - i0);
