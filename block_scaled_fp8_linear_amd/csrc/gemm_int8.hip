@@ -138,7 +138,9 @@ void gemm_int8_kernel(GemmArgs g) {
     xrs = make_rsrc(g.xq + (size_t)U.m0 * K, (uint32_t)(U.nsteps > 0 ? min(M - U.m0, kTM) * K : 0));
     wrs = make_rsrc(g.wq + (size_t)U.n0 * K, (uint32_t)(U.nsteps > 0 ? min(N - U.n0, kTN) * K : 0));
   };
-  // load i (of kLoads) of step `kt` of the load unit into the stage at `sb`
+  // load i (of kLoads) of step `kt` of the load unit into the stage at `sb`; behind
+  // the unit's last step everything is out of range, without a scalar offset that
+  // would pass the descriptor's size too
   auto issue = [&](int sb, int kt, int i) {
     const int kbase = (LU.step0 + kt) * kBK;
     const int klim = kt < LU.nsteps ? K - kbase : 0;
@@ -148,7 +150,7 @@ void gemm_int8_kernel(GemmArgs g) {
     const uint32_t vo = of_x ? xvo[of_x ? j : 0] : wvo[of_x ? 0 : j];
     const int row = of_x ? (kTM / 4) * wave + T::kRows * j : kTM + (kTN / 4) * wave + T::kRows * j;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(of_x ? xrs : wrs, (lds_ptr_t)&lds[sb + row * kBK], 16, in ? vo : kOob,
-                                             (uint32_t)kbase, 0, 0);
+                                             (uint32_t)(klim > 0 ? kbase : 0), 0, 0);
   };
 
   // ---- Operands of slice s of a stage.
