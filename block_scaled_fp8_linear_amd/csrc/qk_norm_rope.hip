@@ -27,9 +27,11 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 }
 
 // fl32(x / s) for the codes. With y = fl32(1 / s), q0 = fl32(x y) and the residual
-// r = x - q0 s (exact), fma(r, y, q0) is the quotient but for the last bit's
-// rounding where it lies within 2^-23 of a bit's half; subnormal scales and their
-// like, whose residuals are not exact, take the IEEE division.
+// r = x - q0 s (exact), fma(r, y, q0) is the quotient, but for its last bit where
+// the quotient lies within 2^-22 of a last bit's step of the middle between two
+// floats: of 2^14 pairs of bf16 mantissas none gets another code that way.
+// Subnormal scales and their like, whose residuals are not exact, take the IEEE
+// division.
 __device__ __forceinline__ void quotients(float (&x)[8], float s) {
   if (s >= 0x1p-64f) {
     const float y = __fdiv_rn(1.0f, s);

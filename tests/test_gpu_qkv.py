@@ -306,6 +306,26 @@ def test_one_slot_for_all():
         check_store(before, after, slots, R.stored(c.k), R.stored(c.v))
 
 
+def test_store_every_bf16_quotient():
+    """Every pair of mantissas of a value and its head's largest, the values down
+    to 2^-12 of it: codes of the IEEE quotient, ties among them."""
+    m = torch.arange(128, 256, dtype=torch.float64)
+    x = (m[:, None] * 2.0 ** -torch.arange(13, dtype=torch.float64)).reshape(-1)
+    x = torch.cat([x, torch.zeros(-len(x) % 255)])
+    heads = len(x) // 255
+    a = m[:, None, None, None].expand(128, heads, 1, 1)
+    values = torch.minimum(x.view(1, heads, 255, 1).expand(128, heads, 255, 1), a)
+    v = torch.cat([a, values], 2).squeeze(-1)
+    for scale in (1.0, 2.0 ** -40, 2.0 ** 90):
+        k = (v * scale).to(BF).cuda()
+        assert torch.equal(k.double().cpu(), v * scale)
+        after = cache(128, heads, 256)
+        before = [c.clone() for c in after]
+        slots = torch.arange(128, dtype=torch.int32, device="cuda")
+        F.fp8_kv_store(k, -k, slots, *after)
+        check_store(before, after, slots, R.stored(k), R.stored(-k))
+
+
 def test_special_heads():
     """Heads of zeros of both signs, subnormals, the largest values, ties."""
     d = 32
