@@ -39,8 +39,8 @@ index and ``quantization_config``).
 The functions here only marshal torch tensors (device memory and the current
 stream) into the C ABI declared in include/ (fp8bl.h, fp8bl_layers.h,
 fp8bl_int8.h, fp8bl_qkv.h), in Python over ctypes or, for the last two headers, in
-the compiled module _tensors; all arithmetic runs in the HIP kernels. There is no CPU fallback: without the built library every
-call raises.
+the compiled module _tensors; all arithmetic runs in the HIP kernels. There is no
+CPU fallback: without the built library every call raises.
 """
 
 from __future__ import annotations
@@ -51,7 +51,8 @@ from . import _lib
 from ._lib import (  # noqa: F401
     ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU,
     PATH_AUTO, PATH_LARGE, PATH_SKINNY, PATH_TILED, Fp8blError, abi_version, device_supported,
-    int8_workspace_size, layer_workspace_size, qk_norm_rope_backward_workspace_size, status_string, w8a8_workspace_size, workspace_size,
+    int8_workspace_size, layer_workspace_size, qk_norm_rope_backward_workspace_size, status_string,
+    w8a8_workspace_size, workspace_size,
 )
 
 BLOCK = 128
@@ -550,9 +551,7 @@ _COMPILED = ("int8_row_quantize", "int8_linear", "int8_linear_bf16", "fp8_qk_nor
              "fp8_kv_store", "fp8_kv_load", "fp8_qk_norm_rope_store")
 
 
-def __getattr__(name: str):
-    if name not in _COMPILED:
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+def _compiled(name: str):
     _lib.load()
     try:
         from . import _tensors
@@ -561,3 +560,13 @@ def __getattr__(name: str):
     _tensors.configure(Fp8blError, _raw_stream)
     globals().update({f: getattr(_tensors, f) for f in _COMPILED})
     return globals()[name]
+
+
+def __getattr__(name: str):
+    if name not in _COMPILED:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    try:
+        return _compiled(name)
+    except (ImportError, OSError, RuntimeError):
+        # not built: like the other functions, it can be imported and raises when called
+        return lambda *args, **kwargs: _compiled(name)(*args, **kwargs)

@@ -35,7 +35,12 @@ struct Raise {
 PyObject* g_error;        // the package's Fp8blError
 PyObject* g_raw_stream;   // torch's current stream of a device, as a number
 
-void check(int status, const char* where) {
+// Makes a call, other threads running meanwhile: a launch can wait for the GPU.
+template <typename F>
+void run(const char* where, F call) {
+  PyThreadState* const state = PyEval_SaveThread();
+  const int status = call();
+  PyEval_RestoreThread(state);
   if (status == FP8BL_OK) return;
   PyObject* e = PyObject_CallFunction(g_error, "is", status, where);
   if (e != nullptr) {
@@ -262,9 +267,10 @@ PyObject* row_quantize(Args a) {
   int8_t* const qp = static_cast<int8_t*>(a.array(1, ScalarType::Char, {m, k}, idx));
   float* const sp = static_cast<float*>(a.array(2, ScalarType::Float, {m}, idx));
   const hipStream_t st = stream_of(idx);
-  check(bf16 ? int8_row_quantize_bf16(static_cast<uint16_t*>(xp), qp, sp, m, k, st)
-             : int8_row_quantize(static_cast<float*>(xp), qp, sp, m, k, st),
-        "int8_row_quantize");
+  run("int8_row_quantize", [&] {
+    return bf16 ? int8_row_quantize_bf16(static_cast<uint16_t*>(xp), qp, sp, m, k, st)
+                : int8_row_quantize(static_cast<float*>(xp), qp, sp, m, k, st);
+  });
   return pair(q, scale);
 }
 
@@ -284,7 +290,8 @@ PyObject* linear(Args a) {
   auto* bias = static_cast<uint16_t*>(a.optional(4, ScalarType::BFloat16, {n}, idx));
   auto* y = static_cast<uint16_t*>(a.array(5, ScalarType::BFloat16, {m, n}, idx));
   const Workspace w(a, 6, int8_linear_workspace_size(m, n, k), idx, x);
-  check(int8_linear(xq, xs, wq, ws, bias, y, m, n, k, w.p, w.bytes, stream_of(idx)), "int8_linear");
+  const hipStream_t st = stream_of(idx);
+  run("int8_linear", [&] { return int8_linear(xq, xs, wq, ws, bias, y, m, n, k, w.p, w.bytes, st); });
   return out.release();
 }
 
@@ -303,7 +310,8 @@ PyObject* linear_bf16(Args a) {
   auto* bias = static_cast<uint16_t*>(a.optional(3, ScalarType::BFloat16, {n}, idx));
   auto* y = static_cast<uint16_t*>(a.array(4, ScalarType::BFloat16, {m, n}, idx));
   const Workspace w(a, 5, int8_linear_bf16_workspace_size(m, n, k), idx, xt);
-  check(int8_linear_bf16(x, wq, ws, bias, y, m, n, k, w.p, w.bytes, stream_of(idx)), "int8_linear_bf16");
+  const hipStream_t st = stream_of(idx);
+  run("int8_linear_bf16", [&] { return int8_linear_bf16(x, wq, ws, bias, y, m, n, k, w.p, w.bytes, st); });
   return out.release();
 }
 
@@ -399,7 +407,8 @@ PyObject* norm_rope(Args a) {
   const With wq(a, 9, qo), wk(a, 10, ko);
   g.q_out = a.heads(9, qs, idx);
   g.k_out = a.heads(10, ks, idx);
-  check(fp8_qk_norm_rope(&g, stream_of(idx)), "fp8_qk_norm_rope");
+  const hipStream_t st = stream_of(idx);
+  run("fp8_qk_norm_rope", [&] { return fp8_qk_norm_rope(&g, st); });
   return pair(qo, ko);
 }
 
@@ -422,7 +431,6 @@ PyObject* norm_rope_backward(Args a) {
   const With wq(a, 11, qg), wk(a, 12, kg);
   g.q_out = a.heads(11, qs, idx);
   g.k_out = a.heads(12, ks, idx);
-  Output none_q, none_k;
   PyObject* weights[2] = {nullptr, nullptr};
   const bool need = a.truth(13, true);
   Tensor dqw, dkw;
@@ -433,7 +441,8 @@ PyObject* norm_rope_backward(Args a) {
     g.dk_weight = static_cast<float*>(dkw.data_ptr());
   }
   const Workspace w(a, 14, fp8_qk_norm_rope_backward_workspace_size(g.tokens, g.q_heads, g.k_heads, g.head_dim), idx, q);
-  check(fp8_qk_norm_rope_backward(&g, w.p, w.bytes, stream_of(idx)), "fp8_qk_norm_rope_backward");
+  const hipStream_t st = stream_of(idx);
+  run("fp8_qk_norm_rope_backward", [&] { return fp8_qk_norm_rope_backward(&g, w.p, w.bytes, st); });
   if (need) {
     weights[0] = THPVariable_Wrap(dqw);
     weights[1] = THPVariable_Wrap(dkw);
@@ -468,7 +477,8 @@ PyObject* store(Args a) {
   g.k = a.heads(0, ks, idx);
   g.v = a.heads(1, ks, idx);
   set_cache(a, 2, 3, idx, &g);
-  check(fp8_kv_store(&g, stream_of(idx)), "fp8_kv_store");
+  const hipStream_t st = stream_of(idx);
+  run("fp8_kv_store", [&] { return fp8_kv_store(&g, st); });
   Py_RETURN_NONE;
 }
 
@@ -486,7 +496,8 @@ PyObject* load(Args a) {
   const With wk(a, 5, k), wv(a, 6, v);
   g.k_out = a.heads(5, ks, idx);
   g.v_out = a.heads(6, ks, idx);
-  check(fp8_kv_load(&g, stream_of(idx)), "fp8_kv_load");
+  const hipStream_t st = stream_of(idx);
+  run("fp8_kv_load", [&] { return fp8_kv_load(&g, st); });
   return pair(k, v);
 }
 
@@ -508,7 +519,8 @@ PyObject* norm_rope_store(Args a) {
   Output qo(a, 15, qs, ScalarType::BFloat16, q);
   const With wq(a, 15, qo);
   g.q_out = a.heads(15, qs, idx);
-  check(fp8_qk_norm_rope_store(&g, stream_of(idx)), "fp8_qk_norm_rope_store");
+  const hipStream_t st = stream_of(idx);
+  run("fp8_qk_norm_rope_store", [&] { return fp8_qk_norm_rope_store(&g, st); });
   return qo.release();
 }
 

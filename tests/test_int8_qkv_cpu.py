@@ -291,3 +291,18 @@ def test_compiled_calls_check_their_parameters():
     # keyword names that are not the interned ones
     with pytest.raises(TypeError, match="device tensor"):
         F.int8_linear(i8, f, **{"".join(["w", "q"]): i8, "".join(["w_", "scale"]): f})
+
+
+def test_names_without_the_library(monkeypatch):
+    """Not built: the compiled functions are there like the others, and raise when
+    they are called."""
+    for name in F._COMPILED:
+        monkeypatch.delitem(vars(F), name, raising=False)
+    monkeypatch.setattr(F._lib, "_lib", None)
+    monkeypatch.setattr(F._lib, "LIB_PATH", "/nowhere/libfp8bl.so")
+    for name in F._COMPILED:
+        with pytest.raises(ImportError, match="not built"):
+            getattr(F, name)()
+    monkeypatch.undo()
+    with pytest.raises(TypeError, match="missing argument"):
+        F.int8_linear()
