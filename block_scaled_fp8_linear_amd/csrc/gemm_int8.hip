@@ -68,7 +68,10 @@ struct Tile {
   static constexpr int kRows = 1024 / kBK;                        // of a load
   static constexpr int kXLoads = kTM / 4 / kRows, kWLoads = kTN / 4 / kRows;    // for each wave and step
   static constexpr int kLoads = kXLoads + kWLoads;
-  static_assert(S * kStage + (2 * kTN + kTM) * 4 <= 160 * 1024, "the stages and the epilogue's vectors fit the LDS");
+  static constexpr int kVectors = (2 * kTN + kTM) * 4;            // of the epilogue
+  static constexpr int kRowsOut = WN >= 2 ? 4 * 32 * 128 : 0;     // and its rows
+  static constexpr int kLds = S * kStage + kVectors + kRowsOut;
+  static_assert(kLds <= 160 * 1024, "the stages, the epilogue's vectors and its rows fit the LDS");
   static constexpr int kStores = 2 * WM * WN;                     // of a wave's sums as bf16 (the splits' own are twice as many)
   static_assert((S - 2) * kLoads + kStores <= 63 && (S - 1) * kLoads <= 63, "outstanding loads fit the counter");
 };
@@ -81,10 +84,11 @@ void gemm_int8_kernel(GemmArgs g) {
   // The stages and the epilogue's vectors in one array: with several, the
   // compiler tells their accesses apart and waits for every load into LDS
   // before the next read of it.
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[S * kStage + (2 * kTN + kTM) * 4];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::kLds];
   float* const ep_ws = reinterpret_cast<float*>(&lds[S * kStage]);
   float* const ep_bias = ep_ws + kTN;
   float* const ep_xs = ep_bias + kTN;
+  uint8_t* const rows_out = &lds[S * kStage + T::kVectors + (T::kRowsOut / 4) * (threadIdx.x >> 6)];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -279,7 +283,7 @@ void gemm_int8_kernel(GemmArgs g) {
     // ---- Epilogue of unit ci.
     // With 16 blocks the sums stay in accumulation registers and are read out one
     // at a time: left to itself the compiler copies all of them at once and
-    // spills what the loop keeps (8192 x 12288 x 4096 392 us, 381 so). It knows
+    // spills what the loop keeps (8192 x 12288 x 4096 3% slower). It knows
     // nothing of the wait between the last products and these reads, so that is
     // here, for every block.
     constexpr bool kReadOut = WM * WN >= 16;
@@ -323,54 +327,82 @@ void gemm_int8_kernel(GemmArgs g) {
           }
       }
     } else {
+      // Two blocks of columns at a time go through LDS, 32 rows of 128 bytes for each
+      // wave, and leave eight lanes a row: whole lines where N is a multiple of 64, and
+      // those past the caches (8192 x 12288 x 4096 with its quantizer 388 us, 410 with
+      // stores of 32 bytes a row straight from the registers; 16384 x 5120 x 5120 377
+      // and 384; 4000 x 4300 x 4096, whose lines are in parts, 98 and 94). Lines in
+      // parts are slower past the caches: 8191 x 8191 x 4096 277 us and 259 through
+      // them, 287 from the registers.
+      constexpr int kWide = WN >= 2 ? 2 : 1;
+      const bool lines = kWide == 2 && N % 64 == 0;
+      auto put = [&](int row, int col, u32x4 out) {
+        uint16_t* const to = g.y + ((size_t)CU.m0 + row) * N + col;
+        if (lines && row < rows && col < N)
+          __builtin_nontemporal_store(out, reinterpret_cast<u32x4*>(to));
+        else if (row < rows && col + 8 <= N)
+          __builtin_memcpy(to, &out, 16);
+        else if (row < rows)
 #pragma unroll
-      for (int n = 0; n < WN; ++n)
+          for (int i = 0; i < 8; ++i)
+            if (col + i < N) to[i] = (uint16_t)(out[i >> 1] >> (16 * (i & 1)));
+      };
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {            // column groups 2 p and 2 p + 1
-          float w[2][4], b[2][4];
+      for (int n0 = 0; n0 < WN; n0 += kWide) {
+        float w[kWide][4][4], b[kWide][4][4];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int at = col0 + 32 * n + 16 * p + 8 * q + 4 * eh;
+        for (int j = 0; j < kWide; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int at = col0 + 32 * (n0 + j) + 8 * q + 4 * eh;
             const f32x4 wv = *reinterpret_cast<const f32x4*>(&ep_ws[at]);
             const f32x4 bv = *reinterpret_cast<const f32x4*>(&ep_bias[at]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[q][i] = wv[i], b[q][i] = bv[i];
+            for (int i = 0; i < 4; ++i) w[j][q][i] = wv[i], b[j][q][i] = bv[i];
           }
 #pragma unroll
-          for (int m = 0; m < WM; ++m) {
-            __builtin_amdgcn_sched_barrier(0);   // a few sums at a time in registers
-            const float x = ep_xs[row0 + 32 * m];
-            uint32_t d[2][2];
+        for (int m = 0; m < WM; ++m) {
+          const int row = row0 + 32 * m;
+          const float x = ep_xs[row];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              float v[4];
+          for (int j = 0; j < kWide; ++j)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                v[i] = (float)sum(n, m, 4 * (2 * p + q) + i) * (x * w[q][i]);
-                if (g.bias) v[i] += b[q][i];
+            for (int p = 0; p < 2; ++p) {        // column groups 2 p and 2 p + 1
+              __builtin_amdgcn_sched_barrier(0);   // a few sums at a time in registers
+              uint32_t d[2][2];
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  v[i] = (float)sum(n0 + j, m, 4 * (2 * p + q) + i) * (x * w[j][2 * p + q][i]);
+                  if (g.bias) v[i] += b[j][2 * p + q][i];
+                }
+                d[q][0] = pack_bf16x2(v[0], v[1]);
+                d[q][1] = pack_bf16x2(v[2], v[3]);
               }
-              d[q][0] = pack_bf16x2(v[0], v[1]);
-              d[q][1] = pack_bf16x2(v[2], v[3]);
-            }
-            // halves of the wave trade groups: each lane then has 8 columns in a row
-            u32x4 out;
+              // halves of the wave trade groups: each lane then has 8 columns in a row
+              u32x4 out;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const auto t = __builtin_amdgcn_permlane32_swap(d[0][i], d[1][i], false, false);
-              out[i] = t[0];
-              out[2 + i] = t[1];
+              for (int i = 0; i < 2; ++i) {
+                const auto t = __builtin_amdgcn_permlane32_swap(d[0][i], d[1][i], false, false);
+                out[i] = t[0];
+                out[2 + i] = t[1];
+              }
+              if constexpr (kWide == 2)          // into the wave's 32 rows of 128 bytes
+                *reinterpret_cast<u32x4*>(&rows_out[er * 128 + (((4 * j + 2 * p + eh) ^ (er & 7)) << 4)]) = out;
+              else
+                put(row, CU.n0 + col0 + 16 * p + 8 * eh, out);
             }
-            const int row = row0 + 32 * m;
-            const int col = CU.n0 + col0 + 32 * n + 16 * p + 8 * eh;
-            uint16_t* const to = g.y + ((size_t)CU.m0 + row) * N + col;
-            if (row < rows && col + 8 <= N)
-              __builtin_memcpy(to, &out, 16);
-            else if (row < rows)
+          if constexpr (kWide == 2)
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (col + i < N) to[i] = (uint16_t)(out[i >> 1] >> (16 * (i & 1)));
-          }
+            for (int i = 0; i < 4; ++i) {
+              const int r = 8 * i + (le >> 3);
+              const u32x4 out = *reinterpret_cast<const u32x4*>(&rows_out[r * 128 + (((le & 7) ^ (r & 7)) << 4)]);
+              put(32 * WM * wm + 32 * m + r, CU.n0 + col0 + 32 * n0 + 8 * (le & 7), out);
+            }
         }
+      }
     }
 #pragma unroll
     for (int n = 0; n < WN; ++n)
@@ -474,7 +506,7 @@ hipError_t launch_tiles(GemmArgs g, hipStream_t stream) {
   g.tiles_m = (g.M + tm - 1) / tm;
   g.tiles_n = (g.N + tn - 1) / tn;
   const int64_t units = (int64_t)g.tiles_m * g.tiles_n * g.splits;
-  const int64_t most = (int64_t)device_cus() * (160 * 1024 / (S * Tile<WM, WN, S>::kStage + (2 * tn + tm) * 4));
+  const int64_t most = (int64_t)device_cus() * (160 * 1024 / Tile<WM, WN, S>::kLds);
   const dim3 grid((uint32_t)(units < most ? units : most));
   if (g.splits == 1)
     hipLaunchKernelGGL((gemm_int8_kernel<WM, WN, S, false>), grid, dim3(kThreads), 0, stream, g);
