@@ -16,7 +16,7 @@ struct LoadArgs {
   int tokens, dim, rows;
 };
 
-template <int L>
+template <int L, bool PAST>
 __global__ __launch_bounds__(kQkvThreads)
 void load_kernel(LoadArgs g) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -32,12 +32,13 @@ void load_kernel(LoadArgs g) {
         u32x4 out = {0, 0, 0, 0};
         if (kept) {
           const size_t row = (size_t)slot * heads + h;
-          const u32x2 codes = *reinterpret_cast<const u32x2*>(g.codes[i] + row * g.dim + col);
+          const u32x2* const from = reinterpret_cast<const u32x2*>(g.codes[i] + row * g.dim + col);
+          const u32x2 codes = PAST ? __builtin_nontemporal_load(from) : *from;
           const float s = g.scales[i][row];
           const u32x2 a = dequant4(codes[0], s), b = dequant4(codes[1], s);
           out = u32x4{a[0], a[1], b[0], b[1]};
         }
-        *reinterpret_cast<u32x4*>(g.out[i].p + token * g.out[i].ts + h * g.out[i].hs + col) = out;
+        put8<PAST>(g.out[i].p + token * g.out[i].ts + h * g.out[i].hs + col, out);
       }
     }
   }
@@ -56,8 +57,11 @@ struct Load {
                      (int)a.head_dim,
                      (int)a.cache_rows};
     const int64_t blocks = (a.tokens + kQkvWaves - 1) / kQkvWaves;
-    hipLaunchKernelGGL((load_kernel<L>), dim3((uint32_t)(blocks < kMaxBlocks ? blocks : kMaxBlocks)),
-                       dim3(kQkvThreads), 0, stream, g);
+    const dim3 grid((uint32_t)(blocks < kMaxBlocks ? blocks : kMaxBlocks));
+    if (past_caches(a.tokens * a.k_heads * a.head_dim * 6))       // of keys and values one byte and two each
+      hipLaunchKernelGGL((load_kernel<L, true>), grid, dim3(kQkvThreads), 0, stream, g);
+    else
+      hipLaunchKernelGGL((load_kernel<L, false>), grid, dim3(kQkvThreads), 0, stream, g);
     return hipGetLastError();
   }
 };

@@ -66,7 +66,7 @@ struct CacheArgs {
 // steps' loads on their way at a time.
 constexpr int kAhead = 2;
 
-template <int L>
+template <int L, bool PAST>
 struct Heads {
   const uint16_t* src;
   uint16_t* dst;
@@ -80,23 +80,23 @@ struct Heads {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int h = h0 + i * (64 / L) + sub;
-      raw[i] = mine && h < last ? *reinterpret_cast<const u32x4*>(src + h * in_hs) : u32x4{0, 0, 0, 0};
+      raw[i] = mine && h < last ? get8<PAST>(src + h * in_hs) : u32x4{0, 0, 0, 0};
     }
   }
 };
 
-template <int L>
-__device__ __forceinline__ Heads<L> heads_of(const HeadView& in, const HeadView& out, const uint16_t* w, int dim,
-                                             int token, int first, int last, int lane) {
+template <int L, bool PAST>
+__device__ __forceinline__ Heads<L, PAST> heads_of(const HeadView& in, const HeadView& out, const uint16_t* w, int dim,
+                                                   int token, int first, int last, int lane) {
   const int col = 8 * (lane % L);
-  return Heads<L>{in.p + token * in.ts + col, out.p + token * out.ts + col, w + col, in.hs, out.hs, first, last,
-                  lane / L, col < dim, {}};
+  return Heads<L, PAST>{in.p + token * in.ts + col, out.p + token * out.ts + col, w + col, in.hs, out.hs, first, last,
+                        lane / L, col < dim, {}};
 }
 
 // The first loads are on their way already.
-template <int L, bool INTER>
-__device__ __forceinline__ void rope_heads(Heads<L>& g, float inv_dim, float eps, const Chunk& ch, const float (&c)[8],
-                                           const float (&s)[8]) {
+template <int L, bool INTER, bool PAST>
+__device__ __forceinline__ void rope_heads(Heads<L, PAST>& g, float inv_dim, float eps, const Chunk& ch,
+                                           const float (&c)[8], const float (&s)[8]) {
   float a[8], b[8];
   {
     const u32x4 raw = g.mine ? *reinterpret_cast<const u32x4*>(g.w) : u32x4{0, 0, 0, 0};
@@ -122,21 +122,21 @@ __device__ __forceinline__ void rope_heads(Heads<L>& g, float inv_dim, float eps
       const float r = rsqrtf(head_sum<L>(sq) * inv_dim + eps);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = r * __builtin_fmaf(x[e], a[e], o[e] * b[e]);
-      if (g.mine && h < g.last) *reinterpret_cast<u32x4*>(g.dst + h * g.out_hs) = pack8(x);
+      if (g.mine && h < g.last) put8<PAST>(g.dst + h * g.out_hs, pack8(x));
     }
   }
 }
 
 // One wave's part of a token's heads: steps of 64 / L heads, q's then k's. The
 // first heads are loaded ahead of the angles.
-template <int L, bool INTER>
+template <int L, bool INTER, bool PAST>
 __device__ __forceinline__ void rope_unit(const RopeArgs& g, int k_heads, int unit, int lane, float2* table) {
   const int token = unit / g.parts, part = unit % g.parts;
   constexpr int G = 64 / L;
   const int sq = (g.q.heads + G - 1) / G, sk = (k_heads + G - 1) / G;
   const int s0 = (sq + sk) * part / g.parts, s1 = (sq + sk) * (part + 1) / g.parts;
-  Heads<L> q = heads_of<L>(g.q, g.qo, g.t.wq, g.t.dim, token, s0 * G, min(min(s1, sq) * G, g.q.heads), lane);
-  Heads<L> k = heads_of<L>(g.k, g.ko, g.t.wk, g.t.dim, token, max(s0 - sq, 0) * G, min((s1 - sq) * G, k_heads), lane);
+  auto q = heads_of<L, PAST>(g.q, g.qo, g.t.wq, g.t.dim, token, s0 * G, min(min(s1, sq) * G, g.q.heads), lane);
+  auto k = heads_of<L, PAST>(g.k, g.ko, g.t.wk, g.t.dim, token, max(s0 - sq, 0) * G, min((s1 - sq) * G, k_heads), lane);
   if (s0 < sq) q.load(q.first);
   if (s0 >= sq) k.load(k.first);
   for (int p = lane; p < g.t.pairs; p += 64) table[p] = turn_of(g.t, g.t.axis[p], p, token);
@@ -145,27 +145,27 @@ __device__ __forceinline__ void rope_unit(const RopeArgs& g, int k_heads, int un
   float c[8], s[8];
   turn_factors<INTER>(table, ch, c, s);
   const float inv_dim = 1.0f / (float)g.t.dim;
-  if (s0 < sq) rope_heads<L, INTER>(q, inv_dim, g.t.eps, ch, c, s);
+  if (s0 < sq) rope_heads<L, INTER, PAST>(q, inv_dim, g.t.eps, ch, c, s);
   if (s1 > sq) {
     if (s0 < sq) k.load(k.first);
-    rope_heads<L, INTER>(k, inv_dim, g.t.eps, ch, c, s);
+    rope_heads<L, INTER, PAST>(k, inv_dim, g.t.eps, ch, c, s);
   }
 }
 
 // The units of one wave. (tokens * parts is below 2^31: parts is above 1 only
 // for few tokens.)
-template <int L, bool INTER>
+template <int L, bool INTER, bool PAST>
 __device__ __forceinline__ void rope_waves(const RopeArgs& g, int k_heads, int block, int blocks, float2* table) {
   const int units = g.t.tokens * g.parts, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (int64_t u = (int64_t)block * kQkvWaves + wave; u < units; u += (int64_t)blocks * kQkvWaves)
-    rope_unit<L, INTER>(g, k_heads, (int)u, threadIdx.x & 63, table);
+    rope_unit<L, INTER, PAST>(g, k_heads, (int)u, threadIdx.x & 63, table);
 }
 
-template <int L, bool INTER>
+template <int L, bool INTER, bool PAST>
 __global__ __launch_bounds__(kQkvThreads)
 void rope_kernel(RopeArgs g) {
   __shared__ float2 table[kQkvWaves][FP8BL_MAX_PAIRS];
-  rope_waves<L, INTER>(g, g.k.heads, blockIdx.x, gridDim.x, table[threadIdx.x >> 6]);
+  rope_waves<L, INTER, PAST>(g, g.k.heads, blockIdx.x, gridDim.x, table[threadIdx.x >> 6]);
 }
 
 constexpr int kMaxRun = 16;
@@ -325,7 +325,7 @@ void store_kernel(RopeArgs g, CacheArgs k) {
 }
 
 // The first workgroups store, the others norm and turn q.
-template <int L, bool INTER>
+template <int L, bool INTER, bool PAST>
 __global__ __launch_bounds__(kQkvThreads)
 void rope_store_kernel(RopeArgs g, CacheArgs k, int runs) {
   __shared__ float2 table[kQkvWaves][FP8BL_MAX_PAIRS];
@@ -333,7 +333,7 @@ void rope_store_kernel(RopeArgs g, CacheArgs k, int runs) {
     store_run<L, INTER, true>(g, k, blockIdx.x);
     return;
   }
-  rope_waves<L, INTER>(g, 0, (int)blockIdx.x - runs, (int)gridDim.x - runs, table[threadIdx.x >> 6]);
+  rope_waves<L, INTER, PAST>(g, 0, (int)blockIdx.x - runs, (int)gridDim.x - runs, table[threadIdx.x >> 6]);
 }
 
 // Waves to a token: as many as there are steps of 64 / L heads where few
@@ -371,16 +371,20 @@ uint32_t blocks_of(int64_t tokens, int parts) {
 struct Rope {
   const fp8bl_qkv& a;
   hipStream_t stream;
-  template <int L>
-  hipError_t run() {
+  template <int L, bool INTER>
+  hipError_t launch() {
     RopeArgs g = rope_args(a);
     g.parts = parts_of(a.tokens, steps_of(a.q_heads, L) + steps_of(a.k_heads, L));
     const dim3 grid(blocks_of(a.tokens, g.parts)), block(kQkvThreads);
-    if (a.interleaved)
-      hipLaunchKernelGGL((rope_kernel<L, true>), grid, block, 0, stream, g);
+    if (past_caches(a.tokens * (a.q_heads + a.k_heads) * a.head_dim * 4))
+      hipLaunchKernelGGL((rope_kernel<L, INTER, true>), grid, block, 0, stream, g);
     else
-      hipLaunchKernelGGL((rope_kernel<L, false>), grid, block, 0, stream, g);
+      hipLaunchKernelGGL((rope_kernel<L, INTER, false>), grid, block, 0, stream, g);
     return hipGetLastError();
+  }
+  template <int L>
+  hipError_t run() {
+    return a.interleaved ? launch<L, true>() : launch<L, false>();
   }
 };
 
@@ -404,18 +408,22 @@ struct Store {
 struct RopeStore {
   const fp8bl_qkv& a;
   hipStream_t stream;
-  template <int L>
-  hipError_t run() {
+  template <int L, bool INTER>
+  hipError_t launch() {
     RopeArgs g = rope_args(a);
     const CacheArgs k = cache_args(a);
     const int runs = a.k_heads > 0 ? (int)((a.tokens + k.run - 1) / k.run) : 0;
     g.parts = parts_of(a.tokens, steps_of(a.q_heads, L));
     const dim3 grid(runs + (a.q_heads > 0 ? blocks_of(a.tokens, g.parts) : 0)), block(kQkvThreads);
-    if (a.interleaved)
-      hipLaunchKernelGGL((rope_store_kernel<L, true>), grid, block, 0, stream, g, k, runs);
+    if (past_caches(a.tokens * a.q_heads * a.head_dim * 4))
+      hipLaunchKernelGGL((rope_store_kernel<L, INTER, true>), grid, block, 0, stream, g, k, runs);
     else
-      hipLaunchKernelGGL((rope_store_kernel<L, false>), grid, block, 0, stream, g, k, runs);
+      hipLaunchKernelGGL((rope_store_kernel<L, INTER, false>), grid, block, 0, stream, g, k, runs);
     return hipGetLastError();
+  }
+  template <int L>
+  hipError_t run() {
+    return a.interleaved ? launch<L, true>() : launch<L, false>();
   }
 };
 

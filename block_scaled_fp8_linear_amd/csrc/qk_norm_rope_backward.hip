@@ -20,7 +20,7 @@ struct BackArgs {
   float* part;                     // [workgroups][2][dim]
 };
 
-template <int L, bool INTER>
+template <int L, bool INTER, bool PAST>
 __device__ __forceinline__ void back_heads(const BackArgs& g, int which, const uint16_t* weight, int token, int first,
                                            int last, int lane, const Chunk& ch, const float (&c)[8],
                                            const float (&s)[8], float (&dw)[8]) {
@@ -41,8 +41,8 @@ __device__ __forceinline__ void back_heads(const BackArgs& g, int which, const u
     for (int j = 0; j < kAhead; ++j) {
       const int h = h0 + j * G + lane / L;
       const bool live = mine && h < last;
-      xr[j] = live ? *reinterpret_cast<const u32x4*>(xp + h * xv.hs) : u32x4{0, 0, 0, 0};
-      yr[j] = live ? *reinterpret_cast<const u32x4*>(yp + h * yv.hs) : u32x4{0, 0, 0, 0};
+      xr[j] = live ? get8<PAST>(xp + h * xv.hs) : u32x4{0, 0, 0, 0};
+      yr[j] = live ? get8<PAST>(yp + h * yv.hs) : u32x4{0, 0, 0, 0};
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
@@ -68,12 +68,12 @@ __device__ __forceinline__ void back_heads(const BackArgs& g, int which, const u
         dw[i] = __builtin_fmaf(y[i] * rl, x[i], dw[i]);
         o[i] = r * __builtin_fmaf(-x[i], along, y[i] * w[i]);
       }
-      if (live) *reinterpret_cast<u32x4*>(op + h * ov.hs) = pack8(o);
+      if (live) put8<PAST>(op + h * ov.hs, pack8(o));
     }
   }
 }
 
-template <int L, bool INTER>
+template <int L, bool INTER, bool PAST>
 __global__ __launch_bounds__(kQkvThreads)
 void back_kernel(BackArgs g) {
   __shared__ float2 tables[kQkvWaves][FP8BL_MAX_PAIRS];
@@ -93,10 +93,10 @@ void back_kernel(BackArgs g) {
     turn_factors<INTER>(tables[wave], ch, c, s);
     const int s0 = (sq + sk) * part / g.parts, s1 = (sq + sk) * (part + 1) / g.parts;
     if (s0 < sq)
-      back_heads<L, INTER>(g, 0, g.t.wq, token, s0 * G, min(min(s1, sq) * G, g.x[0].heads), lane, ch, c, s, dwq);
+      back_heads<L, INTER, PAST>(g, 0, g.t.wq, token, s0 * G, min(min(s1, sq) * G, g.x[0].heads), lane, ch, c, s, dwq);
     if (s1 > sq)
-      back_heads<L, INTER>(g, 1, g.t.wk, token, max(s0 - sq, 0) * G, min((s1 - sq) * G, g.x[1].heads), lane, ch, c, s,
-                           dwk);
+      back_heads<L, INTER, PAST>(g, 1, g.t.wk, token, max(s0 - sq, 0) * G, min((s1 - sq) * G, g.x[1].heads), lane, ch,
+                                 c, s, dwk);
   }
   // over the heads a wave holds side by side, then over the waves
 #pragma unroll
@@ -122,14 +122,23 @@ void back_kernel(BackArgs g) {
 }
 
 // Sum over the workgroups: 16 columns a workgroup, 64 rows of the partials at
-// a time.
+// a time, kRows loads of a thread on their way.
 __global__ __launch_bounds__(1024)
 void back_sum_kernel(const float* __restrict__ part, int blocks, int dim, float* dwq, float* dwk) {
   __shared__ float sums[64][17];
   const int col = threadIdx.x & 15, row = threadIdx.x >> 4, e = blockIdx.x * 16 + col;
+  constexpr int kRows = 8;
   float t = 0.0f;
-  if (e < 2 * dim)
-    for (int b = row; b < blocks; b += 64) t += part[(size_t)b * 2 * dim + e];
+  for (int b0 = row; b0 < blocks; b0 += 64 * kRows) {
+    float v[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int b = b0 + 64 * i;
+      v[i] = b < blocks && e < 2 * dim ? part[(size_t)b * 2 * dim + e] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) t += v[i];
+  }
   sums[row][col] = t;
   __syncthreads();
   for (int half = 32; half >= 1; half /= 2) {
@@ -162,8 +171,8 @@ struct Back {
   const fp8bl_qkv& a;
   float* part;
   hipStream_t stream;
-  template <int L>
-  hipError_t run() {
+  template <int L, bool INTER>
+  hipError_t launch() {
     BackArgs g{{head_view(a.q, a.q_heads), head_view(a.k, a.k_heads)},
                {head_view(a.dq, a.q_heads), head_view(a.dk, a.k_heads)},
                {head_view(a.q_out, a.q_heads), head_view(a.k_out, a.k_heads)},
@@ -171,15 +180,19 @@ struct Back {
                back_parts(a.tokens, a.q_heads, a.k_heads, a.head_dim),
                part};
     const int blocks = (int)back_blocks(a.tokens, g.parts);
-    if (a.interleaved)
-      hipLaunchKernelGGL((back_kernel<L, true>), dim3(blocks), dim3(kQkvThreads), 0, stream, g);
+    if (past_caches(a.tokens * (a.q_heads + a.k_heads) * a.head_dim * 6))
+      hipLaunchKernelGGL((back_kernel<L, INTER, true>), dim3(blocks), dim3(kQkvThreads), 0, stream, g);
     else
-      hipLaunchKernelGGL((back_kernel<L, false>), dim3(blocks), dim3(kQkvThreads), 0, stream, g);
+      hipLaunchKernelGGL((back_kernel<L, INTER, false>), dim3(blocks), dim3(kQkvThreads), 0, stream, g);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || (a.dq_weight == nullptr && a.dk_weight == nullptr)) return e;
     hipLaunchKernelGGL(back_sum_kernel, dim3((uint32_t)((2 * a.head_dim + 15) / 16)), dim3(1024), 0, stream, part,
                        blocks, (int)a.head_dim, a.dq_weight, a.dk_weight);
     return hipGetLastError();
+  }
+  template <int L>
+  hipError_t run() {
+    return a.interleaved ? launch<L, true>() : launch<L, false>();
   }
 };
 

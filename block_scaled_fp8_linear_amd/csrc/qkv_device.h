@@ -44,6 +44,30 @@ inline TurnArgs turn_args(const fp8bl_qkv& a) {
   return t;
 }
 
+// Whether a call goes past the caches: what it reads and writes is more than
+// the 256 MB of the last-level cache, so nothing of it would be found there by the
+// next kernel. Norm and rotation of 16384 tokens of 80 heads of 128 take 120 us so
+// and 126 through the caches (185 and 188 with a copy of the results behind
+// them), of 2048 tokens 18.5 and 20.5 (28.3 and 25.9); their backward pass at
+// 16384 tokens 185 and 198 (312 and 326), at 1024 20.3 and 18.8 (31.7 and 29.0);
+// rows of eight heads of 128 read back 142 and 159 at 131072 tokens (342 and 357),
+// 7.7 and 6.1 at 4096 (17.3 and 13.4).
+inline bool past_caches(int64_t bytes) { return bytes > (int64_t)256 << 20; }
+
+// Eight elements, past the caches or through them.
+template <bool PAST>
+__device__ __forceinline__ u32x4 get8(const uint16_t* p) {
+  if constexpr (PAST) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  return *reinterpret_cast<const u32x4*>(p);
+}
+template <bool PAST>
+__device__ __forceinline__ void put8(uint16_t* p, u32x4 v) {
+  if constexpr (PAST)
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+  else
+    *reinterpret_cast<u32x4*>(p) = v;
+}
+
 inline int head_lanes(int64_t dim) {
   int l = 2;
   while (8 * l < dim) l *= 2;

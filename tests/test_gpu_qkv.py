@@ -461,6 +461,45 @@ def test_heads_past_32_bit_offsets():
     assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d", [16, 24, 64, 120, 256])
+def test_sizes_past_the_caches(d, interleaved):
+    """Calls that move more than 256 MB go past the caches: token by token the bits of
+    the same call on a quarter of the tokens."""
+    say("past the caches", d, interleaved)
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    t = 40000
+    hq, hk = 2 ** 26 // (t * d) + 1, 3
+    q, dq = (torch.randn(t, hq, d, generator=gen, device="cuda").to(BF) for _ in range(2))
+    k, v, dk = (torch.randn(t, hk, d, generator=gen, device="cuda").to(BF) for _ in range(3))
+    w = [(1 + 0.3 * torch.randn(d, generator=gen, device="cuda")).to(BF) for _ in range(2)]
+    positions = torch.randint(0, 100000, (t,), generator=gen, device="cuda", dtype=torch.int32)
+    freq = torch.rand(8, generator=gen, device="cuda")
+    slots = torch.randperm(t, generator=gen, device="cuda").to(torch.int32)
+    how = {"interleaved": interleaved}
+
+    def calls(a, b, store):
+        part = [x[a:b] for x in (q, k, v, dq, dk, positions, slots)]
+        table = (*w, part[5], freq)
+        turned = F.fp8_qk_norm_rope(part[0], part[1], *table, **how)
+        grads = F.fp8_qk_norm_rope_backward(part[3], part[4], part[0], part[1], *table, **how)[:2]
+        stored = F.fp8_qk_norm_rope_store(part[0], part[1], part[2], *table, part[6], *store, **how)
+        return (*turned, *grads, stored)
+
+    whole, parts = cache(t, hk, d), cache(t, hk, d)
+    got = calls(0, t, whole)
+    for a in range(0, t, t // 4):
+        for x, y in zip(got, calls(a, a + t // 4, parts)):
+            assert torch.equal(x[a:a + t // 4].view(torch.int16), y.view(torch.int16))
+    assert all(torch.equal(x, y) for x, y in zip(whole, parts))
+    # a long context: each row of the cache many times
+    again = -(-2 ** 28 // (6 * t * hk * d)) + 1
+    out = F.fp8_kv_load(*whole, slots.repeat(again))
+    once = F.fp8_kv_load(*whole, slots)
+    for x, y in zip(out, once):
+        assert all(torch.equal(x[i * t:(i + 1) * t], y) for i in range(again))
+
+
 def test_writes_only_its_workspace():
     c = Case(515, 8, 2, 128, None, 3, False)
     ref = F.fp8_qk_norm_rope_backward(c.dq, c.dk, c.q, c.k, *c.table, **c.how)
