@@ -23,6 +23,10 @@
 // l / 32, A (the weight) and B (X) alike; it holds the sums of X row l % 32 and
 // weight rows 8 g + 4 (l / 32) + i, g and i from 0 to 3.
 //
+// MI355X: 8192 x 8192 x 8192 463 us (2.37 POP/s), 8192 x 12288 x 4096 370 (2.2),
+// 512 x 5120 x 5120 25, 333 x 4300 x 1168 8.4, the matrix cores busy about half the
+// time in the first two.
+//
 // Rows past M or N and K past the end read as zero: buffer descriptors that
 // cover the valid rows, and offsets out of range for chunks behind K.
 #include "fp8bl_device.h"

@@ -4,7 +4,9 @@ in a training step, with its gradients; and sizes drawn over the whole range."""
 
 from __future__ import annotations
 
+import os
 import random
+import re
 
 import pytest
 
@@ -136,6 +138,48 @@ def test_training_step():
         LR.check_linear_act_backward(dz, None, q8, s8, "none", x.grad, dz, None, "projection")
     with pytest.raises(RuntimeError, match="autograd"):
         F.fp8_qk_norm_rope(q, k, qw, kw, positions, freq, axes)
+
+
+def printed(name):
+    """What the README's Python block that defines `name` defines."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    blocks = re.findall(r"```python\n(.*?)```", open(os.path.join(root, "README.md")).read(), flags=re.S)
+    scope = {"torch": torch, "F": F}
+    exec(next(b for b in blocks if re.search(rf"(def|class) {name}\b", b)), scope)
+    return scope
+
+
+def test_printed_serving_example():
+    gen, w, weights, freq, axes = block(2)
+    scope = printed("attention_inputs")
+    x = torch.randn(50, WIDTH, generator=gen).to(BF).cuda()
+    wq, ws = F.int8_row_quantize(w)
+    cache = [torch.zeros(64, HK, D, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    cache += [torch.ones(64, HK, device="cuda") for _ in range(2)]
+    slots = torch.randperm(64, generator=gen)[:50].to(torch.int32).cuda()
+    positions = torch.randint(0, 99, (3, 50), generator=gen, dtype=torch.int32).cuda()
+    out = scope["attention_inputs"](x, wq, ws, *weights, positions, freq, axes, slots, cache, (HQ, HK), D)
+    q, k, v = split(I.linear(*I.quantize(x), wq, ws))
+    assert R.outside(out, *R.forward(q, weights[0], positions, freq, axes, 1e-6, False)) <= 1
+    _, loaded = scope["context"](slots, cache)
+    codes, scale = R.stored(v)
+    assert torch.equal(loaded, (codes * scale.double()[..., None]).float().to(BF))
+
+
+def test_printed_training_example():
+    """Gradients through the printed function, from an expanded output gradient too."""
+    gen, _, weights, freq, axes = block(3)
+    turn = printed("QkNormRope")["QkNormRope"].apply
+    q, k = (torch.randn(40, h, D, generator=gen).to(BF).cuda().requires_grad_(True) for h in (HQ, HK))
+    weights = [x.requires_grad_(True) for x in weights]
+    positions = torch.randint(0, 99, (3, 40), generator=gen, dtype=torch.int32).cuda()
+    out = turn(q, k, *weights, positions, freq, axes)
+    (out[0].sum() + out[1].float().square().sum()).backward()
+    for x, w, dy in ((q, weights[0], torch.ones_like(q)), (k, weights[1], (2 * out[1].float()).to(BF))):
+        with torch.no_grad():
+            dx, bound, dw, dw_bound = R.backward(dy, x, w, positions, freq, axes, 1e-6, False, 1)
+            assert R.outside(x.grad, dx, bound) <= 1
+            assert bool(((w.grad.double() - dw).abs() <= 2.0 ** -8 * 1.01 * dw.abs() + 1.01 * dw_bound).all())
 
 
 def _log(rng, lo, hi):
