@@ -13,7 +13,10 @@
 // Stages of (TM + TN) x 128 bytes are filled by loads that write LDS themselves,
 // S steps ahead. The last operands of a stage are read during the step's third
 // slice, so one barrier a step, before the fourth, tells both that the next
-// stage has landed and that this one can be refilled.
+// stage has landed and that this one can be refilled: half of its loads are issued
+// in the fourth slice, half in the next step's first, one behind a product (all in
+// the fourth take 8192 x 8192 x 8192 from 451 to 480 us, 2048 x 5120 x 5120 from 59
+// to 66; thirds in three slices 473).
 //
 // LDS rows are 128 bytes with the 16-byte chunks permuted by
 // (row & 7) ^ ((row >> 3) & 1): 16 consecutive rows of one chunk lie in 16
@@ -71,7 +74,7 @@ struct Tile {
   static constexpr int kStage = (kTM + kTN) * kBK;
   static constexpr int kRows = 1024 / kBK;                        // of a load
   static constexpr int kXLoads = kTM / 4 / kRows, kWLoads = kTN / 4 / kRows;    // for each wave and step
-  static constexpr int kLoads = kXLoads + kWLoads;
+  static constexpr int kLoads = kXLoads + kWLoads, kHalf = kLoads / 2;
   static constexpr int kVectors = (2 * kTN + kTM) * 4;            // of the epilogue
   static constexpr int kRowsOut = WN >= 2 ? 4 * 32 * 128 : 0;     // and its rows
   static constexpr int kLds = S * kStage + kVectors + kRowsOut;
@@ -178,7 +181,7 @@ void gemm_int8_kernel(GemmArgs g) {
     asm volatile("" ::: "memory");
   };
 
-  // Prologue: the first S steps; wait for the first of them.
+  // Prologue: the first S steps, half of the last; wait for the first of them.
   set_load_unit(unit_of(0));
   int lci = 0, lkt = 0;                // the next step to load: of unit lci
   auto next_load = [&] {
@@ -190,10 +193,10 @@ void gemm_int8_kernel(GemmArgs g) {
 #pragma unroll
   for (int a = 0; a < S; ++a) {
 #pragma unroll
-    for (int i = 0; i < T::kLoads; ++i) issue(a * kStage, lkt, i);
-    next_load();
+    for (int i = 0; i < (a == S - 1 ? T::kHalf : T::kLoads); ++i) issue(a * kStage, lkt, i);
+    if (a < S - 1) next_load();
   }
-  __builtin_amdgcn_s_waitcnt(vm_wait((S - 1) * T::kLoads));
+  __builtin_amdgcn_s_waitcnt(vm_wait((S - 2) * T::kLoads + T::kHalf));
   wg_barrier();
 
   i32x4 xf[2][WM], wf[2][WN];
@@ -216,6 +219,7 @@ void gemm_int8_kernel(GemmArgs g) {
       const int sb = stage * kStage;
       const int nstage = stage + 1 == S ? 0 : stage + 1;
       const int sbn = nstage * kStage;
+      const int psb = (stage == 0 ? S - 1 : stage - 1) * kStage;
       const bool last = kt == g.steps_per_unit - 1;
       // the epilogue's vectors, one element a thread: on their way during the
       // unit's last step
@@ -232,11 +236,11 @@ void gemm_int8_kernel(GemmArgs g) {
           // this wave's reads of the stage have returned and its loads of the
           // next stage have landed; behind the barrier so have all waves'
           __builtin_amdgcn_s_waitcnt(kLgkmWait0);
-          // (In a unit's first step the last unit's stores are the newest
-          // operations: where all of them were issued, those of a whole tile, they
-          // may take until the second step.)
+          // (In a unit's first step the last unit's stores are newer than the next
+          // stage, with S above 2: where all of them were issued, those of a whole
+          // tile, they may take until the second step.)
           if (kt == 0 && ci > 0) {
-            if (stored)
+            if (S > 2 && stored)
               __builtin_amdgcn_s_waitcnt(vm_wait((S - 2) * T::kLoads + T::kStores));
             else
               __builtin_amdgcn_s_waitcnt(vm_wait(0));
@@ -261,26 +265,30 @@ void gemm_int8_kernel(GemmArgs g) {
         for (int b = 0; b < WM; ++b) xf[nxt][b] = read_x(rb, (s + 1) % kSlices, b);
         if (s == kSlices - 1) {
 #pragma unroll
-          for (int i = 0; i < T::kLoads; ++i) issue(sb, lkt, i);
+          for (int i = 0; i < T::kHalf; ++i) issue(sb, lkt, i);
+        }
+        if (s == 0) {                            // the other half, into the stage before
+#pragma unroll
+          for (int i = T::kHalf; i < T::kLoads; ++i) issue(psb, lkt, i);
         }
 #pragma unroll
         for (int n = 0; n < WN; ++n)
 #pragma unroll
           for (int m = 0; m < WM; ++m)
             acc[n][m] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[cur][n], xf[cur][m], acc[n][m], 0, 0, 0);
-        // reads behind the first products, in the last slice loads behind the others
+        // reads behind the first products, loads behind the others
         constexpr int kProducts = WM * WN, kReads = WM + WN, kEvery = kReads > kProducts / 2 ? 2 * kReads / kProducts : 1;
         constexpr int kFirst = kReads / kEvery, kRest = kProducts > kFirst ? kProducts - kFirst : 1;
 #pragma unroll
         for (int i = 0; i < kProducts; ++i) {
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                     // MFMA
           if (i < kFirst) __builtin_amdgcn_sched_group_barrier(0x100, kEvery, 0);                // DS read
-          if (s == kSlices - 1 && i >= kFirst)
-            __builtin_amdgcn_sched_group_barrier(0x020, (T::kLoads + kRest - 1) / kRest, 0);     // VMEM
+          if ((s == kSlices - 1 || s == 0) && i >= kFirst)
+            __builtin_amdgcn_sched_group_barrier(0x020, (T::kHalf + kRest - 1) / kRest, 0);      // VMEM
         }
         __builtin_amdgcn_sched_barrier(0);
+        if (s == 0) next_load();
       }
-      next_load();
       stage = nstage;
     }
 
