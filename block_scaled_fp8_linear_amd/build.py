@@ -95,7 +95,7 @@ def _link_binding(obj: str, verbose: bool) -> None:
     torch_lib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
     tmp = BINDING_PATH + ".tmp"
     _run(["g++", "-shared", obj, "-o", tmp, "-L", PKG_DIR, "-l:libfp8bl.so", "-L", torch_lib, "-lc10", "-ltorch_cpu",
-          "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "link of _tensors.so", verbose)
+          "-ltorch_hip", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "link of _tensors.so", verbose)
     os.replace(tmp, BINDING_PATH)
 
 

@@ -182,6 +182,30 @@ def test_printed_training_example():
             assert bool(((w.grad.double() - dw).abs() <= 2.0 ** -8 * 1.01 * dw.abs() + 1.01 * dw_bound).all())
 
 
+def test_outputs_are_ordinary_tensors():
+    """What the functions allocate: contiguous, without a gradient, usable by recorded
+    operations, inference tensors in inference mode, from the pool of a capture."""
+    x = torch.randn(4, 64, device="cuda").to(BF)
+    wq, ws = F.int8_row_quantize(torch.randn(32, 64, device="cuda"))
+    y = F.int8_linear_bf16(x, wq, ws)
+    assert wq.dtype == torch.int8 and ws.dtype == torch.float32 and y.dtype == BF and y.shape == (4, 32)
+    assert y.is_contiguous() and not y.requires_grad and not y.is_inference() and y.device == x.device
+    leaf = torch.ones_like(y).requires_grad_(True)
+    (leaf * y).sum().backward()
+    assert torch.equal(leaf.grad, y)
+    with torch.inference_mode():
+        z = F.int8_linear_bf16(x, wq, ws)
+        assert z.is_inference() and torch.equal(z, y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        z = F.int8_linear_bf16(x, wq, ws)
+    for _ in range(3):
+        x.mul_(0.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(z, F.int8_linear_bf16(x, wq, ws))
+
+
 def _log(rng, lo, hi):
     return int(round(lo * (hi / lo) ** rng.random()))
 
