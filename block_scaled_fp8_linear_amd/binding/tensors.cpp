@@ -616,7 +616,7 @@ PyMethodDef kFunctions[] = {
              "                       v_cache, k_scale, v_scale, axes=None, eps=1e-6, interleaved=False,\n"
              "                       q_out=None)\n--\n\n"
              "fp8_qk_norm_rope and fp8_kv_store in one pass -> q_out: the cache receives v and the\n"
-             "normed and turned k, quantized from fp32 (storing a returned k rounds it to bf16\n"
+             "normed and turned k, quantized from fp64 (storing a returned k rounds it to bf16\n"
              "first)."),
     {"configure", configure, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr}};

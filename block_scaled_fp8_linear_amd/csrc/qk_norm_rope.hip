@@ -16,7 +16,10 @@
 // the same slot, the earlier one is not stored: the workgroup compares its run
 // with every later slot first, while its heads are on their way. 8192 tokens of
 // 8 heads of 128 take 16.9 us (3.0 TB/s), 14.5 without the comparison; the fused
-// call for 16 tokens of 64 and 8 heads 4.8 us.
+// call for 16 tokens of 64 and 8 heads 4.8 us. Its keys are normed, turned and
+// divided in fp64: in fp32 one code in 200000 was its neighbour's, where the value
+// lies next to the border between them. That costs 8192 tokens 79 us for 75, 16 tokens
+// nothing.
 #include "fp8bl_ops.h"
 #include "qkv_device.h"
 
@@ -152,10 +155,10 @@ __device__ __forceinline__ void rope_unit(const RopeArgs& g, int k_heads, int un
   float c[8], s[8];
   turn_factors<INTER>(table, ch, c, s);
   const float inv_dim = 1.0f / (float)g.t.dim;
-  if (s0 < sq) rope_heads<L, INTER, PAST>(q, inv_dim, g.t.eps, ch, c, s);
+  if (s0 < sq) rope_heads<L, INTER, PAST>(q, inv_dim, (float)g.t.eps, ch, c, s);
   if (s1 > sq) {
     if (s0 < sq) k.load(k.first);
-    rope_heads<L, INTER, PAST>(k, inv_dim, g.t.eps, ch, c, s);
+    rope_heads<L, INTER, PAST>(k, inv_dim, (float)g.t.eps, ch, c, s);
   }
 }
 
@@ -239,7 +242,7 @@ __device__ __forceinline__ uint32_t later_ones(const int32_t* __restrict__ slots
 template <int L, bool INTER, bool FUSED>
 __device__ __forceinline__ void store_run(const RopeArgs& g, const CacheArgs& k, int run_index) {
   __shared__ uint32_t found[kQkvWaves];
-  __shared__ float2 tables[FUSED ? kMaxRun : 1][FUSED ? FP8BL_MAX_PAIRS : 1];
+  __shared__ double2 tables[FUSED ? kMaxRun : 1][FUSED ? FP8BL_MAX_PAIRS : 1];
   constexpr int G = 64 / L, kBatch = 2;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -273,7 +276,8 @@ __device__ __forceinline__ void store_run(const RopeArgs& g, const CacheArgs& k,
   if (lane == 0) found[wave] = mine_found;
   if constexpr (FUSED)
     for (int p = tid; p < run * g.t.pairs; p += kQkvThreads)
-      tables[p / g.t.pairs][p % g.t.pairs] = turn_of(g.t, g.t.axis[p % g.t.pairs], p % g.t.pairs, i0 + p / g.t.pairs);
+      tables[p / g.t.pairs][p % g.t.pairs] =
+          turn64<true>(g.t, g.t.axis[p % g.t.pairs], p % g.t.pairs, i0 + p / g.t.pairs);
   __syncthreads();
   uint32_t dead = found[0];
 #pragma unroll
@@ -287,7 +291,6 @@ __device__ __forceinline__ void store_run(const RopeArgs& g, const CacheArgs& k,
     unpack8(wr, w);
     unpack8(other_members<INTER>(wr, ch.partner), wo);
   }
-  const float inv_dim = 1.0f / (float)dim;
   for (int u0 = wave; u0 < items; u0 += kBatch * kQkvWaves) {
     if (u0 != wave) load(u0);
 #pragma unroll
@@ -297,25 +300,34 @@ __device__ __forceinline__ void store_run(const RopeArgs& g, const CacheArgs& k,
       const Item t = item(u);
       const int slot = __builtin_amdgcn_readlane(run_slots, t.r);
       if (slot < 0 || slot >= k.rows || (dead >> t.r & 1)) continue;
-      float x[8];
+      float x[8], sc;
       unpack8(raw[i], x);
       if (FUSED && !t.of_v) {
-        float o[8], c[8], s[8], sq = 0.0f;
+        float o[8];
+        double c[8], s[8], v[8], sq = 0.0, amax = 0.0;
         unpack8(other_members<INTER>(raw[i], ch.partner), o);
         turn_factors<INTER>(tables[t.r], ch, c, s);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sq = __builtin_fmaf(x[e], x[e], sq);
-        const float n = rsqrtf(head_sum<L>(sq) * inv_dim + g.t.eps);
+        for (int e = 0; e < 8; ++e) sq = fma((double)x[e], (double)x[e], sq);
+        const double n = 1.0 / sqrt(head_sum<L>(sq) / dim + g.t.eps);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = n * __builtin_fmaf(x[e], w[e] * c[e], o[e] * (wo[e] * s[e]));
+        for (int e = 0; e < 8; ++e) {
+          v[e] = n * fma((double)(x[e] * w[e]), c[e], (double)(o[e] * wo[e]) * s[e]);     // (16-bit products: exact)
+          amax = fmax(amax, fabs(v[e]));
+        }
+        sc = (float)(head_max<L>(amax) / 448.0);
+        if (sc == 0.0f) sc = 1.0f;
+        const double inv = 1.0 / (double)sc;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = (float)(v[e] * inv);
+      } else {
+        float amax = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+        sc = __fdiv_rn(head_max<L>(amax), 448.0f);
+        if (sc == 0.0f) sc = 1.0f;
+        quotients(x, sc);
       }
-      float amax = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
-      amax = head_max<L>(amax);
-      float sc = __fdiv_rn(amax, 448.0f);
-      if (sc == 0.0f) sc = 1.0f;
-      quotients(x, sc);
       if (mine && t.h < heads) {
         const size_t row = (size_t)slot * heads + t.h;
         const u32x2 codes = {e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7])};

@@ -53,7 +53,7 @@ __device__ __forceinline__ void back_heads(const BackArgs& g, int which, const u
       sq = __builtin_fmaf(x[i], x[i], sq);
       ux = __builtin_fmaf(y[i] * w[i], x[i], ux);
     }
-    const float r = rsqrtf(head_sum<L>(sq) * inv_dim + g.t.eps);
+    const float r = rsqrtf(head_sum<L>(sq) * inv_dim + (float)g.t.eps);
     const float along = head_sum<L>(ux) * inv_dim * r * r;
     // a head that is not there leaves zeros in the sums, whatever r is
     const float rl = live ? r : 0.0f;

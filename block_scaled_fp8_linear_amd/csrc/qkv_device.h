@@ -33,13 +33,13 @@ struct TurnArgs {
   const int32_t* positions;
   const float* inv_freq;
   int tokens, dim, pairs;
-  float eps;
+  double eps;
   uint8_t axis[FP8BL_MAX_PAIRS];
 };
 
 inline TurnArgs turn_args(const fp8bl_qkv& a) {
   TurnArgs t{a.q_weight, a.k_weight, a.positions, a.inv_freq, (int)a.tokens, (int)a.head_dim, (int)a.pairs,
-             (float)a.eps, {}};
+             a.eps, {}};
   for (int i = 0; i < (int)a.pairs; ++i) t.axis[i] = a.axis[i];
   return t;
 }
@@ -90,11 +90,16 @@ template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
 }
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  return __hiloint2double(__builtin_amdgcn_mov_dpp(__double2hiint(v), CTRL, 0xF, 0xF, true),
+                          __builtin_amdgcn_mov_dpp(__double2loint(v), CTRL, 0xF, 0xF, true));
+}
 constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E, kHalfMirror = 0x141, kRowRor8 = 0x128;
 
 // Sum (maximum) over the L lanes of a head, the same bits in each of them.
-template <int L, typename Op>
-__device__ __forceinline__ float head_reduce(float v, Op op) {
+template <int L, typename T, typename Op>
+__device__ __forceinline__ T head_reduce(T v, Op op) {
   v = op(v, dpp<kQuadXor1>(v));
   if constexpr (L >= 4) v = op(v, dpp<kQuadXor2>(v));
   if constexpr (L >= 8) v = op(v, dpp<kHalfMirror>(v));
@@ -102,13 +107,13 @@ __device__ __forceinline__ float head_reduce(float v, Op op) {
   if constexpr (L >= 32) v = op(v, __shfl_xor(v, 16, 64));
   return v;
 }
-template <int L>
-__device__ __forceinline__ float head_sum(float v) {
-  return head_reduce<L>(v, [](float a, float b) { return a + b; });
+template <int L, typename T>
+__device__ __forceinline__ T head_sum(T v) {
+  return head_reduce<L>(v, [](T a, T b) { return a + b; });
 }
-template <int L>
-__device__ __forceinline__ float head_max(float v) {
-  return head_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
+template <int L, typename T>
+__device__ __forceinline__ T head_max(T v) {
+  return head_reduce<L>(v, [](T a, T b) { return a > b ? a : b; });
 }
 
 __device__ __forceinline__ void unpack8(u32x4 a, float (&v)[8]) {
@@ -124,19 +129,26 @@ __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
 
 // cos and sin of pair p of a token. The angle position * inv_freq reaches 2^31
 // radians: it is taken in fp64 as a number of turns. What is left of it behind
-// whole quarter turns, at most pi / 4, goes through the two power series to
-// a^11 and a^10 (off by 2e-10), so that both come out rounded once to fp32.
-__device__ __forceinline__ float2 turn_of(const TurnArgs& t, int axis, int p, int token) {
+// whole quarter turns, at most pi / 4, goes through the two power series: to a^11
+// and a^10 (off by 2e-10), so that both come out rounded once to fp32, or to a^13 and
+// a^12 where they stay fp64 (off by 4e-13).
+template <bool FP64>
+__device__ __forceinline__ double2 turn64(const TurnArgs& t, int axis, int p, int token) {
   const double turns = (double)t.positions[(size_t)axis * t.tokens + token] *
                        ((double)t.inv_freq[p] * 0.15915494309189533577);
   const double quarters = rint(4.0 * turns);
   const double a = (turns - 0.25 * quarters) * 6.28318530717958647693, z = a * a;
-  const double s = a * fma(z, fma(z, fma(z, fma(z, fma(z, -1.0 / 39916800, 1.0 / 362880), -1.0 / 5040), 1.0 / 120),
-                               -1.0 / 6), 1.0);
-  const double c = fma(z, fma(z, fma(z, fma(z, fma(z, -1.0 / 3628800, 1.0 / 40320), -1.0 / 720), 1.0 / 24), -0.5), 1.0);
+  const double s11 = FP64 ? fma(z, 1.0 / 6227020800, -1.0 / 39916800) : -1.0 / 39916800;
+  const double c10 = FP64 ? fma(z, 1.0 / 479001600, -1.0 / 3628800) : -1.0 / 3628800;
+  const double s = a * fma(z, fma(z, fma(z, fma(z, fma(z, s11, 1.0 / 362880), -1.0 / 5040), 1.0 / 120), -1.0 / 6), 1.0);
+  const double c = fma(z, fma(z, fma(z, fma(z, fma(z, c10, 1.0 / 40320), -1.0 / 720), 1.0 / 24), -0.5), 1.0);
   const int q = (int)(int64_t)quarters & 3;
-  const float fs = (float)(q & 1 ? c : s), fc = (float)(q & 1 ? s : c);
-  return float2{q == 1 || q == 2 ? -fc : fc, q >= 2 ? -fs : fs};
+  const double fs = q & 1 ? c : s, fc = q & 1 ? s : c;
+  return double2{q == 1 || q == 2 ? -fc : fc, q >= 2 ? -fs : fs};
+}
+__device__ __forceinline__ float2 turn_of(const TurnArgs& t, int axis, int p, int token) {
+  const double2 v = turn64<false>(t, axis, p, token);
+  return float2{(float)v.x, (float)v.y};
 }
 
 // Where the lane's chunk c of a head stands: in the first or second members of
@@ -157,19 +169,19 @@ __device__ __forceinline__ Chunk chunk_of(int lane, int c, int pairs) {
 
 // What the lane's elements are multiplied with in a turn, from the token's
 // table of cosines and sines: out_i = x_i c_i + (other member)_i s_i.
-template <bool INTER>
-__device__ __forceinline__ void turn_factors(const float2* table, const Chunk& ch, float (&c)[8], float (&s)[8]) {
+template <bool INTER, typename T2, typename T>
+__device__ __forceinline__ void turn_factors(const T2* table, const Chunk& ch, T (&c)[8], T (&s)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if (ch.sign == 0.0f) {
-      c[i] = 1.0f;
-      s[i] = 0.0f;
+      c[i] = 1;
+      s[i] = 0;
     } else if constexpr (INTER) {
-      const float2 t = table[ch.pair + i / 2];
+      const T2 t = table[ch.pair + i / 2];
       c[i] = t.x;
       s[i] = i & 1 ? t.y : -t.y;
     } else {
-      const float2 t = table[ch.pair + i];
+      const T2 t = table[ch.pair + i];
       c[i] = t.x;
       s[i] = ch.sign * t.y;
     }

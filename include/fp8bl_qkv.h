@@ -117,7 +117,8 @@ int fp8_kv_store(const fp8bl_qkv* args, hipStream_t stream);
 int fp8_kv_load(const fp8bl_qkv* args, hipStream_t stream);
 
 /* fp8_qk_norm_rope and fp8_kv_store in one pass: q_out as there, and the cache
- * receives v and the normed and turned k, which is quantized from fp32 (storing
+ * receives v and the normed and turned k, which is computed in fp64 and quantized
+ * from there, S = fl32(max |k| / 448) and the code nearest to fl32(k / S) (storing
  * a k_out rounds it to bf16 first). Reads and writes what the two do, but for
  * k_out. At most 65536 tokens. */
 int fp8_qk_norm_rope_store(const fp8bl_qkv* args, hipStream_t stream);

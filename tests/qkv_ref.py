@@ -125,6 +125,22 @@ def stored(x: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
     return nearest((x.double() / s.double()[..., None]).to(torch.float32).double()), s
 
 
+def stored_turned(x, w, positions, inv_freq, axes, eps, interleaved):
+    """(E4M3 values, scales, where the values are sure, where the scales are) of the
+    fused store's keys: sure where fp64's own error cannot cross a border."""
+    ref, _ = forward(x, w, positions, inv_freq, axes, eps, interleaved)
+    n = x.double() / (x.double().square().mean(-1, keepdim=True) + eps).sqrt() * w.double()
+    size, far = reach(n, angles(positions, inv_freq, axes), interleaved)
+    off = size * (2.0 ** -38 + 2.0 ** -50 * far)
+    top, most, s = ref.abs().amax(-1), off.amax(-1), scales(ref)
+    sure = ((top - most) / 448.0).to(torch.float32) == ((top + most) / 448.0).to(torch.float32)
+
+    def code(z):
+        return nearest((z / s.double()[..., None]).to(torch.float32).double())
+
+    return code(ref), s, (code(ref - off) == code(ref + off)) & sure[..., None], sure
+
+
 def loaded(codes, scale, slots) -> torch.Tensor:
     """bf16 rows, zeros for a slot outside the cache."""
     kept = (slots >= 0) & (slots < codes.shape[0])

@@ -49,6 +49,9 @@ class Case:
     def ref(self, x, w, eps=1e-6):
         return R.forward(x, w, self.positions, self.freq, self.axes, eps, self.how["interleaved"])
 
+    def stored_turned(self, eps=1e-6):
+        return R.stored_turned(self.k, self.kw, self.positions, self.freq, self.axes, eps, self.how["interleaved"])
+
     def ref_back(self, dy, x, w, eps=1e-6):
         # one wave's steps of 64 / L heads; its units, where there are more than
         # 1024 workgroups of 4 waves
@@ -370,6 +373,11 @@ def check_fused(c, before, after, q, slots, name):
     got = R.values(after[0][rows]) * after[2][rows].double()[..., None]
     most = torch.maximum(2.0 ** -4 * ref.abs()[live], 2.0 ** -10 * s_ref[..., None]) * (1 + 2.0 ** -10) + 2 * bound[live]
     assert bool(((got - ref[live]).abs() <= most).all()), name
+    # and the very codes and scales, but within fp64's own error of a border
+    codes, scale, sure, sure_scale = (x[live] for x in c.stored_turned())
+    assert float(sure.double().mean()) > 0.99, name
+    assert bool(((R.values(after[0][rows]) == codes) | ~sure).all()), name
+    assert bool(((after[2][rows] == scale) | ~sure_scale).all()), name
     untouched = torch.ones(before[0].shape[0], dtype=torch.bool, device="cuda")
     untouched[rows] = False
     assert all(torch.equal(a[untouched], b[untouched]) for a, b in zip(before, after)), name
