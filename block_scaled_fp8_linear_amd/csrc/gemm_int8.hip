@@ -26,9 +26,10 @@
 // l / 32, A (the weight) and B (X) alike; it holds the sums of X row l % 32 and
 // weight rows 8 g + 4 (l / 32) + i, g and i from 0 to 3.
 //
-// MI355X: 8192 x 8192 x 8192 463 us (2.37 POP/s), 8192 x 12288 x 4096 370 (2.2),
-// 512 x 5120 x 5120 25, 333 x 4300 x 1168 8.4, the matrix cores busy about half the
-// time in the first two.
+// MI355X: 8192 x 8192 x 8192 433 to 451 us from one card to the next (2.44 to 2.54
+// POP/s), 8192 x 12288 x 4096 348 to 365, 2048 x 5120 x 5120 57, 512 x 5120 x 5120
+// 25, 333 x 4300 x 1168 9, the matrix cores busy 59% of the time in the second. The
+// loads bound the first two: without them 387.
 //
 // Rows past M or N and K past the end read as zero: buffer descriptors that
 // cover the valid rows, and offsets out of range for chunks behind K.
@@ -471,13 +472,14 @@ struct Plan {
 };
 
 // Tile edge and split count by a time estimate in microseconds, fitted to 21
-// shapes from 48 x 8000 x 8192 to 2000 x 256 x 25600 measured with every choice
-// (the choices' times are 0.7% above the best ones' on average): a step of 128 of
-// K on a compute unit, a unit's start and epilogue, and the join of splits. Units
-// of 64 run two to a compute unit. 512 x 5120 x 5120 takes 25.3 us in tiles of
-// 128, 31.5 of 64 and 65.5 of 256; 333 x 4300 x 1168 11.4, 9.2 and 25.8; 8192 x
-// 8192 x 8192 623, 907 and 486; 64 x 1000 x 25600 57.6 in tiles of 64 and 13.4
-// with eight splits.
+// shapes from 48 x 8000 x 8192 to 2000 x 256 x 25600 measured with every choice: a
+// step of 128 of K on a compute unit, a unit's start and epilogue, and the join of
+// splits (large tiles have become a little faster since; on 13 shapes measured again
+// the choices are at most 3% above the best). Units of 64 run two to a compute unit.
+// 512 x 5120 x 5120 takes 24.9 us in tiles of 128, 31.3 of 64 and 55.8 of 256;
+// 333 x 4300 x 1168 11.4, 9.0 and 25.6; 2048 x 5120 x 5120 66.9, 90.8 and 57.5;
+// 4096 x 4096 x 4096 77.2, 114 and 60.2; 64 x 1000 x 25600 57.6 in tiles of 64 and
+// 13.4 with eight splits.
 Plan plan_int8(int64_t m, int64_t n, int64_t k) {
   constexpr int kEdge[3] = {256, 128, 64};
   constexpr double kStepUs[3] = {1.8, 0.61, 0.33}, kUnitUs[3] = {5.0, 2.2, 1.1};
