@@ -57,6 +57,51 @@ def test_linear(shape):
     assert R.same_bits(plain, R.linear(xq, xs, wq, ws))
 
 
+# Large tiles in one round of workgroups and in several (whole and cut off, with
+# few steps and many, rows of whole lines and not), splits of K of every tile and of
+# few rows, and of the smallest last range.
+LARGE = [
+    (2048, 5120, 2064), (2045, 5117, 528), (1999, 8001, 1040), (1280, 13000, 1040), (8192, 8192, 400), (8190, 8200, 1024),
+    (16385, 5120, 272), (16300, 5121, 144), (500, 5000, 25600), (1500, 1203, 40960), (500, 2000, 12304), (300, 2501, 20496),
+    (1000, 1000, 30000), (64, 1000, 25600), (200, 136, 131056), (1, 300, 32784), (1, 5000, 32784), (1, 4500, 16400),
+    (9, 500, 16400), (16, 300, 25600), (16, 5000, 20480), (32, 1000, 8208), (20, 4500, 8208), (29, 100, 131056),
+]
+
+
+@pytest.mark.parametrize("shape", LARGE, ids=["x".join(map(str, s)) for s in LARGE])
+def test_large_tiles_and_splits(shape):
+    say("int8_linear", *shape)
+    xq, xs, wq, ws, bias = operands(*shape)
+    want = R.linear(xq, xs, wq, ws, bias)
+    for _ in range(3):
+        assert R.same_bits(F.int8_linear(xq, xs, wq, ws, bias=bias), want)
+
+
+def test_two_threads():
+    """Calls from two threads at once, each on a stream of its own."""
+    import threading
+    say("int8_linear from two threads")
+    shapes = [(300, 2501, 4112), (17, 700, 8208)]
+    data = [operands(*s) for s in shapes]
+    want = [R.linear(*d) for d in data]
+    wrong = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            got = [F.int8_linear(*data[i][:4], bias=data[i][4]) for _ in range(40)]
+        stream.synchronize()
+        wrong.extend(i for y in got if not R.same_bits(y, want[i]))
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 @pytest.mark.parametrize("m,n", [(1, 40), (16, 40), (100, 300)])
 def test_largest_sums(m, n):
     """k at its limit with every code -128: sums of 2^31 - 2^18."""
