@@ -312,7 +312,7 @@ __device__ __forceinline__ void store_run(const RopeArgs& g, const CacheArgs& k,
         const double n = 1.0 / sqrt(head_sum<L>(sq) / dim + g.t.eps);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          v[e] = n * fma((double)(x[e] * w[e]), c[e], (double)(o[e] * wo[e]) * s[e]);     // (16-bit products: exact)
+          v[e] = n * fma((double)x[e] * (double)w[e], c[e], (double)o[e] * (double)wo[e] * s[e]);
           amax = fmax(amax, fabs(v[e]));
         }
         sc = (float)(head_max<L>(amax) / 448.0);
