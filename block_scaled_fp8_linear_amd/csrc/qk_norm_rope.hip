@@ -105,7 +105,7 @@ __device__ __forceinline__ Heads<L, PAST> heads_of(const HeadView& in, const Hea
 
 // The first loads are on their way already.
 template <int L, bool INTER, bool PAST>
-__device__ __forceinline__ void rope_heads(Heads<L, PAST>& g, float inv_dim, float eps, const Chunk& ch,
+__device__ __forceinline__ void rope_heads(Heads<L, PAST>& g, float inv_dim, double eps, const Chunk& ch,
                                            const float (&c)[8], const float (&s)[8]) {
   float a[8], b[8];
   {
@@ -129,7 +129,14 @@ __device__ __forceinline__ void rope_heads(Heads<L, PAST>& g, float inv_dim, flo
       float sq = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) sq = __builtin_fmaf(x[e], x[e], sq);
-      const float r = rsqrtf(head_sum<L>(sq) * inv_dim + eps);
+      float mean = head_sum<L>(sq) * inv_dim + (float)eps;
+      if (__builtin_expect(!norm_in_range(mean), 0)) {
+        const int by = norm_exponent<L>(x, eps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = ldexpf(x[e], -by), o[e] = ldexpf(o[e], -by);
+        mean = norm_scaled<L>(x, inv_dim, eps, by);
+      }
+      const float r = rsqrtf(mean);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = r * __builtin_fmaf(x[e], a[e], o[e] * b[e]);
       if (g.mine && h < g.last) put8<PAST>(g.dst + h * g.out_hs, pack8(x));
@@ -155,10 +162,10 @@ __device__ __forceinline__ void rope_unit(const RopeArgs& g, int k_heads, int un
   float c[8], s[8];
   turn_factors<INTER>(table, ch, c, s);
   const float inv_dim = 1.0f / (float)g.t.dim;
-  if (s0 < sq) rope_heads<L, INTER, PAST>(q, inv_dim, (float)g.t.eps, ch, c, s);
+  if (s0 < sq) rope_heads<L, INTER, PAST>(q, inv_dim, g.t.eps, ch, c, s);
   if (s1 > sq) {
     if (s0 < sq) k.load(k.first);
-    rope_heads<L, INTER, PAST>(k, inv_dim, (float)g.t.eps, ch, c, s);
+    rope_heads<L, INTER, PAST>(k, inv_dim, g.t.eps, ch, c, s);
   }
 }
 
@@ -309,7 +316,8 @@ __device__ __forceinline__ void store_run(const RopeArgs& g, const CacheArgs& k,
         turn_factors<INTER>(tables[t.r], ch, c, s);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sq = fma((double)x[e], (double)x[e], sq);
-        const double n = 1.0 / sqrt(head_sum<L>(sq) / dim + g.t.eps);
+        const double mean = head_sum<L>(sq) / dim + g.t.eps;
+        const double n = mean == 0.0 ? 0.0 : 1.0 / sqrt(mean);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           v[e] = n * fma((double)x[e] * (double)w[e], c[e], (double)o[e] * (double)wo[e] * s[e]);

@@ -53,7 +53,20 @@ __device__ __forceinline__ void back_heads(const BackArgs& g, int which, const u
       sq = __builtin_fmaf(x[i], x[i], sq);
       ux = __builtin_fmaf(y[i] * w[i], x[i], ux);
     }
-    const float r = rsqrtf(head_sum<L>(sq) * inv_dim + (float)g.t.eps);
+    float mean = head_sum<L>(sq) * inv_dim + (float)g.t.eps;
+    int by = 0;
+    if (__builtin_expect(!norm_in_range(mean), 0)) {
+      // with x scaled, r and the gradient of x come scaled the other way
+      by = norm_exponent<L>(x, g.t.eps);
+      ux = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[i] = ldexpf(x[i], -by);
+        ux = __builtin_fmaf(y[i] * w[i], x[i], ux);
+      }
+      mean = norm_scaled<L>(x, inv_dim, g.t.eps, by);
+    }
+    const float r = rsqrtf(mean);
     const float along = head_sum<L>(ux) * inv_dim * r * r;
     // a head that is not there leaves zeros in the sums, whatever r is
     const float rl = live ? r : 0.0f;
@@ -61,6 +74,10 @@ __device__ __forceinline__ void back_heads(const BackArgs& g, int which, const u
     for (int i = 0; i < 8; ++i) {
       dw[i] = __builtin_fmaf(y[i] * rl, x[i], dw[i]);
       o[i] = r * __builtin_fmaf(-x[i], along, y[i] * w[i]);
+    }
+    if (__builtin_expect(by != 0, 0)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = ldexpf(o[i], -by);
     }
     if (live) put8<PAST>(op + h * ov.hs, pack8(o));
   }

@@ -74,10 +74,12 @@ typedef struct fp8bl_qkv {
  *   pair i (a, b) of n -> (a cos theta_i - b sin theta_i, b cos theta_i + a sin theta_i)
  * Pair i is elements i and i + pairs, or 2 i and 2 i + 1 where `interleaved`;
  * elements from 2 * pairs on are not turned. `pairs` is a multiple of 8, or of
- * 4 where `interleaved`. theta is reduced in fp64, all else is fp32 (the sum of
- * a head's squares too, which has to stay below 3.4e38), and the result is
- * rounded to bf16 once. A head with a value that is not finite gives
- * unspecified values of its own.
+ * 4 where `interleaved`. theta is reduced in fp64, all else is fp32, and the
+ * result is rounded to bf16 once. A head whose mean(x^2) + eps lies outside
+ * 2^-32 .. 2^64 is scaled by a power of two first, so that any finite head and
+ * any eps give what the formula says; a head of zeros with an eps of 0 gives
+ * zeros. A head with a value that is not finite gives unspecified values of its
+ * own.
  * Reads tokens, q_heads, k_heads, head_dim, q, k, q_weight, k_weight,
  * positions, inv_freq, axes, pairs, interleaved, eps, axis; writes q_out (which
  * may be q) and k_out (which may be k). inv_freq and positions 4-byte, weights
@@ -90,9 +92,11 @@ int fp8_qk_norm_rope(const fp8bl_qkv* args, hipStream_t stream);
  *   gradient of weight  sum over tokens and heads of dn x r  -> dq_weight, dk_weight
  * Reads what fp8_qk_norm_rope reads, and dq and dk; writes q_out (which may be
  * dq), k_out (which may be dk), and dq_weight and dk_weight (4-byte aligned),
- * each of which may be NULL. Sums in fp32 in an order fixed by the sizes: the
- * same bits on every call. The workspace (256-byte aligned, of at least the
- * queried size) needs no initialisation; calls that share one must be ordered. */
+ * each of which may be NULL. A head of zeros with an eps of 0 gives zeros here
+ * too, and adds nothing to the weight's gradient. Sums in fp32 in an order fixed
+ * by the sizes: the same bits on every call. The workspace (256-byte aligned, of
+ * at least the queried size) needs no initialisation; calls that share one must
+ * be ordered. */
 size_t fp8_qk_norm_rope_backward_workspace_size(int64_t tokens, int64_t q_heads, int64_t k_heads,
                                                 int64_t head_dim);
 int fp8_qk_norm_rope_backward(const fp8bl_qkv* args, void* workspace, size_t workspace_bytes,
