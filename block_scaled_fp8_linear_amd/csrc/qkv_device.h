@@ -158,21 +158,29 @@ __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
 }
 
 // cos and sin of pair p of a token. The angle position * inv_freq reaches 2^31
-// radians: it is taken in fp64 as a number of turns. What is left of it behind
-// whole quarter turns, at most pi / 4, goes through the two power series: to a^11
-// and a^10 (off by 2e-10), so that both come out rounded once to fp32, or to a^13 and
-// a^12 where they stay fp64 (off by 4e-13).
+// radians and more, and is reduced in fp64 without losing any of it: the product's
+// rounding error e comes back with the rest, and quarter turns go off it in two parts,
+// pi / 2 = h + l but for 2^-109. theta - q h is a multiple of 2^-52 (or theta is below
+// 1), so the first fma is exact. What is left, at most pi / 4, is off by 2^-53 for
+// angles below 2^40; where q itself is off by more, far past 2^48, whole quarter turns
+// are taken. It goes through the two power series: to a^11 and a^10 (off by 2e-10), so
+// that both come out rounded once to fp32, or to a^13 and a^12 where they stay fp64 (off
+// by 4e-13).
 template <bool FP64>
 __device__ __forceinline__ double2 turn64(const TurnArgs& t, int axis, int p, int token) {
-  const double turns = (double)t.positions[(size_t)axis * t.tokens + token] *
-                       ((double)t.inv_freq[p] * 0.15915494309189533577);
-  const double quarters = rint(4.0 * turns);
-  const double a = (turns - 0.25 * quarters) * 6.28318530717958647693, z = a * a;
+  constexpr double h = 1.57079632679489655800, l = 6.12323399573676603587e-17;
+  const double at = (double)t.positions[(size_t)axis * t.tokens + token], f = (double)t.inv_freq[p];
+  const double theta = at * f, e = fma(at, f, -theta);
+  constexpr double whole = 6755399441055744.0;       // 1.5 2^52: a sum with it has the nearest integer in its low bits
+  const double sum = fma(at, f * 0.63661977236758134308, whole), quarters = sum - whole;
+  double a = fma(-quarters, h, theta) + fma(-quarters, l, e);
+  if (fabs(a) > 1.0) a = 0.0;
+  const double z = a * a;
   const double s11 = FP64 ? fma(z, 1.0 / 6227020800, -1.0 / 39916800) : -1.0 / 39916800;
   const double c10 = FP64 ? fma(z, 1.0 / 479001600, -1.0 / 3628800) : -1.0 / 3628800;
   const double s = a * fma(z, fma(z, fma(z, fma(z, fma(z, s11, 1.0 / 362880), -1.0 / 5040), 1.0 / 120), -1.0 / 6), 1.0);
   const double c = fma(z, fma(z, fma(z, fma(z, fma(z, c10, 1.0 / 40320), -1.0 / 720), 1.0 / 24), -0.5), 1.0);
-  const int q = (int)(int64_t)quarters & 3;
+  const int q = __double2loint(sum) & 3;
   const double fs = q & 1 ? c : s, fc = q & 1 ? s : c;
   return double2{q == 1 || q == 2 ? -fc : fc, q >= 2 ? -fs : fs};
 }

@@ -74,12 +74,12 @@ typedef struct fp8bl_qkv {
  *   pair i (a, b) of n -> (a cos theta_i - b sin theta_i, b cos theta_i + a sin theta_i)
  * Pair i is elements i and i + pairs, or 2 i and 2 i + 1 where `interleaved`;
  * elements from 2 * pairs on are not turned. `pairs` is a multiple of 8, or of
- * 4 where `interleaved`. theta is reduced in fp64, all else is fp32, and the
- * result is rounded to bf16 once. A head whose mean(x^2) + eps lies outside
- * 2^-32 .. 2^64 is scaled by a power of two first, so that any finite head and
- * any eps give what the formula says; a head of zeros with an eps of 0 gives
- * zeros. A head with a value that is not finite gives unspecified values of its
- * own.
+ * 4 where `interleaved`. theta is the exact product, reduced in fp64 (to 2^-53
+ * below 2^40 radians); all else is fp32, and the result is rounded to bf16 once.
+ * A head whose mean(x^2) + eps lies outside 2^-32 .. 2^64 is scaled by a power
+ * of two first, so that any finite head and any eps give what the formula says; a
+ * head of zeros with an eps of 0 gives zeros. A head with a value that is not
+ * finite gives unspecified values of its own.
  * Reads tokens, q_heads, k_heads, head_dim, q, k, q_weight, k_weight,
  * positions, inv_freq, axes, pairs, interleaved, eps, axis; writes q_out (which
  * may be q) and k_out (which may be k). inv_freq and positions 4-byte, weights
