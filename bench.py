@@ -100,10 +100,10 @@ KERNEL_SOURCES = {
     "glu_backward_kernel": ("act_backward.hip", "fp8bl_act.h"),
     "column_sum_kernel": ("act_backward.hip", "fp8bl_act.h"),
     # the 8-bit integer linear
-    "int8_quantize_kernel": ("fp8bl_int8.hip", "fp8bl_ops.h", "int8_quantize.hip", "int8_row.h"),
-    "gemm_int8_skinny_kernel": ("fp8bl_int8.hip", "fp8bl_ops.h", "gemm_int8_skinny.hip", "int8_row.h"),
-    "join_int8_kernel": ("fp8bl_int8.hip", "fp8bl_ops.h", "gemm_int8.hip"),
-    "gemm_int8_kernel": ("fp8bl_int8.hip", "fp8bl_ops.h", "gemm_int8.hip"),
+    "int8_quantize_kernel": ("fp8bl_int8.hip", "fp8bl_ops.h", "int8_plan.h", "int8_quantize.hip", "int8_row.h"),
+    "gemm_int8_skinny_kernel": ("fp8bl_int8.hip", "fp8bl_ops.h", "int8_plan.h", "gemm_int8_skinny.hip", "int8_row.h"),
+    "join_int8_kernel": ("fp8bl_int8.hip", "fp8bl_ops.h", "int8_plan.h", "gemm_int8.hip"),
+    "gemm_int8_kernel": ("fp8bl_int8.hip", "fp8bl_ops.h", "int8_plan.h", "gemm_int8.hip"),
     # from the QKV projection to its cache
     "rope_kernel": ("fp8bl_qkv.hip", "fp8bl_ops.h", "qk_norm_rope.hip", "qkv_device.h"),
     "store_kernel": ("fp8bl_qkv.hip", "fp8bl_ops.h", "qk_norm_rope.hip", "qkv_device.h"),

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "fp8bl_internal.h"
+#include "int8_plan.h"
 
 struct fp8bl_qkv;
 
@@ -18,12 +19,10 @@ hipError_t launch_int8_gemm(const int8_t* xq, const float* xs, const int8_t* wq,
                             hipStream_t stream);
 // At up to kInt8SkinnyRows rows; and from one row of bf16, quantized on the way
 // where int8_skinny_quantizes says so.
-constexpr int64_t kInt8SkinnyRows = 32;
 size_t int8_skinny_bytes(int64_t m, int64_t n, int64_t k);
 hipError_t launch_int8_skinny(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws,
                               const uint16_t* bias, uint16_t* y, int64_t m, int64_t n, int64_t k, void* workspace,
                               hipStream_t stream);
-bool int8_skinny_quantizes(int64_t m, int64_t k);
 hipError_t launch_int8_skinny_bf16(const uint16_t* x, const int8_t* wq, const float* ws, const uint16_t* bias,
                                    uint16_t* y, int64_t n, int64_t k, hipStream_t stream);
 // Sum of K splits' partials (slabs of partial_slab(m, n)) with the epilogue.

@@ -421,7 +421,7 @@ void gemm_int8_kernel(GemmArgs g) {
     for (int n = 0; n < WN; ++n)
 #pragma unroll
       for (int m = 0; m < WM; ++m) acc[n][m] = i32x16{};
-    stored = CU.m0 + kTM <= M && CU.n0 + kTN <= N;
+    stored = M - CU.m0 >= kTM && N - CU.n0 >= kTN;     // (m0 + kTM can pass 2^31)
     if constexpr (!SPLIT) wg_barrier();          // the vectors have been read
   }
   __builtin_amdgcn_s_waitcnt(vm_wait(0));        // loads behind the last step still target the LDS
@@ -466,62 +466,19 @@ void join_int8_kernel(const int32_t* __restrict__ part, const float* __restrict_
   }
 }
 
-struct Plan {
-  int tile;        // 0: 256 x 256, 1: 128 x 128, 2: 64 x 64
-  int splits;
-};
-
-// Tile edge and split count by a time estimate in microseconds, fitted to 21
-// shapes from 48 x 8000 x 8192 to 2000 x 256 x 25600 measured with every choice: a
-// step of 128 of K on a compute unit, a unit's start and epilogue, and the join of
-// splits (large tiles have become a little faster since; on 13 shapes measured again
-// the choices are at most 3% above the best). Units of 64 run two to a compute unit.
-// 512 x 5120 x 5120 takes 24.9 us in tiles of 128, 31.3 of 64 and 55.8 of 256;
-// 333 x 4300 x 1168 11.4, 9.0 and 25.6; 2048 x 5120 x 5120 66.9, 90.8 and 57.5;
-// 4096 x 4096 x 4096 77.2, 114 and 60.2; 64 x 1000 x 25600 57.6 in tiles of 64 and
-// 13.4 with eight splits.
-Plan plan_int8(int64_t m, int64_t n, int64_t k) {
-  constexpr int kEdge[3] = {256, 128, 64};
-  constexpr double kStepUs[3] = {1.8, 0.61, 0.33}, kUnitUs[3] = {5.0, 2.2, 1.1};
-  constexpr double kJoinUs = 2.2, kJoinElemUs = 2.1e-6;
-  const int64_t steps = (k + 127) / 128;
-  Plan best{0, 1};
-  double least = 1e300;
-  for (int t = 0; t < 3; ++t) {
-    const int64_t tiles = ((m + kEdge[t] - 1) / kEdge[t]) * ((n + kEdge[t] - 1) / kEdge[t]);
-    for (const int splits : {1, 2, 3, 4, 6, 8}) {
-      const int64_t each = (steps + splits - 1) / splits;
-      if (splits > 1 && each < 4) break;
-      const int64_t units = tiles * splits;
-      double us;
-      if (t == 2) {
-        const int64_t rest = units % 512;
-        us = (double)(2 * (units / 512) + (rest == 0 ? 0 : rest <= 256 ? 1 : 2)) * each * kStepUs[t] +
-             (double)((units + 511) / 512) * kUnitUs[t];
-      } else {
-        us = (double)((units + 255) / 256) * (each * kStepUs[t] + kUnitUs[t]);
-      }
-      if (splits > 1) us += kJoinUs + kJoinElemUs * splits * (double)m * (double)n;
-      if (us < least) {
-        least = us;
-        best = Plan{t, splits};
-      }
-    }
-  }
-  return best;
-}
-
 template <int WM, int WN, int S>
 hipError_t launch_tiles(GemmArgs g, hipStream_t stream) {
-  constexpr int tm = Tile<WM, WN, S>::kTM, tn = Tile<WM, WN, S>::kTN;
-  g.steps = (g.K + kBK - 1) / kBK;
-  g.steps_per_unit = (g.steps + g.splits - 1) / g.splits;
-  g.splits = (g.steps + g.steps_per_unit - 1) / g.steps_per_unit;
-  g.tiles_m = (g.M + tm - 1) / tm;
-  g.tiles_n = (g.N + tn - 1) / tn;
-  const int64_t units = (int64_t)g.tiles_m * g.tiles_n * g.splits;
+  constexpr int tm = Tile<WM, WN, S>::kTM;
+  static_assert(tm == Tile<WM, WN, S>::kTN, "the plan counts square tiles");
+  static_assert(kBK == kInt8StepK, "the plan counts this kernel's steps");
+  const Int8Cut c = cut_int8(g.M, g.N, g.K, tm, g.splits);
+  g.steps = (int)c.steps;
+  g.steps_per_unit = (int)c.steps_per_unit;
+  g.splits = (int)c.splits;
+  g.tiles_m = (int)c.tiles_m;
+  g.tiles_n = (int)c.tiles_n;
   const int64_t most = (int64_t)device_cus() * (160 * 1024 / Tile<WM, WN, S>::kLds);
-  const dim3 grid((uint32_t)(units < most ? units : most));
+  const dim3 grid((uint32_t)(c.units < most ? c.units : most));
   if (g.splits == 1)
     hipLaunchKernelGGL((gemm_int8_kernel<WM, WN, S, false>), grid, dim3(kThreads), 0, stream, g);
   else
@@ -543,7 +500,7 @@ hipError_t launch_int8_join(const int32_t* part, const float* xs, const float* w
 
 size_t int8_gemm_bytes(int64_t m, int64_t n, int64_t k) {
   if (m <= kInt8SkinnyRows) return int8_skinny_bytes(m, n, k);
-  const Plan p = plan_int8(m, n, k);
+  const Int8Plan p = plan_int8(m, n, k);
   return p.splits <= 1 ? 0 : round_up((size_t)p.splits * partial_slab(m, n) * sizeof(int32_t), kWorkspaceAlign);
 }
 
@@ -551,7 +508,7 @@ hipError_t launch_int8_gemm(const int8_t* xq, const float* xs, const int8_t* wq,
                             const uint16_t* bias, uint16_t* y, int64_t m, int64_t n, int64_t k, void* workspace,
                             hipStream_t stream) {
   if (m <= kInt8SkinnyRows) return launch_int8_skinny(xq, xs, wq, ws, bias, y, m, n, k, workspace, stream);
-  const Plan p = plan_int8(m, n, k);
+  const Int8Plan p = plan_int8(m, n, k);
   const GemmArgs g{xq, xs, wq, ws, bias, y, static_cast<int32_t*>(workspace), (int)m, (int)n, (int)k, 0, 0, p.splits,
                    0, 0};
   switch (p.tile) {

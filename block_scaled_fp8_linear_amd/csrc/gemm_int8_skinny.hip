@@ -53,7 +53,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, ui
 // The row that a workgroup quantizes for itself stays in registers between the
 // maximum and the codes. In LDS it is whole super-steps long, zero behind K; 16
 // more zeros stand for the operand's rows that are not there.
-constexpr int kFusedElems = 16384, kFusedCodes = kFusedElems + 16;
+constexpr int kFusedElems = kInt8FusedK, kFusedCodes = kFusedElems + 16;
 
 template <int MT, int NT, int WAVES, int KW, bool FUSED>
 __global__ __launch_bounds__(WAVES * 64)
@@ -249,38 +249,8 @@ void gemm_int8_skinny_kernel(SkinnyArgs a) {
   }
 }
 
-// How a workgroup is cut, by the row tiles of X (m > 16) and whether 16 weight
-// rows a workgroup still leave no compute unit a second one (few).
-//
-// With few columns (n <= 4096): 16 rows by eight waves (four for two row tiles of
-// X): 1 x 4000 x 8192 takes 7.4 us so, 9.9 in 32 rows by four waves; 1 x 1000 x
-// 8192 5.8 and 8.1. Otherwise several workgroups share a compute unit, for which
-// super-steps of 128 or few waves leave the LDS: 16 x 25600 x 5120 takes 26.5 us
-// in 32 rows, four waves and super-steps of 128, 33.0 with super-steps of 256 (one
-// workgroup a compute unit, 800 of them), 31.7 in 16 rows by eight waves; one row
-// in 16 rows by four waves 25600 x 5120 25.8, 8000 x 8192 12.0 (14.5 in 32 rows).
-//
-// K is split over workgroups from 16384 on (8192 with two row tiles), in pieces
-// of 2048 or more, as far as there are compute units for them: the join costs
-// 2.5 us, 16 x 300 x 25600 takes 17.5 us whole and 7.7 in eight, 16 x 2000 x 8192
-// 8.0 and 8.2 in two. Not for a row of bf16 that is quantized on the way: its
-// quantizer would need a launch of its own.
-struct Plan {
-  bool few;
-  int splits, k_split;
-};
-Plan plan_skinny8(int64_t m, int64_t n, int64_t k) {
-  const int64_t groups = (n + 15) / 16;
-  Plan p{groups <= 256, 1, 0};
-  if (k >= (m > 16 ? 8192 : 16384) && !int8_skinny_quantizes(m, k))
-    while (groups * p.splits * 2 <= 256 && k >= 4096 * (int64_t)p.splits) p.splits *= 2;
-  p.k_split = (int)((k + 256 * p.splits - 1) / (256 * p.splits)) * 256;      // whole super-steps of either size
-  p.splits = (int)((k + p.k_split - 1) / p.k_split);
-  return p;
-}
-
 template <int MT, int NT, int WAVES, int KW, bool FUSED>
-hipError_t launch(const SkinnyArgs& a, const Plan& p, hipStream_t stream) {
+hipError_t launch(const SkinnyArgs& a, const Int8SkinnyPlan& p, hipStream_t stream) {
   hipLaunchKernelGGL((gemm_int8_skinny_kernel<MT, NT, WAVES, KW, FUSED>),
                      dim3((uint32_t)((a.N + 16 * NT - 1) / (16 * NT)), (uint32_t)p.splits), dim3(WAVES * 64), 0, stream,
                      a);
@@ -288,26 +258,21 @@ hipError_t launch(const SkinnyArgs& a, const Plan& p, hipStream_t stream) {
 }
 
 SkinnyArgs args_of(const void* x, const float* xs, const int8_t* wq, const float* ws, const uint16_t* bias,
-                   uint16_t* y, int64_t m, int64_t n, int64_t k, void* workspace, const Plan& p) {
+                   uint16_t* y, int64_t m, int64_t n, int64_t k, void* workspace, const Int8SkinnyPlan& p) {
   return SkinnyArgs{x, xs, wq, ws, bias, y, static_cast<int32_t*>(workspace), (int)m, (int)n, (int)k, p.k_split};
 }
 
 }  // namespace
 
 size_t int8_skinny_bytes(int64_t m, int64_t n, int64_t k) {
-  const Plan p = plan_skinny8(m, n, k);
+  const Int8SkinnyPlan p = plan_skinny8(m, n, k);
   return p.splits > 1 ? round_up((size_t)p.splits * partial_slab(m, n) * sizeof(int32_t), kWorkspaceAlign) : 0;
-}
-
-// One row of up to 16384, which the threads' registers hold.
-bool int8_skinny_quantizes(int64_t m, int64_t k) {
-  return m == 1 && k <= kFusedElems;
 }
 
 hipError_t launch_int8_skinny(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws,
                               const uint16_t* bias, uint16_t* y, int64_t m, int64_t n, int64_t k, void* workspace,
                               hipStream_t stream) {
-  const Plan p = plan_skinny8(m, n, k);
+  const Int8SkinnyPlan p = plan_skinny8(m, n, k);
   const SkinnyArgs a = args_of(xq, xs, wq, ws, bias, y, m, n, k, workspace, p);
   const hipError_t e = m > 16 ? p.few ? launch<2, 1, 4, 128, false>(a, p, stream) : launch<2, 2, 2, 256, false>(a, p, stream)
                        : p.few ? launch<1, 1, 8, 128, false>(a, p, stream)
@@ -319,7 +284,7 @@ hipError_t launch_int8_skinny(const int8_t* xq, const float* xs, const int8_t* w
 
 hipError_t launch_int8_skinny_bf16(const uint16_t* x, const int8_t* wq, const float* ws, const uint16_t* bias,
                                    uint16_t* y, int64_t n, int64_t k, hipStream_t stream) {
-  const Plan p = plan_skinny8(1, n, k);
+  const Int8SkinnyPlan p = plan_skinny8(1, n, k);
   const SkinnyArgs a = args_of(x, nullptr, wq, ws, bias, y, 1, n, k, nullptr, p);
   return p.few ? launch<1, 1, 8, 128, true>(a, p, stream) : launch<1, 1, 4, 256, true>(a, p, stream);
 }
