@@ -5,6 +5,9 @@
 Each HIP source is compiled to an object in ``_build/`` (in parallel), then
 linked into ``block_scaled_fp8_linear_amd/libfp8bl.so``; binding/tensors.cpp, host
 code over torch's headers, becomes ``_tensors.so`` beside it. Always rebuilds.
+
+The library needs hipcc alone: it is linked first, whatever becomes of the binding.
+Without torch (run this file by its path then) there is no binding to build.
 """
 
 from __future__ import annotations
@@ -78,23 +81,39 @@ def _run(cmd: list[str], what: str, verbose: bool) -> None:
         raise RuntimeError(f"{what} failed:\n{res.stdout}\n{res.stderr}")
 
 
-def _compile_binding(obj: str, verbose: bool) -> None:
+def _torch_dir() -> str | None:
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec is not None and spec.origin else None
+
+
+def _rocm_dir() -> str:
+    return os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+
+
+def _cxx() -> str:
+    """The host's C++ compiler, or the one that hipcc drives."""
+    for cand in ("g++", "c++", "clang++"):
+        if shutil.which(cand):
+            return cand
+    return os.path.join(_rocm_dir(), "llvm", "bin", "clang++")
+
+
+def _compile_binding(torch_dir: str, obj: str, verbose: bool) -> None:
     """binding/tensors.cpp to an object: host code only, with the host compiler."""
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
-    rocm = os.path.dirname(os.path.dirname(os.path.realpath(hipcc())))
+    rocm = _rocm_dir()
     includes = [sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
                 os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"), os.path.join(rocm, "include"), INCLUDE]
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__", "-c", BINDING, "-o", obj]
+    cmd = [_cxx(), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__", "-c", BINDING, "-o", obj]
     for path in includes:
         cmd += ["-I", path]
-    _run(cmd, "g++ for tensors.cpp", verbose)
+    _run(cmd, "compilation of tensors.cpp", verbose)
 
 
-def _link_binding(obj: str, verbose: bool) -> None:
+def _link_binding(torch_dir: str, obj: str, verbose: bool) -> None:
     """Against the library beside it and torch, which is loaded by then."""
-    torch_lib = os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), "lib")
+    torch_lib = os.path.join(torch_dir, "lib")
     tmp = BINDING_PATH + ".tmp"
-    _run(["g++", "-shared", obj, "-o", tmp, "-L", PKG_DIR, "-l:libfp8bl.so", "-L", torch_lib, "-lc10", "-ltorch_cpu",
+    _run([_cxx(), "-shared", obj, "-o", tmp, "-L", PKG_DIR, "-l:libfp8bl.so", "-L", torch_lib, "-lc10", "-ltorch_cpu",
           "-ltorch_hip", "-ltorch_python", "-Wl,-rpath,$ORIGIN"], "link of _tensors.so", verbose)
     os.replace(tmp, BINDING_PATH)
 
@@ -103,15 +122,20 @@ def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
     objs = [os.path.join(BUILD_DIR, os.path.basename(s) + ".o") for s in srcs]
-    binding = os.path.join(BUILD_DIR, "tensors.cpp.o")
+    binding, torch_dir = os.path.join(BUILD_DIR, "tensors.cpp.o"), _torch_dir()
+    host = None
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
-        host = ex.submit(_compile_binding, binding, verbose)
+        if torch_dir is not None:
+            host = ex.submit(_compile_binding, torch_dir, binding, verbose)
         list(ex.map(lambda so: _compile(so[0], so[1], verbose), zip(srcs, objs)))
-        host.result()
     tmp = LIB_PATH + ".tmp"
     _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp], "link", verbose)
     os.replace(tmp, LIB_PATH)
-    _link_binding(binding, verbose)
+    if host is None:
+        print("no torch here: _tensors.so, the compiled binding over it, is not built", file=sys.stderr)
+        return LIB_PATH
+    host.result()
+    _link_binding(torch_dir, binding, verbose)
     return LIB_PATH
 
 
