@@ -90,6 +90,7 @@ struct Signature {
   const char* name;
   int required, count;
   const char* params[kMaxParams];
+  const char* backward = nullptr;     // its backward function, where there is one
   PyObject* interned[kMaxParams] = {};
 };
 
@@ -140,8 +141,9 @@ struct Args {
     for (int i : inputs)
       if (given(i) && tensor(i).requires_grad())
         throw Raise{PyExc_RuntimeError,
-                    std::string(s.name) + " is not recorded by autograd and an input requires grad: call it in a "
-                                          "torch.autograd.Function with its backward function, or under torch.no_grad()"};
+                    std::string(s.name) + " is not recorded by autograd and an input requires grad: call it " +
+                        (s.backward ? std::string("in a torch.autograd.Function with ") + s.backward + ", or " : "") +
+                        "under torch.no_grad()" + (s.backward ? "" : " (there is no backward function)")};
   }
   int64_t device(int i) const {
     const Tensor& t = tensor(i);
@@ -398,7 +400,8 @@ fp8bl_qkv sizes(const Args& a, int q, int k) {
 
 Signature kNormRope{"fp8_qk_norm_rope", 6, 11,
                     {"q", "k", "q_weight", "k_weight", "positions", "inv_freq", "axes", "eps", "interleaved", "q_out",
-                     "k_out"}};
+                     "k_out"},
+                    "fp8_qk_norm_rope_backward"};
 PyObject* norm_rope(Args a) {
   a.outside_autograd({0, 1, 2, 3});
   const int64_t idx = a.device(0);
