@@ -12,7 +12,6 @@
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/GradMode.h>
 
-#include <initializer_list>
 #include <string>
 
 #include "fp8bl_int8.h"
@@ -134,14 +133,14 @@ struct Args {
     if (d == -1.0 && PyErr_Occurred()) throw Raise{nullptr, {}};
     return d;
   }
-  // Nothing here is recorded by autograd: an input that asks for a gradient
-  // would lose it without a word, so it is refused.
-  void outside_autograd(std::initializer_list<int> inputs) const {
+  // Nothing here is recorded by autograd: a tensor that asks for a gradient, be it
+  // read or written, would lose it without a word, so it is refused.
+  void outside_autograd() const {
     if (!c10::GradMode::is_enabled()) return;
-    for (int i : inputs)
-      if (given(i) && tensor(i).requires_grad())
+    for (int i = 0; i < s.count; ++i)
+      if (v[i] && THPVariable_Check(v[i]) && THPVariable_Unpack(v[i]).requires_grad())
         throw Raise{PyExc_RuntimeError,
-                    std::string(s.name) + " is not recorded by autograd and an input requires grad: call it " +
+                    std::string(s.name) + " is not recorded by autograd and " + s.params[i] + " requires grad: call it " +
                         (s.backward ? std::string("in a torch.autograd.Function with ") + s.backward + ", or " : "") +
                         "under torch.no_grad()" + (s.backward ? "" : " (there is no backward function)")};
   }
@@ -261,7 +260,7 @@ PyObject* pair(Output& a, Output& b) {
 
 Signature kRowQuantize{"int8_row_quantize", 1, 3, {"x", "q", "scale"}};
 PyObject* row_quantize(Args a) {
-  a.outside_autograd({0});
+  a.outside_autograd();
   const int64_t idx = a.device(0);
   const Tensor& x = a.tensor(0);
   const c10::DeviceGuard guard(x.device());
@@ -284,7 +283,7 @@ PyObject* row_quantize(Args a) {
 
 Signature kLinear{"int8_linear", 4, 7, {"xq", "x_scale", "wq", "w_scale", "bias", "out", "workspace"}};
 PyObject* linear(Args a) {
-  a.outside_autograd({1, 3, 4});
+  a.outside_autograd();
   const int64_t idx = a.device(0);
   const Tensor& x = a.tensor(0);
   const c10::DeviceGuard guard(x.device());
@@ -305,7 +304,7 @@ PyObject* linear(Args a) {
 
 Signature kLinearBf16{"int8_linear_bf16", 3, 6, {"x", "wq", "w_scale", "bias", "out", "workspace"}};
 PyObject* linear_bf16(Args a) {
-  a.outside_autograd({0, 2, 3});
+  a.outside_autograd();
   const int64_t idx = a.device(0);
   const Tensor& xt = a.tensor(0);
   const c10::DeviceGuard guard(xt.device());
@@ -403,7 +402,7 @@ Signature kNormRope{"fp8_qk_norm_rope", 6, 11,
                      "k_out"},
                     "fp8_qk_norm_rope_backward"};
 PyObject* norm_rope(Args a) {
-  a.outside_autograd({0, 1, 2, 3});
+  a.outside_autograd();
   const int64_t idx = a.device(0);
   const Tensor& q = a.tensor(0);
   const c10::DeviceGuard guard(q.device());
@@ -425,7 +424,7 @@ Signature kNormRopeBackward{"fp8_qk_norm_rope_backward", 8, 15,
                             {"dq", "dk", "q", "k", "q_weight", "k_weight", "positions", "inv_freq", "axes", "eps",
                              "interleaved", "q_grad", "k_grad", "need_weights", "workspace"}};
 PyObject* norm_rope_backward(Args a) {
-  a.outside_autograd({0, 1, 2, 3, 4, 5});
+  a.outside_autograd();
   const int64_t idx = a.device(2);
   const Tensor& q = a.tensor(2);
   const c10::DeviceGuard guard(q.device());
@@ -477,7 +476,7 @@ PyObject* norm_rope_backward(Args a) {
 
 Signature kStore{"fp8_kv_store", 7, 7, {"k", "v", "slots", "k_cache", "v_cache", "k_scale", "v_scale"}};
 PyObject* store(Args a) {
-  a.outside_autograd({0, 1});
+  a.outside_autograd();
   const int64_t idx = a.device(0);
   const c10::DeviceGuard guard(a.tensor(0).device());
   fp8bl_qkv g = sizes(a, 0, 0);
@@ -493,6 +492,7 @@ PyObject* store(Args a) {
 
 Signature kLoad{"fp8_kv_load", 5, 7, {"k_cache", "v_cache", "k_scale", "v_scale", "slots", "k_out", "v_out"}};
 PyObject* load(Args a) {
+  a.outside_autograd();
   const int64_t idx = a.device(0);
   const Tensor& c = a.tensor(0);
   const c10::DeviceGuard guard(c.device());
@@ -514,7 +514,7 @@ Signature kNormRopeStore{"fp8_qk_norm_rope_store", 12, 16,
                          {"q", "k", "v", "q_weight", "k_weight", "positions", "inv_freq", "slots", "k_cache", "v_cache",
                           "k_scale", "v_scale", "axes", "eps", "interleaved", "q_out"}};
 PyObject* norm_rope_store(Args a) {
-  a.outside_autograd({0, 1, 2, 3, 4});
+  a.outside_autograd();
   const int64_t idx = a.device(0);
   const Tensor& q = a.tensor(0);
   const c10::DeviceGuard guard(q.device());
@@ -592,7 +592,7 @@ PyMethodDef kFunctions[] = {
              "numbers on the host (a tuple or bytes), not needed with one axis. Pair i is\n"
              "elements (i, i + P), or (2 i, 2 i + 1) with interleaved; elements from 2 P on are\n"
              "not turned. D is a multiple of 8 from 16 to 256, P of 8 (4 with interleaved).\n\n"
-             "Not recorded by autograd: while gradients are enabled, inputs that require one\n"
+             "Not recorded by autograd: while gradients are enabled, tensors that require one\n"
              "are refused; fp8_qk_norm_rope_backward is its backward pass."),
     FUNCTION(kNormRopeBackward, norm_rope_backward,
              "fp8_qk_norm_rope_backward(dq, dk, q, k, q_weight, k_weight, positions, inv_freq, axes=None,\n"

@@ -58,3 +58,20 @@ def test_the_refusal_names_functions_that_exist(name):
         assert "torch.autograd.Function" not in text and "there is no backward function" in text
     with torch.no_grad(), pytest.raises(TypeError, match="device tensor"):
         getattr(F, name)(**args)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_every_tensor_that_requires_grad_is_refused(name):
+    """Scales, frequencies and given outputs among them."""
+    floats = [k for k, v in calls()[name].items() if v.is_floating_point()]
+    assert floats
+    for param in floats:
+        args = calls()[name]
+        args[param].requires_grad_(True)
+        with pytest.raises(RuntimeError, match=f"autograd and {param} requires grad"):
+            getattr(F, name)(**args)
+        args[param] = args[param] * 2                    # not a leaf
+        with pytest.raises(RuntimeError, match=f"autograd and {param} requires grad"):
+            getattr(F, name)(**args)
+        with torch.no_grad(), pytest.raises(TypeError, match="device tensor"):
+            getattr(F, name)(**args)
