@@ -135,14 +135,21 @@ struct Args {
   }
   // Nothing here is recorded by autograd: a tensor that asks for a gradient, be it
   // read or written, would lose it without a word, so it is refused.
+  // A tangent (forward mode, which no_grad leaves on) is refused likewise.
   void outside_autograd() const {
-    if (!c10::GradMode::is_enabled()) return;
-    for (int i = 0; i < s.count; ++i)
-      if (v[i] && THPVariable_Check(v[i]) && THPVariable_Unpack(v[i]).requires_grad())
+    const bool grad = c10::GradMode::is_enabled();
+    for (int i = 0; i < s.count; ++i) {
+      if (!v[i] || !THPVariable_Check(v[i])) continue;
+      const Tensor& t = THPVariable_Unpack(v[i]);
+      if (t._fw_grad(0).defined())
+        throw Raise{PyExc_RuntimeError,
+                    std::string(s.name) + " is not recorded by autograd and " + s.params[i] + " has a tangent: unpack it first"};
+      if (grad && t.requires_grad())
         throw Raise{PyExc_RuntimeError,
                     std::string(s.name) + " is not recorded by autograd and " + s.params[i] + " requires grad: call it " +
                         (s.backward ? std::string("in a torch.autograd.Function with ") + s.backward + ", or " : "") +
                         "under torch.no_grad()" + (s.backward ? "" : " (there is no backward function)")};
+    }
   }
   int64_t device(int i) const {
     const Tensor& t = tensor(i);

@@ -75,3 +75,20 @@ def test_every_tensor_that_requires_grad_is_refused(name):
             getattr(F, name)(**args)
         with torch.no_grad(), pytest.raises(TypeError, match="device tensor"):
             getattr(F, name)(**args)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_tangent_is_refused(name):
+    """Forward mode: a dual tensor's tangent would be lost, under no_grad too."""
+    ad = torch.autograd.forward_ad
+    for param in (k for k, v in calls()[name].items() if v.is_floating_point()):
+        args = calls()[name]
+        with ad.dual_level():
+            args[param] = ad.make_dual(args[param], torch.ones_like(args[param]))
+            with pytest.raises(RuntimeError, match=f"autograd and {param} has a tangent"):
+                getattr(F, name)(**args)
+            with torch.no_grad(), pytest.raises(RuntimeError, match=f"{param} has a tangent"):
+                getattr(F, name)(**args)
+            args[param] = ad.unpack_dual(args[param]).primal
+            with pytest.raises(TypeError, match="device tensor"):
+                getattr(F, name)(**args)
