@@ -194,13 +194,21 @@ struct Args {
   }
 };
 
+// A caller's tensor was written: autograd tells by its version that what it saved is
+// no longer there. (Inference tensors have none.)
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // An output: the one given, or a new tensor.
 struct Output {
   PyObject* object = nullptr;
+  bool given = false;
   Output(const Args& a, int i, at::IntArrayRef shape, ScalarType dtype, const Tensor& like) {
     if (a.given(i)) {
       a.tensor(i);
       object = a.v[i];
+      given = true;
       Py_INCREF(object);
     } else {
       object = THPVariable_Wrap(fresh(shape, dtype, like));
@@ -215,7 +223,9 @@ struct Output {
   Output(const Output&) = delete;
   Output& operator=(const Output&) = delete;
   ~Output() { Py_XDECREF(object); }
+  // The output for the caller, once the call that writes it is on its way.
   PyObject* release() {
+    if (given) written(THPVariable_Unpack(object));
     PyObject* o = object;
     object = nullptr;
     if (!o) {
@@ -393,6 +403,11 @@ void set_cache(const Args& a, int slots, int at, int64_t idx, fp8bl_qkv* g) {
   g->v_scale = static_cast<float*>(a.array(at + 3, ScalarType::Float, {r, h}, idx));
 }
 
+// The cache was written: parameters as above.
+void cache_written(const Args& a, int at) {
+  for (int i = 0; i < 4; ++i) written(a.tensor(at + i));
+}
+
 // Sizes from the parameters that hold q and k.
 fp8bl_qkv sizes(const Args& a, int q, int k) {
   fp8bl_qkv g{};
@@ -494,6 +509,7 @@ PyObject* store(Args a) {
   set_cache(a, 2, 3, idx, &g);
   const hipStream_t st = stream_of(idx);
   run("fp8_kv_store", [&] { return fp8_kv_store(&g, st); });
+  cache_written(a, 3);
   Py_RETURN_NONE;
 }
 
@@ -537,6 +553,7 @@ PyObject* norm_rope_store(Args a) {
   g.q_out = a.heads(15, qs, idx);
   const hipStream_t st = stream_of(idx);
   run("fp8_qk_norm_rope_store", [&] { return fp8_qk_norm_rope_store(&g, st); });
+  cache_written(a, 8);
   return qo.release();
 }
 
