@@ -557,7 +557,7 @@ def _compiled(name: str):
         from . import _tensors
     except ImportError as e:
         raise ImportError(f"{e}; run `python -m block_scaled_fp8_linear_amd.build`") from e
-    _tensors.configure(Fp8blError, _raw_stream)
+    _tensors.configure(Fp8blError, _raw_stream, torch.OutOfMemoryError)
     globals().update({f: getattr(_tensors, f) for f in _COMPILED})
     return globals()[name]
 

@@ -11,7 +11,9 @@
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/GradMode.h>
+#include <c10/util/Exception.h>
 
+#include <new>
 #include <string>
 
 #include "fp8bl_int8.h"
@@ -33,6 +35,7 @@ struct Raise {
 
 PyObject* g_error;        // the package's Fp8blError
 PyObject* g_raw_stream;   // torch's current stream of a device, as a number
+PyObject* g_memory;       // torch's OutOfMemoryError
 
 // Makes a call, other threads running meanwhile: a launch can wait for the GPU.
 template <typename F>
@@ -565,22 +568,29 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* names) 
     return F(Args(S, args, n, names));
   } catch (const Raise& r) {
     if (r.type) PyErr_SetString(r.type, r.what.c_str());
+  } catch (const c10::OutOfMemoryError& e) {
+    PyErr_SetString(g_memory, e.what_without_backtrace());
+  } catch (const c10::Error& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
+  } catch (const std::bad_alloc&) {
+    PyErr_NoMemory();
   } catch (const std::exception& e) {
     if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
   }
   return nullptr;
 }
 
-// configure(error class, raw stream function)
+// configure(error class, raw stream function, out-of-memory error class)
 PyObject* configure(PyObject*, PyObject* args) {
-  PyObject *error, *raw;
-  if (!PyArg_ParseTuple(args, "OO", &error, &raw)) return nullptr;
-  Py_INCREF(error);
-  Py_INCREF(raw);
-  Py_XDECREF(g_error);
-  Py_XDECREF(g_raw_stream);
-  g_error = error;
-  g_raw_stream = raw;
+  PyObject* given[3];
+  if (!PyArg_ParseTuple(args, "OOO", &given[0], &given[1], &given[2])) return nullptr;
+  PyObject** const kept[] = {&g_error, &g_raw_stream, &g_memory};
+  for (int i = 0; i < 3; ++i) {
+    Py_INCREF(given[i]);
+    PyObject* const was = *kept[i];
+    *kept[i] = given[i];
+    Py_XDECREF(was);
+  }
   Py_RETURN_NONE;
 }
 

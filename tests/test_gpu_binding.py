@@ -69,3 +69,16 @@ def test_a_saved_tensor_that_is_turned_in_place_is_noticed():
         F.fp8_qk_norm_rope(**(args | {"q": q, "q_out": q}))
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+def test_out_of_memory_is_torchs_error():
+    """2 TiB of keys and as many values: torch's own error, by which callers free and
+    try again; the call after it works."""
+    cache = [torch.zeros(1, 4096, 256, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    cache += [torch.ones(1, 4096, device="cuda") for _ in range(2)]
+    slots = torch.zeros(1 << 20, dtype=torch.int32, device="cuda")
+    with pytest.raises(torch.OutOfMemoryError, match="out of memory") as e:
+        F.fp8_kv_load(*cache, slots)
+    assert "frame #" not in str(e.value)
+    k, v = F.fp8_kv_load(*cache, slots[:3])
+    assert k.shape == v.shape == (3, 4096, 256)
