@@ -144,6 +144,7 @@ struct Args {
     for (int i = 0; i < s.count; ++i) {
       if (!v[i] || !THPVariable_Check(v[i])) continue;
       const Tensor& t = THPVariable_Unpack(v[i]);
+      if (t.unsafeGetTensorImpl()->autograd_meta() == nullptr) continue;     // neither
       if (t._fw_grad(0).defined())
         throw Raise{PyExc_RuntimeError,
                     std::string(s.name) + " is not recorded by autograd and " + s.params[i] + " has a tangent: unpack it first"};
