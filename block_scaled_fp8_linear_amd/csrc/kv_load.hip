@@ -1,7 +1,7 @@
 // Rows of the E4M3 cache back as bf16(fl32(code * S)); zeros for a token whose
 // slot is outside the cache. A wave takes a token, 64 / L heads of its keys and
 // values at a time; three bytes an element in all, no other work to speak of, and
-// bound by them: 131071 rows of 8 heads of 128 take 139 us (5.8 TB/s), 129 rows
+// bound by them: 131071 rows of 8 heads of 128 take 137 us (5.9 TB/s), 129 rows
 // 3.2, a launch's own time.
 #include "fp8bl_ops.h"
 #include "qkv_device.h"

@@ -8,18 +8,19 @@
 // (or a part of its heads), works the token's cosines and sines out once, one
 // pair a lane, and shares them through LDS; no wave waits for another. Bound by
 // the heads' bytes, each read and written once: 16384 tokens of 80 heads of 128
-// take 127 us (5.3 TB/s), 512 tokens of 72 heads 7.6 us (2.5 TB/s; the angles'
+// take 125 us (5.4 TB/s), 512 tokens of 72 heads 7.0 us (2.7 TB/s; the angles'
 // fp64 and one wave's chain of loads, sums and stores), of which a launch of
-// nothing is about 3.
+// nothing is about 3. (Times of calls one after another over changing inputs; where
+// choices are compared below, replays of one call in a graph.)
 //
 // Store: a workgroup takes a run of tokens. Where a later token of the call has
 // the same slot, the earlier one is not stored: the workgroup compares its run
 // with every later slot first, while its heads are on their way. 8192 tokens of
-// 8 heads of 128 take 16.9 us (3.0 TB/s), 14.5 without the comparison; the fused
-// call for 16 tokens of 64 and 8 heads 4.8 us. Its keys are normed, turned and
-// divided in fp64: in fp32 one code in 200000 was its neighbour's, where the value
-// lies next to the border between them. That costs 8192 tokens 79 us for 75, 16 tokens
-// nothing.
+// 8 heads of 128 take 15.4 us (3.3 TB/s), of which the comparison is 2.4; the fused
+// call for 16 tokens of 64 and 8 heads 5.2 us on the GPU. Its keys are normed, turned
+// and divided in fp64: in fp32 one code in 200000 was its neighbour's, where the value
+// lies next to the border between them. That costs 8192 tokens of 64 and 8 heads 5%
+// (75 us in all), 16 tokens nothing.
 #include "fp8bl_ops.h"
 #include "qkv_device.h"
 
@@ -192,7 +193,7 @@ constexpr int kMaxRun = 16;
 // load, four loads on their way at a time (the first ahead of the run's own
 // slots); slots outside the run's own range, as nearly all are where tokens lie in
 // pages, need no more than that comparison (slots in random order take all: 16384
-// tokens then take 42 us). Lane r of a wave holds the slot of token i0 + r.
+// tokens then take 44 us). Lane r of a wave holds the slot of token i0 + r.
 __device__ __forceinline__ uint32_t later_ones(const int32_t* __restrict__ slots, int i0, int run, int run_slots,
                                                int tokens) {
   constexpr int kLoads = 4, kRound = kLoads * 4 * kQkvThreads;
@@ -367,7 +368,9 @@ void rope_store_kernel(RopeArgs g, CacheArgs k, int runs) {
 // Waves to a token: as many as there are steps of 64 / L heads where few
 // tokens would leave the chip empty, one where there are enough. Each works the
 // angles out for itself, so more waves than fill the chip cost: 512 tokens of 72
-// heads of 128 take 8.5 us with two waves, 7.6 with four or eight, 9.7 with 16.
+// heads of 128 take 8.3 us with two waves, 7.3 with four, 7.5 with eight, 9.4 with 16;
+// 1024 tokens of them 10.5 with four, 12.1 with eight; 2048 tokens of 18 heads of 80 7.2
+// with two, 9.5 with four; three heads of 64 the same with any number.
 int parts_of(int64_t tokens, int64_t steps) {
   int64_t parts = 4096 / tokens;
   if (parts > steps) parts = steps;
@@ -377,9 +380,17 @@ int parts_of(int64_t tokens, int64_t steps) {
 int steps_of(int64_t heads, int lanes) { return (int)((heads + 64 / lanes - 1) / (64 / lanes)); }
 
 // Tokens to a workgroup that stores: one where tokens are few; four, whose keys
-// and values then take two batches of loads a wave at eight heads of 128 (8192
-// tokens 16.9 us, two 17.6, eight 18.0, one 21.7); sixteen where the comparison of
-// the slots, which grows with the square of the tokens over the run, would weigh.
+// and values then take two batches of loads a wave at eight heads of 128; sixteen
+// where the comparison of the slots, which grows with the square of the tokens over
+// the run, would weigh. By the tokens alone, though a run's other work grows with its
+// heads; in us, with runs of 1, 2, 4, 8, 16:
+//   1 head of 64     1024 tokens  5.4  5.0  5.4  6.9 10.2     8192  17.7 13.2 10.9 11.0 12.5
+//                   16384        35.2 23.9 18.2 16.6 17.5    65536     -  166 92.7 66.9 54.9
+//   8 heads of 128   1024 tokens  5.9  6.1  6.8  9.8 15.9     8192  22.4 18.2 17.2 18.2 21.7
+//                   16384        43.7 32.3 28.2 27.1 29.6    65536     -  225  155  120  105
+//   32 heads of 128  2048 tokens 16.7 17.8 21.3 29.5 53.7     8192  47.2 44.4 44.3 49.9 66.4
+//                   16384         106 92.1 89.6 92.2  117    65536     -  464  382  359  358
+// (2048 tokens of 32 heads lose most by the rule, 21.7 for 16.7.)
 int run_of(int64_t tokens) { return tokens <= 1024 ? 1 : tokens <= 16384 ? 4 : kMaxRun; }
 
 RopeArgs rope_args(const fp8bl_qkv& a) {

@@ -6,7 +6,7 @@
 // A wave takes a token (or a part of its heads) at a time and keeps its share
 // of the weights' gradients in registers until its last one; a second kernel
 // adds the workgroups' sums in a fixed order. Bound by the heads' bytes: 8192
-// tokens of 72 heads of 128 take 90 us (5.0 TB/s), of which the second kernel and
+// tokens of 72 heads of 128 take 88.5 us (5.1 TB/s), of which the second kernel and
 // its launch are 4; 77 tokens of 18 heads of 80 take 7.0, the two launches' own
 // time.
 #include "fp8bl_ops.h"
@@ -162,8 +162,10 @@ void back_sum_kernel(const float* __restrict__ part, int blocks, int dim, float*
 }
 
 // Workgroups: fixed by the sizes alone, for results that are the same on every
-// device and call. Four a compute unit: 8192 tokens of 72 heads of 128 take 98 us
-// through the caches, 105 with 512 workgroups, 101 with 2048.
+// device and call. Four a compute unit; with 512, 1024 and 2048 of them 8192 tokens of
+// 72 heads of 128 take 99, 87 and 91 us, of 18 heads of 80 30.1, 24.0 and 27.0, of
+// three heads of 64 16.6, 15.1 and 18.9; 512 tokens of 72 heads 12.5, 14.0 and 20.3, 2048
+// of 18 heads of 80 12.4, 13.0 and 18.1.
 constexpr int64_t kBackBlocks = 1024;
 
 int back_parts(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim) {

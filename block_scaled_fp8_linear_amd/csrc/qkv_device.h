@@ -46,8 +46,8 @@ inline TurnArgs turn_args(const fp8bl_qkv& a) {
 
 // Whether a call goes past the caches: what it reads and writes is more than
 // the 256 MB of the last-level cache, so nothing of it would be found there by the
-// next kernel. Norm and rotation of 16384 tokens of 80 heads of 128 take 120 us so
-// and 126 through the caches (185 and 188 with a copy of the results behind
+// next kernel. In replays of a graph norm and rotation of 16384 tokens of 80 heads of
+// 128 take 120 us so and 126 through the caches (185 and 188 with a copy of the results behind
 // them), of 2048 tokens 18.5 and 20.5 (28.3 and 25.9); their backward pass at
 // 16384 tokens 185 and 198 (312 and 326), at 1024 20.3 and 18.8 (31.7 and 29.0);
 // rows of eight heads of 128 read back 142 and 159 at 131072 tokens (342 and 357),
